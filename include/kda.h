@@ -262,6 +262,99 @@ kda_status kda_conv_bwd(const kda_conv_problem* p, const void* x, const float* w
                         const float* bias, const void* halo, const void* dy, void* dx, float* dw,
                         float* dbias, void* dhalo, void* ws, size_t ws_bytes, kda_stream_t stream);
 
+/* Serving forms of the conv.  A sequence's window is its last three x rows, bf16 [3, C] -- the layout
+ * of a halo row block.
+ *   kda_conv_tail: after a prompt.  tail[n] = the three rows before document n's end, reaching into
+ *     halo[n] (or zero) where the document is shorter than three tokens.
+ *   kda_conv_step: one token of each of p->N sequences (p->T and p->cu_seqlens are not read).
+ *     x bf16 [N, C] and y [N, C] are the tokens' rows; the window of row n is win[slots[n]]
+ *     (win[n] when slots is NULL) in a pool bf16 [n_slots, 3, C], and win_out (may be win itself)
+ *     receives it shifted by x.  A negative slot marks an unused row: its y is zero and no window
+ *     is touched; a slot >= n_slots is treated the same way and sets the device status
+ *     KDA_ERR_DEVICE_CHECK in ws (nullable, >= 256 bytes).  The used slots must differ from each
+ *     other. */
+kda_status kda_conv_tail(const kda_conv_problem* p, const void* x, const void* halo, void* tail,
+                         kda_stream_t stream);
+kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* w,
+                         const float* bias, const int32_t* slots, int64_t n_slots,
+                         const void* win, void* win_out, void* y, void* ws, kda_stream_t stream);
+
+/* Element type of the selective scan's and the layer norm's rows. */
+typedef enum kda_dtype { KDA_DT_BF16 = 0, KDA_DT_FP16 = 1, KDA_DT_FP32 = 2 } kda_dtype;
+
+/* Selective state-space scan over packed documents: a diagonal state recurrence whose step size and
+ * input / output maps depend on the token.  Per document, channel c (of group g = c / (C / G)) and
+ * state s:
+ *     delta = softplus(dt + dt_bias)   (dt_softplus = 0: delta = dt + dt_bias)
+ *     h_t[c, s] = exp(delta A[c, s]) h_{t-1}[c, s] + delta u[t, c] B[t, g, s]
+ *     y[t, c] = (sum_s Cm[t, g, s] h_t[c, s] + D[c] u[t, c]) * silu(z[t, c])
+ * u, dt, z [T, C] and B, Cm [T, G, S] are of p->dtype; each may be a column range of a wider row-major
+ * tensor (row strides ld_*, in elements; 0 = dense) and needs the alignment of its element only.
+ * Everything else is dense and 16-byte aligned: A fp32 [C, S], D and dt_bias fp32 [C] (nullable:
+ * zero), y, dy and the gradients of u, dt, z, B, Cm in p->dtype, states fp32 [N, C, S].  z is nullable
+ * (no gate); h0 is nullable (zero); ht is nullable.  The states, decays and every sum are fp32.  An
+ * empty document's ht is its h0 and its dh0 is its dht.  Results are bitwise reproducible, and a
+ * document's outputs (dA, dD, ddt_bias excepted, which are sums over documents) do not depend
+ * on the rest of the pack.
+ *
+ * kda_ssm_fwd with a non-NULL saved buffer writes the states at every 64-token chunk's start for
+ * kda_ssm_bwd (saved = NULL there recomputes them).  The backward is that of L = sum(y * dy) +
+ * sum(ht * dht) (dht nullable); dD, ddt_bias and dh0 are nullable, dz is written when z is given.
+ * Workspace sizes (op: KDA_OP_FWD, KDA_OP_BWD_SAVED, KDA_OP_BWD_REPLAY) depend on T, N, C, S, G
+ * only.  The first call on a device sets it up: make it before any stream capture. */
+typedef struct kda_ssm_problem {
+    int64_t T;            /* packed tokens, >= 0 */
+    int32_t N;            /* documents, 1 .. 65535 */
+    int32_t C;            /* channels, >= 1 */
+    int32_t S;            /* states per channel, 1 .. 64 (above: KDA_ERR_UNSUPPORTED) */
+    int32_t G;            /* groups of B and Cm; divides C */
+    int32_t dtype;        /* kda_dtype */
+    int32_t dt_softplus;  /* 1 or 0 */
+    int64_t ld_u, ld_dt, ld_z, ld_b, ld_c; /* row strides; 0 = C, C, C, G S, G S */
+    const int32_t* cu_seqlens;             /* device int32 [N + 1] */
+} kda_ssm_problem;
+kda_status kda_ssm_workspace_size(const kda_ssm_problem* p, int op, size_t* ws_bytes,
+                                  size_t* saved_bytes);
+kda_status kda_ssm_fwd(const kda_ssm_problem* p, const void* u, const void* dt, const float* A,
+                       const void* B, const void* Cm, const float* D, const float* dt_bias,
+                       const void* z, const float* h0, void* y, float* ht, void* saved, void* ws,
+                       size_t ws_bytes, kda_stream_t stream);
+kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* u, const void* dt, const float* A,
+                       const void* B, const void* Cm, const float* D, const float* dt_bias,
+                       const void* z, const float* h0, const void* dy, const float* dht,
+                       const void* saved, void* du, void* ddt, float* dA, void* dB, void* dC,
+                       float* dD, float* ddt_bias, void* dz, float* dh0, void* ws, size_t ws_bytes,
+                       kda_stream_t stream);
+/* One token of each of p->N sequences (p->T and p->cu_seqlens are not read; rows are sequences).
+ * Row n's state is h_in[slots[n]] (h_in[n] when slots is NULL) in a pool fp32 [n_slots, C, S];
+ * h_out (may be h_in itself) receives the new one.  slots and ws as for kda_conv_step. */
+kda_status kda_ssm_step(const kda_ssm_problem* p, const void* u, const void* dt, const float* A,
+                        const void* B, const void* Cm, const float* D, const float* dt_bias,
+                        const void* z, const int32_t* slots, int64_t n_slots, const float* h_in,
+                        float* h_out, void* y, void* ws, kda_stream_t stream);
+
+/* Layer norm over T dense rows of C channels (p->dtype), optionally of x + res:
+ *     v = x + res, rounded to the row type;  y = (v - mean) rstd w + b,  rstd = 1/sqrt(var + eps)
+ * w, b fp32 [C] (nullable: one, zero); res nullable; sum (nullable, requires res) receives v; mean,
+ * rstd fp32 [T] (nullable) are what the backward reads.  The backward takes v as `x` and gives
+ *     dx = rstd (d - mean(d) - xh mean(d xh)) + dsum,  d = dy w,  xh = (v - mean) rstd
+ * (dsum nullable: the gradient that reaches v past the norm; dx is then the gradient of x and of
+ * res), dw = sum_rows dy xh and db = sum_rows dy (fp32 [C], nullable), added in a fixed order. */
+typedef struct kda_layernorm_problem {
+    int64_t T;      /* rows, >= 0 */
+    int32_t C;      /* channels, >= 1 */
+    int32_t dtype;  /* kda_dtype */
+    float eps;
+} kda_layernorm_problem;
+kda_status kda_layernorm_workspace_size(const kda_layernorm_problem* p, size_t* ws_bytes);
+kda_status kda_layernorm_fwd(const kda_layernorm_problem* p, const void* x, const void* res,
+                             const float* w, const float* b, void* sum, void* y, float* mean,
+                             float* rstd, kda_stream_t stream);
+kda_status kda_layernorm_bwd(const kda_layernorm_problem* p, const void* x, const float* w,
+                             const float* mean, const float* rstd, const void* dy,
+                             const void* dsum, void* dx, float* dw, float* db, void* ws,
+                             size_t ws_bytes, kda_stream_t stream);
+
 /* Copies the device status word of `ws` to the host (synchronises `stream`) and clears it.
  * *device_status receives a kda_status value (KDA_OK when no device-side error happened). */
 kda_status kda_read_device_status(void* ws, int* device_status, kda_stream_t stream);

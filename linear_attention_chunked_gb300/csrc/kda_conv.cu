@@ -419,6 +419,100 @@ __global__ void k_conv_reduce(ConvArgs a, int rows) {
     }
 }
 
+// Serving.  tail: the window a prompt leaves -- the last three rows before each document's end,
+// taken from its halo (or zero) where the document is shorter.
+__global__ void k_conv_tail(ConvArgs a, __nv_bfloat16* tail) {
+    const int G = a.C / 8;
+    const int64_t q = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (q >= int64_t(a.N) * 3 * G) return;
+    const int c8 = int(q % G) * 8, i = int(q / G % 3);
+    const int64_t n = q / (3 * G);
+    const int64_t s = a.cu[n], e = a.cu[n + 1], r = e - 3 + i;  // the row, if inside the document
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= s && r >= 0 && r < a.T) v = *reinterpret_cast<const uint4*>(a.x + r * a.C + c8);
+    else if (a.halo && r - s + 3 >= 0 && r - s + 3 < 3)
+        v = *reinterpret_cast<const uint4*>(a.halo + (n * 3 + (r - s + 3)) * a.C + c8);
+    *reinterpret_cast<uint4*>(tail + (n * 3 + i) * a.C + c8) = v;
+}
+
+// step: one token of every sequence.  A thread owns 8 channels (16-byte rows) and walks `rpt`
+// sequences with the channels' taps in registers, so that large batches read the taps once per
+// rpt sequences and small ones still spread over the machine.
+struct ConvStepArgs {
+    int N, C, act, out_fp32, rpt;
+    int64_t nslots;
+    const __nv_bfloat16 *x, *win;
+    const float *w, *bias;
+    const int* slots;
+    __nv_bfloat16* wout;
+    void* y;
+    int* status;
+};
+
+constexpr int CS_THREADS = 128;
+
+__device__ __forceinline__ void bf8_to_f(const uint4& u, float (&f)[8]) {
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = __bfloat1622float2(b[j]);
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+    }
+}
+
+__global__ void __launch_bounds__(CS_THREADS) k_conv_step(ConvStepArgs a) {
+    const int G = a.C / 8, cg = blockIdx.x * CS_THREADS + threadIdx.x;
+    if (cg >= G) return;
+    const int64_t C = a.C, c0 = 8 * cg;
+    float w[4][8], b[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float4 wk = *reinterpret_cast<const float4*>(a.w + (c0 + k) * 4);
+        w[0][k] = wk.x, w[1][k] = wk.y, w[2][k] = wk.z, w[3][k] = wk.w;
+        b[k] = a.bias ? a.bias[c0 + k] : 0.f;
+    }
+    const int n1 = min(int(blockIdx.y + 1) * a.rpt, a.N);
+#pragma unroll 2
+    for (int n = blockIdx.y * a.rpt; n < n1; ++n) {
+        int64_t slot = n;
+        bool use = true;
+        if (a.slots) {
+            slot = a.slots[n];
+            use = slot >= 0 && slot < a.nslots;
+            if (slot >= a.nslots && a.status && cg == 0) *a.status = KDA_ERR_DEVICE_CHECK;
+        }
+        float out[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = 0.f;
+        if (use) {
+            uint4 raw[4];
+#pragma unroll
+            for (int j = 0; j < 3; ++j) raw[j] = *reinterpret_cast<const uint4*>(a.win + (slot * 3 + j) * C + c0);
+            raw[3] = *reinterpret_cast<const uint4*>(a.x + n * C + c0);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(a.wout + (slot * 3 + j) * C + c0) = raw[j + 1];
+            float f[4][8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bf8_to_f(raw[j], f[j]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float z = b[k] + w[0][k] * f[0][k] + w[1][k] * f[1][k] + w[2][k] * f[2][k] + w[3][k] * f[3][k];
+                // the fast division returns 0 past 2^126, the limit for z < -87
+                out[k] = a.act ? __fdividef(z, 1.f + __expf(-z)) : z;
+            }
+        }
+        if (a.out_fp32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.y) + n * C + c0);
+            o[0] = make_float4(out[0], out[1], out[2], out[3]);
+            o[1] = make_float4(out[4], out[5], out[6], out[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + n * C + c0) =
+                make_uint4(pack2(out[0], out[1]), pack2(out[2], out[3]), pack2(out[4], out[5]), pack2(out[6], out[7]));
+        }
+    }
+}
+
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 kda_status check_conv(const kda_conv_problem* p) {
@@ -511,6 +605,61 @@ kda_status kda_conv_bwd(const kda_conv_problem* p, const void* x, const float* w
         ProfScope ps(KK_CONV_REDUCE, st);
         const int n = 5 * p->C;
         k_conv_reduce<<<unsigned((n + 255) / 256), 256, 0, st>>>(a, int(rows));
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_conv_tail(const kda_conv_problem* p, const void* x, const void* halo, void* tail,
+                         kda_stream_t stream) {
+    if (kda_status s = check_conv(p)) return s;
+    if ((p->T > 0 && !x) || !al16(x) || !al16(halo) || !tail || !al16(tail)) return KDA_ERR_INVALID_ARG;
+    const int64_t blocks = (int64_t(p->N) * 3 * (p->C / 8) + 255) / 256;
+    if (blocks > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    {
+        ProfScope ps(KK_CONV_TAIL, st);
+        k_conv_tail<<<unsigned(blocks), 256, 0, st>>>(make_conv(p, x, nullptr, nullptr, halo),
+                                                      static_cast<__nv_bfloat16*>(tail));
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* w, const float* bias,
+                         const int32_t* slots, int64_t n_slots, const void* win, void* win_out, void* y,
+                         void* ws, kda_stream_t stream) {
+    if (!p) return KDA_ERR_INVALID_ARG;
+    kda_conv_problem q = *p;
+    q.T = q.N;  // one token per sequence; T and cu_seqlens are not read
+    static const int32_t none = 0;
+    q.cu_seqlens = &none;
+    if (kda_status s = check_conv(&q)) return s;
+    if (!x || !al16(x) || !w || !al16(w) || !al16(bias) || !win || !al16(win) || !win_out || !al16(win_out) ||
+        !y || !al16(y) || !al16(ws) || (reinterpret_cast<uintptr_t>(slots) & 3u) || n_slots < 1 ||
+        (!slots && n_slots < q.N))
+        return KDA_ERR_INVALID_ARG;
+    ConvStepArgs a{};
+    a.N = q.N;
+    a.C = q.C;
+    a.act = q.activation;
+    a.out_fp32 = q.out_fp32;
+    a.nslots = n_slots;
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.win = static_cast<const __nv_bfloat16*>(win);
+    a.w = w;
+    a.bias = bias;
+    a.slots = slots;
+    a.wout = static_cast<__nv_bfloat16*>(win_out);
+    a.y = y;
+    a.status = static_cast<int*>(ws);
+    const unsigned gx = unsigned((q.C / 8 + CS_THREADS - 1) / CS_THREADS);
+    // one sequence per thread until the grid holds about four blocks per multiprocessor (152 of
+    // them); then four, and more only to keep the grid's second dimension within its limit
+    a.rpt = int64_t(gx) * q.N < 4 * 608 ? 1 : 4;
+    while ((q.N + a.rpt - 1) / a.rpt > 65535) a.rpt *= 2;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    {
+        ProfScope ps(KK_CONV_STEP, st);
+        k_conv_step<<<dim3(gx, unsigned((q.N + a.rpt - 1) / a.rpt)), CS_THREADS, 0, st>>>(a);
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -19,7 +19,11 @@ std::vector<Rec> g_recs;
 const char* const kNames[KK_COUNT] = {"k_plan",      "k_intra_fwd",    "k_chain_fwd",
                                       "k_chain_bwd",    "k_bwd_gemms_tc",    "k_bwd_intra",
                                       "k_param_reduce", "k_walk",         "k_conv_fwd",
-                                      "k_conv_bwd",     "k_conv_reduce"};
+                                      "k_conv_bwd",     "k_conv_reduce",  "k_conv_tail",
+                                      "k_conv_step",    "k_ssm_state",    "k_ssm_carry",
+                                      "k_ssm_out",      "k_ssm_rstate",   "k_ssm_rcarry",
+                                      "k_ssm_bwd",      "k_ssm_reduce",   "k_ssm_step",
+                                      "k_ln_fwd",       "k_ln_bwd",       "k_ln_reduce"};
 }  // namespace
 
 const char* kernel_name(int kind) { return (kind >= 0 && kind < KK_COUNT) ? kNames[kind] : "?"; }

@@ -23,6 +23,8 @@ KDA_STATIC_WS_BYTES = 64 << 20
 KDA_GATE_G, KDA_GATE_RAW = 0, 1
 KDA_OP_FWD, KDA_OP_BWD_SAVED, KDA_OP_BWD_REPLAY, KDA_OP_FRAGMENT, KDA_OP_WALK = 0, 1, 2, 3, 4
 KDA_FRAG_FWD, KDA_FRAG_BWD = 0, 1
+KDA_DT_BF16, KDA_DT_FP16, KDA_DT_FP32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: KDA_DT_BF16, torch.float16: KDA_DT_FP16, torch.float32: KDA_DT_FP32}
 KDA_WALK_FP32, KDA_WALK_TF32, KDA_WALK_TF32_HILO, KDA_WALK_BF16X3, KDA_WALK_BF16X3_HW = 0, 1, 2, 3, 4
 WALK_PRECISIONS = {"fp32": KDA_WALK_FP32, "tf32": KDA_WALK_TF32, "tf32_hilo": KDA_WALK_TF32_HILO,
                    "bf16x3": KDA_WALK_BF16X3, "bf16x3_hw": KDA_WALK_BF16X3_HW}
@@ -30,7 +32,9 @@ WALK_DEFAULT = KDA_WALK_BF16X3_HW  # the format the pages ship as the default wa
 
 EXPORTS = ("kda_workspace_size", "kda_fwd", "kda_fwd_static_ws", "kda_bwd", "kda_fragment_summary",
            "kda_transfer_walk", "kda_conv_workspace_size", "kda_conv_fwd", "kda_conv_bwd",
-           "kda_read_device_status", "kda_profile_enable",
+           "kda_conv_tail", "kda_conv_step", "kda_ssm_workspace_size", "kda_ssm_fwd", "kda_ssm_bwd",
+           "kda_ssm_step", "kda_layernorm_workspace_size", "kda_layernorm_fwd",
+           "kda_layernorm_bwd", "kda_read_device_status", "kda_profile_enable",
            "kda_profile_collect", "kda_kernel_count", "kda_kernel_name", "kda_launch_counter",
            "kda_status_string")
 
@@ -53,6 +57,19 @@ class kda_problem(ctypes.Structure):
                 ("out_fp32", ctypes.c_int32), ("group_chunks", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("l2_eps", ctypes.c_float),
                 ("cu_seqlens", ctypes.c_void_p)]
+
+
+class kda_ssm_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("S", ctypes.c_int32), ("G", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("dt_softplus", ctypes.c_int32), ("ld_u", ctypes.c_int64),
+                ("ld_dt", ctypes.c_int64), ("ld_z", ctypes.c_int64), ("ld_b", ctypes.c_int64),
+                ("ld_c", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p)]
+
+
+class kda_layernorm_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -85,6 +102,17 @@ def lib():
             L.kda_conv_workspace_size.argtypes = [CP, ctypes.POINTER(S)]
             L.kda_conv_fwd.argtypes = [CP, V, V, V, V, V, V]
             L.kda_conv_bwd.argtypes = [CP] + [V] * 9 + [V, S, V]
+            L.kda_conv_tail.argtypes = [CP, V, V, V, V]
+            L.kda_conv_step.argtypes = [CP, V, V, V, V, ctypes.c_int64, V, V, V, V, V]
+            SP = ctypes.POINTER(kda_ssm_problem)
+            L.kda_ssm_workspace_size.argtypes = [SP, I, ctypes.POINTER(S), ctypes.POINTER(S)]
+            L.kda_ssm_fwd.argtypes = [SP] + [V] * 12 + [V, S, V]
+            L.kda_ssm_bwd.argtypes = [SP] + [V] * 21 + [V, S, V]
+            L.kda_ssm_step.argtypes = [SP] + [V] * 9 + [ctypes.c_int64] + [V] * 5
+            NP = ctypes.POINTER(kda_layernorm_problem)
+            L.kda_layernorm_workspace_size.argtypes = [NP, ctypes.POINTER(S)]
+            L.kda_layernorm_fwd.argtypes = [NP] + [V] * 9
+            L.kda_layernorm_bwd.argtypes = [NP] + [V] * 10 + [S, V]
             L.kda_read_device_status.argtypes = [V, ctypes.POINTER(I), V]
             L.kda_selftest_wait_timeout.argtypes = [V, ctypes.c_uint32, V]
             L.kda_profile_enable.argtypes = [I]
@@ -98,7 +126,10 @@ def lib():
             L.kda_status_string.restype = ctypes.c_char_p
             for name in ("kda_workspace_size", "kda_fwd", "kda_fwd_static_ws", "kda_bwd", "kda_fragment_summary",
                          "kda_transfer_walk", "kda_conv_workspace_size", "kda_conv_fwd",
-                         "kda_conv_bwd", "kda_read_device_status", "kda_selftest_wait_timeout",
+                         "kda_conv_bwd", "kda_conv_tail", "kda_conv_step", "kda_ssm_workspace_size",
+                         "kda_ssm_fwd", "kda_ssm_bwd", "kda_ssm_step",
+                         "kda_layernorm_workspace_size", "kda_layernorm_fwd",
+                         "kda_layernorm_bwd", "kda_read_device_status", "kda_selftest_wait_timeout",
                          "kda_profile_enable",
                          "kda_profile_collect", "kda_kernel_count"):
                 getattr(L, name).restype = ctypes.c_int
@@ -359,6 +390,288 @@ def kda_conv_bwd(x, w, cu_seqlens, dy, *, bias=None, halo=None, activation=True,
                                 _ptr(dy), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out.get("dbias")),
                                 _ptr(out.get("dhalo")), _ptr(ws), ws.numel(), _stream(dev))
     _check("kda_conv_bwd", st)
+    return out
+
+
+def _check_tensor(fn, name, t, shape, dtype, device, *, strided=False):
+    """A tensor handed to the library has the shape, type and device the call works on and dense
+    rows; `strided` ones (views of a projection) may have any row stride."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        inner = t[0] if strided and t.shape[0] else None
+        if inner is None or not inner.is_contiguous() or (t.shape[0] > 1 and t.stride(0) < inner.numel()):
+            raise ValueError(f"{fn}: {name} has strides {t.stride()}, expected dense "
+                             f"{'rows' if strided else 'storage'}")
+
+
+def _row_stride(t):
+    """The row stride of a tensor whose rows are dense (0, the library's dense, where it has at
+    most one row)."""
+    return 0 if t is None or t.shape[0] < 2 else t.stride(0)
+
+
+def _slots(fn, slots, rows, pool, dev):
+    if slots is None:
+        if pool < rows:
+            raise ValueError(f"{fn}: {rows} rows need as many states, the pool has {pool}")
+    else:
+        _check_tensor(fn, "slots", slots, (rows,), torch.int32, dev)
+
+
+def kda_conv_tail(x, cu_seqlens, *, halo=None, tail=None):
+    """The conv window that a prompt leaves: tail [N, 3, C] bf16, the three rows before each
+    document's end (from halo [N, 3, C], or zero, where the document is shorter)."""
+    fn = "kda_conv_tail"
+    T, N, C = _conv_shape(x, cu_seqlens)
+    dev = x.device
+    if tail is None:
+        tail = torch.empty((N, 3, C), dtype=torch.bfloat16, device=dev)
+    _check_tensor(fn, "x", x, x.shape, torch.bfloat16, dev)
+    _check_tensor(fn, "halo", halo, (N, 3, C), torch.bfloat16, dev)
+    _check_tensor(fn, "tail", tail, (N, 3, C), torch.bfloat16, dev)
+    pr = make_conv_problem(T, N, C, cu_seqlens)
+    with torch.cuda.device(dev):
+        st = lib().kda_conv_tail(ctypes.byref(pr), _ptr(x), _ptr(halo), _ptr(tail), _stream(dev))
+    _check(fn, st)
+    return tail
+
+
+def kda_conv_step(x, w, win, *, bias=None, activation=True, slots=None, out_dtype=torch.bfloat16,
+                  win_out=None, y=None, ws=None):
+    """The conv of one token per sequence: x [N, C] bf16, taps w [C, 4] fp32, windows win
+    [n_slots, 3, C] bf16 (row n's is win[slots[n]], win[n] without slots).  Returns (y [N, C] in
+    out_dtype, win_out); win_out defaults to win, updated in place.  A negative slot marks an
+    unused row; ws (optional, >= 256 bytes) receives the device status."""
+    fn = "kda_conv_step"
+    N, C = x.shape
+    dev = x.device
+    if win_out is None:
+        win_out = win
+    if y is None:
+        y = torch.empty((N, C), dtype=out_dtype, device=dev)
+    _check_tensor(fn, "x", x, (N, C), torch.bfloat16, dev)
+    _check_tensor(fn, "w", w, (C, 4), torch.float32, dev)
+    _check_tensor(fn, "bias", bias, (C,), torch.float32, dev)
+    _check_tensor(fn, "win", win, (win.shape[0], 3, C), torch.bfloat16, dev)
+    _check_tensor(fn, "win_out", win_out, win.shape, torch.bfloat16, dev)
+    _check_tensor(fn, "y", y, (N, C), out_dtype, dev)
+    _slots(fn, slots, N, win.shape[0], dev)
+    pr = make_conv_problem(N, N, C, activation=activation, out_dtype=out_dtype)
+    with torch.cuda.device(dev):
+        st = lib().kda_conv_step(ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(bias), _ptr(slots),
+                                 win.shape[0], _ptr(win), _ptr(win_out), _ptr(y), _ptr(ws),
+                                 _stream(dev))
+    _check(fn, st)
+    return y, win_out
+
+
+def _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens):
+    """Checks the scan's inputs and describes the call: B, C [T, G, S] or [T, S] (one group)."""
+    T, ch = u.shape
+    S, dev, dtype = A.shape[-1], u.device, u.dtype
+    G = B.shape[1] if B.dim() == 3 else 1
+    if dtype not in _DTYPES:
+        raise ValueError(f"{fn}: u is {dtype}, expected one of bfloat16, float16, float32")
+    _check_tensor(fn, "u", u, (T, ch), dtype, dev, strided=True)
+    _check_tensor(fn, "dt", dt, (T, ch), dtype, dev, strided=True)
+    _check_tensor(fn, "z", z, (T, ch), dtype, dev, strided=True)
+    bc = (T, G, S) if B.dim() == 3 else (T, S)
+    _check_tensor(fn, "B", B, bc, dtype, dev, strided=True)
+    _check_tensor(fn, "C", C, bc, dtype, dev, strided=True)
+    _check_tensor(fn, "A", A, (ch, S), torch.float32, dev)
+    _check_tensor(fn, "D", D, (ch,), torch.float32, dev)
+    _check_tensor(fn, "dt_bias", dt_bias, (ch,), torch.float32, dev)
+    if cu_seqlens is not None:
+        _check_tensor(fn, "cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    return kda_ssm_problem(T, N, ch, S, G, _DTYPES[dtype], int(bool(softplus)), _row_stride(u),
+                           _row_stride(dt), _row_stride(z), _row_stride(B), _row_stride(C),
+                           None if cu_seqlens is None else cu_seqlens.data_ptr())
+
+
+def _ssm_sizes(pr, op):
+    ws, sv = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("kda_ssm_workspace_size",
+           lib().kda_ssm_workspace_size(ctypes.byref(pr), int(op), ctypes.byref(ws), ctypes.byref(sv)))
+    return ws.value, sv.value
+
+
+def kda_ssm_workspace_size(T, N, C, S, G, op, *, dtype=torch.bfloat16):
+    """Returns (workspace bytes, saved-set bytes) of the scan's op."""
+    pr = kda_ssm_problem(T, N, C, S, G, _DTYPES[dtype], 1, 0, 0, 0, 0, 0, 16)  # cu_seqlens is not read
+    return _ssm_sizes(pr, op)
+
+
+def kda_ssm_fwd(u, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, z=None, h0=None,
+                softplus=True, save=True, y=None, ht=None, saved=None, ws=None):
+    """Selective state-space scan of packed documents: u, dt, z [T, ch], B, C [T, G, S] (or [T, S])
+    of one type (bf16, fp16, fp32; views with a row stride are taken as they are), A [ch, S], D,
+    dt_bias [ch], h0 [N, ch, S] fp32.  Returns (y [T, ch], ht [N, ch, S], saved) -- saved is None
+    when save=False."""
+    fn = "kda_ssm_fwd"
+    N, dev = cu_seqlens.numel() - 1, u.device
+    pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens)
+    ws_b, sv_b = _ssm_sizes(pr, KDA_OP_FWD)
+    state = (N, pr.C, pr.S)
+    if ws is None:
+        ws = _empty_bytes(ws_b, dev)
+    if not save:
+        saved = None
+    elif saved is None:
+        saved = _empty_bytes(sv_b, dev)
+    elif saved.numel() * saved.element_size() < sv_b:
+        raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
+    if y is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    if ht is None:
+        ht = torch.empty(state, dtype=torch.float32, device=dev)
+    _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
+    _check_tensor(fn, "ht", ht, state, torch.float32, dev)
+    _check_tensor(fn, "h0", h0, state, torch.float32, dev)
+    with torch.cuda.device(dev):
+        st = lib().kda_ssm_fwd(ctypes.byref(pr), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                               _ptr(dt_bias), _ptr(z), _ptr(h0), _ptr(y), _ptr(ht), _ptr(saved),
+                               _ptr(ws), ws.numel(), _stream(dev))
+    _check(fn, st)
+    return y, ht, saved
+
+
+def kda_ssm_bwd(u, dt, A, B, C, cu_seqlens, dy, *, saved=None, D=None, dt_bias=None, z=None,
+                h0=None, dht=None, softplus=True, want_dh0=True, ws=None):
+    """Backward of the scan for L = sum(y * dy) + sum(ht * dht) (saved=None: the states are
+    recomputed).  Returns a dict: du, ddt, dB, dC and (with z) dz in the inputs' type, dA and, for
+    what was given, dD, ddt_bias fp32, and dh0 fp32 when wanted."""
+    fn = "kda_ssm_bwd"
+    N, dev, dtype = cu_seqlens.numel() - 1, u.device, u.dtype
+    pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens)
+    state = (N, pr.C, pr.S)
+    _check_tensor(fn, "dy", dy, u.shape, dtype, dev)
+    _check_tensor(fn, "h0", h0, state, torch.float32, dev)
+    _check_tensor(fn, "dht", dht, state, torch.float32, dev)
+    ws_b, sv_b = _ssm_sizes(pr, KDA_OP_BWD_REPLAY if saved is None else KDA_OP_BWD_SAVED)
+    if saved is not None and saved.numel() * saved.element_size() < sv_b:
+        raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
+    if ws is None:
+        ws = _empty_bytes(ws_b, dev)
+    rows, par = dict(dtype=dtype, device=dev), dict(dtype=torch.float32, device=dev)
+    out = dict(du=torch.empty(u.shape, **rows), ddt=torch.empty(u.shape, **rows),
+               dA=torch.empty(A.shape, **par), dB=torch.empty(B.shape, **rows),
+               dC=torch.empty(B.shape, **rows))
+    if D is not None:
+        out["dD"] = torch.empty(D.shape, **par)
+    if dt_bias is not None:
+        out["ddt_bias"] = torch.empty(dt_bias.shape, **par)
+    if z is not None:
+        out["dz"] = torch.empty(u.shape, **rows)
+    if want_dh0:
+        out["dh0"] = torch.empty(state, **par)
+    with torch.cuda.device(dev):
+        st = lib().kda_ssm_bwd(ctypes.byref(pr), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                               _ptr(dt_bias), _ptr(z), _ptr(h0), _ptr(dy), _ptr(dht), _ptr(saved),
+                               _ptr(out["du"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
+                               _ptr(out["dC"]), _ptr(out.get("dD")), _ptr(out.get("ddt_bias")),
+                               _ptr(out.get("dz")), _ptr(out.get("dh0")), _ptr(ws), ws.numel(),
+                               _stream(dev))
+    _check(fn, st)
+    return out
+
+
+def kda_ssm_step(u, dt, A, B, C, h, *, D=None, dt_bias=None, z=None, softplus=True, slots=None,
+                 h_out=None, y=None, ws=None):
+    """The scan of one token per sequence: rows are sequences, h [n_slots, ch, S] fp32 the states
+    (row n's is h[slots[n]], h[n] without slots).  Returns (y, h_out); h_out defaults to h, updated
+    in place.  A negative slot marks an unused row; ws (optional, >= 256 bytes) receives the
+    device status."""
+    fn = "kda_ssm_step"
+    N, dev = u.shape[0], u.device
+    pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, None)
+    if h_out is None:
+        h_out = h
+    if y is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    _check_tensor(fn, "h", h, (h.shape[0], pr.C, pr.S), torch.float32, dev)
+    _check_tensor(fn, "h_out", h_out, h.shape, torch.float32, dev)
+    _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
+    _slots(fn, slots, N, h.shape[0], dev)
+    with torch.cuda.device(dev):
+        st = lib().kda_ssm_step(ctypes.byref(pr), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                                _ptr(dt_bias), _ptr(z), _ptr(slots), h.shape[0], _ptr(h), _ptr(h_out),
+                                _ptr(y), _ptr(ws), _stream(dev))
+    _check(fn, st)
+    return y, h_out
+
+
+def _layernorm_problem(fn, x, eps):
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"{fn}: x is {x.dtype}, expected one of bfloat16, float16, float32")
+    _check_tensor(fn, "x", x, x.shape, x.dtype, x.device)
+    C = x.shape[-1]
+    return kda_layernorm_problem(x.numel() // max(C, 1), C, _DTYPES[x.dtype], float(eps))
+
+
+def kda_layernorm_workspace_size(T, C, *, dtype=torch.bfloat16):
+    pr = kda_layernorm_problem(int(T), int(C), _DTYPES[dtype], 0.0)
+    ws = ctypes.c_size_t(0)
+    _check("kda_layernorm_workspace_size",
+           lib().kda_layernorm_workspace_size(ctypes.byref(pr), ctypes.byref(ws)))
+    return ws.value
+
+
+def kda_layernorm_fwd(x, w=None, b=None, *, res=None, eps=1e-5, y=None, sum=None):
+    """Layer norm of x [..., C] (bf16, fp16, fp32) over the last axis, of x + res when res is given;
+    w, b fp32 [C].  Returns (y, sum, mean, rstd): sum is x + res in x's type (x itself without
+    res), mean and rstd fp32 one per row -- what kda_layernorm_bwd takes."""
+    fn = "kda_layernorm_fwd"
+    pr = _layernorm_problem(fn, x, eps)
+    dev = x.device
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if res is None:
+        if sum is not None:
+            raise ValueError(f"{fn}: a sum needs a residual")
+    elif sum is None:
+        sum = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    _check_tensor(fn, "res", res, x.shape, x.dtype, dev)
+    _check_tensor(fn, "sum", sum, x.shape, x.dtype, dev)
+    _check_tensor(fn, "y", y, x.shape, x.dtype, dev)
+    _check_tensor(fn, "w", w, (pr.C,), torch.float32, dev)
+    _check_tensor(fn, "b", b, (pr.C,), torch.float32, dev)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = lib().kda_layernorm_fwd(ctypes.byref(pr), _ptr(x), _ptr(res), _ptr(w), _ptr(b), _ptr(sum),
+                                     _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev))
+    _check(fn, st)
+    return y, x if res is None else sum, mean, rstd
+
+
+def kda_layernorm_bwd(x, w, mean, rstd, dy, *, dsum=None, ws=None):
+    """Backward of the layer norm: x is what was normalised (the forward's sum), dsum the gradient
+    that reaches it past the norm.  Returns dict dx, dw, db (w may be None: ones)."""
+    fn = "kda_layernorm_bwd"
+    pr = _layernorm_problem(fn, x, 0.0)
+    dev = x.device
+    _check_tensor(fn, "dy", dy, x.shape, x.dtype, dev)
+    _check_tensor(fn, "dsum", dsum, x.shape, x.dtype, dev)
+    _check_tensor(fn, "w", w, (pr.C,), torch.float32, dev)
+    _check_tensor(fn, "mean", mean, x.shape[:-1], torch.float32, dev)
+    _check_tensor(fn, "rstd", rstd, x.shape[:-1], torch.float32, dev)
+    if ws is None:
+        ws = _empty_bytes(kda_layernorm_workspace_size(pr.T, pr.C, dtype=x.dtype), dev)
+    out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev),
+               dw=torch.empty((pr.C,), dtype=torch.float32, device=dev),
+               db=torch.empty((pr.C,), dtype=torch.float32, device=dev))
+    with torch.cuda.device(dev):
+        st = lib().kda_layernorm_bwd(ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dy),
+                                     _ptr(dsum), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["db"]),
+                                     _ptr(ws), ws.numel(), _stream(dev))
+    _check(fn, st)
     return out
 
 
