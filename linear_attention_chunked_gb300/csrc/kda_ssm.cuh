@@ -17,6 +17,8 @@ namespace kda {
 
 constexpr int SSM_THREADS = 128;
 constexpr int SSM_MAXS = 64;  // states per channel
+constexpr int SSM_UT = 16;           // tokens between the states kept for the backward
+constexpr int SSM_SUB = CH / SSM_UT;
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct SsmArgs {
@@ -33,7 +35,9 @@ struct SsmArgs {
     int *status, *nchunks, *doc_off;
     int4* chunk_tab;  // {doc, first token, length, chunk index within the doc}
     float* sumdt;     // [maxC][C] sum of delta over the chunk
-    float* hs;        // [maxC][C][S] state at each chunk's start (a document's first chunk: h0)
+    float* hs;        // [maxC][sub][C][S] states at the chunks' starts (a document's first chunk: h0)
+                      // and, with sub = SSM_SUB, at every SSM_UT-th token (the backward's set)
+    int sub;
     float* gs;        // [maxC][C][S] gradient of the state at each chunk's end (last chunk: dht)
     float* pBC;       // [channel blocks][T][2 S] partial sums of dB and dC
     float* pA;        // [maxC][C][S + 2] partial sums of dA, dD, dbias
@@ -110,16 +114,35 @@ __device__ __forceinline__ f2 keep2(f2 v, int s, int S) {
     return pk2(s < S ? x : 0.f, s + 1 < S ? y : 0.f);
 }
 
-// z silu'(..) helpers: the fast reciprocal is 0 once 1 + e^-z exceeds 2^126, the limit there
-__device__ __forceinline__ float ssm_sigmoid(float z) { return __fdividef(1.f, 1.f + ex2(-LOG2E * z)); }
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float ssm_sigmoid(float z) { return rcp(1.f + ex2(-LOG2E * z)); }
+// z sigmoid(z).  Past z = -87 the divisor leaves the range of its reciprocal: the limit there is 0
 __device__ __forceinline__ float ssm_silu(float z) {
-    // below -87 the quotient's divisor overflows the fast division's range: the limit there is 0
-    return z < -87.f ? 0.f * z : __fdividef(z, 1.f + ex2(-LOG2E * z));
+    return z * (z < -87.f ? 0.f : rcp(1.f + ex2(-LOG2E * z)));
 }
 
+// softplus(x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], with log1p(u) = 2 atanh(u / (2 + u)) as its
+// odd series (argument at most 1/3: the terms past the 13th power are below 1e-7 of the sum)
 __device__ __forceinline__ float ssm_delta(float raw, int softplus) {
-    return softplus ? softplus_f(raw) : raw;
+    if (!softplus) return raw;
+    const float u = ex2(-LOG2E * fabsf(raw));
+    const float z = u * rcp(2.f + u), z2 = z * z;
+    float p = fmaf(z2, 2.f / 13.f, 2.f / 11.f);
+    p = fmaf(z2, p, 2.f / 9.f);
+    p = fmaf(z2, p, 2.f / 7.f);
+    p = fmaf(z2, p, 2.f / 5.f);
+    p = fmaf(z2, p, 2.f / 3.f);
+    p = fmaf(z2, p, 2.f);
+    return fmaf(z, p, fmaxf(raw, 0.f));
 }
+
+// An element as it lies in memory: rows loaded ahead are kept so, and widened where they are used (a
+// widening right behind the load would wait for it)
+template <class E> __device__ __forceinline__ float ssm_f(E v) { return ssm_ld<E>(&v, 0); }
 
 // SP = P SPT states per channel slot; the block's B (and C) rows of a chunk as fp32 [CH][SP]
 template <class E, int SP, int NTH = SSM_THREADS>
@@ -131,10 +154,26 @@ __device__ __forceinline__ void ssm_load_rows(float* s, const void* g, int64_t l
     }
 }
 
-// Slots of a lane for S states per channel: SPT states per lane, P lanes per channel.
-struct SsmShape { int spt, p; };
-
-// ---- launches ----
-enum { SSM_BF16 = KDA_DT_BF16, SSM_FP16 = KDA_DT_FP16, SSM_FP32 = KDA_DT_FP32 };
+// Rows of one channel, read GR tokens ahead of their use.  The rows past the chunk's end repeat its
+// last one.
+template <class E, int GR>
+struct Ahead {
+    const E* p;  // the next group's first row
+    int64_t ld;
+    E raw[GR];
+    __device__ __forceinline__ Ahead(const void* base, int64_t row, int64_t ld_, int c)
+        : p(static_cast<const E*>(base) + row * ld_ + c), ld(ld_) {}
+    // left: rows from the group's first to the chunk's end
+    __device__ __forceinline__ void load(int left) {
+        if (left >= GR) {
+#pragma unroll
+            for (int i = 0; i < GR; ++i) raw[i] = p[i * ld];
+        } else {
+#pragma unroll
+            for (int i = 0; i < GR; ++i) raw[i] = p[min(i, left - 1) * ld];
+        }
+        p += GR * ld;
+    }
+};
 
 }  // namespace kda

@@ -61,7 +61,7 @@ kda_status check_problem(const kda_ssm_problem* p) {
 
 struct Regions {
     size_t status, nchunks, doc_off, doc_order, chunk_tab, sumdt, hs, gs, pBC, pA;
-    size_t fwd, bwd_saved, bwd_replay, saved;
+    size_t head, fwd, bwd_saved, bwd_replay, saved;
 };
 
 Regions regions(const kda_ssm_problem* p) {
@@ -76,14 +76,14 @@ Regions regions(const kda_ssm_problem* p) {
     r.doc_order = take(sizeof(int) * size_t(p->N));
     r.chunk_tab = take(sizeof(int4) * nc);
     r.sumdt = take(nc * p->C * 4);
-    const size_t head = o;
-    r.saved = align256(nc * CS * 4);
-    r.fwd = head + r.saved;  // a forward without a saved set keeps the states behind the header
+    r.head = o;
+    r.saved = align256(nc * SSM_SUB * CS * 4);
+    r.fwd = r.head + align256(nc * CS * 4);  // without a saved set the chunks' states lie behind the header
     r.gs = take(nc * CS * 4);
     r.pBC = take(size_t(p->G) * pl.splits * size_t(p->T) * 2 * p->S * 4);
     r.pA = take(nc * p->C * size_t(p->S + 2) * 4);
     r.bwd_saved = o;
-    r.hs = take(nc * CS * 4);  // replay's states
+    r.hs = take(r.saved);  // replay's states
     r.bwd_replay = o;
     return r;
 }
@@ -166,16 +166,17 @@ kda_status kda_ssm_fwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     if (kda_status s = check_inputs(p, u, dt, A, B, Cm, D_, dt_bias, z, h0)) return s;
     if ((p->T > 0 && !req(y)) || !opt(y) || !opt(ht) || !opt(saved) || !req(ws)) return KDA_ERR_INVALID_ARG;
     const Regions r = regions(p);
-    if (ws_bytes < (saved ? r.fwd - r.saved : r.fwd)) return KDA_ERR_WORKSPACE;
+    if (ws_bytes < (saved ? r.head : r.fwd)) return KDA_ERR_WORKSPACE;
     if (kda_status s = setup_ssm()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     SsmArgs a = make_args(p, r, ws);
     a.u = u, a.dt = dt, a.A = A, a.B = B, a.Cm = Cm, a.D = D_, a.bias = dt_bias, a.z = z, a.h0 = h0;
     a.y = y;
     a.ht = ht;
-    a.hs = static_cast<float*>(saved ? saved : static_cast<char*>(ws) + (r.fwd - r.saved));
+    a.hs = static_cast<float*>(saved ? saved : static_cast<char*>(ws) + r.head);
+    a.sub = saved ? SSM_SUB : 1;
     launch_plan(a, r, ws, st);
-    launch_ssm_scan(a, p->dtype, true, st);
+    launch_ssm_scan(a, p->dtype, st);
     return launched();
 }
 
@@ -196,12 +197,13 @@ kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     SsmArgs a = make_args(p, r, ws);
     a.u = u, a.dt = dt, a.A = A, a.B = B, a.Cm = Cm, a.D = D_, a.bias = dt_bias, a.z = z, a.h0 = h0;
+    a.sub = SSM_SUB;
     launch_plan(a, r, ws, st);
     if (saved) {
         a.hs = static_cast<float*>(const_cast<void*>(saved));
-    } else {  // recompute the chunk start states (no y, no final state)
+    } else {  // recompute the states (no y, no final state)
         a.hs = reinterpret_cast<float*>(static_cast<char*>(ws) + r.hs);
-        launch_ssm_scan(a, p->dtype, false, st);
+        launch_ssm_scan(a, p->dtype, st);
     }
     a.dy = dy, a.dht = dht;
     a.du = du, a.ddt = ddt, a.dA = dA, a.dB = dB, a.dC = dC, a.dD = dD, a.dbias = ddt_bias, a.dz = dz, a.dh0 = dh0;

@@ -11,12 +11,15 @@
 //   k_ssm_bwd      per (chunk, channel tile): the gradients
 //   k_ssm_reduce_* the sums over channel tiles (dB, dC) and over chunks (dA, dD, dbias), in order
 //
-// k_ssm_bwd needs h_{t-1} in reverse.  A chunk is swept forward once from its start state, the
-// states every SB = 8 tokens kept in shared memory; each run of 8 tokens is then recomputed from
-// its start with states and decays in registers and walked backwards.  Four lanes hold a channel's 16
-// states (four each).  A lane's eight dB / dC terms per token are summed over two channels in
-// registers before they cross lanes, and cross them by halving (each step a lane gives away half
-// of its values), 7 shuffles for 8 values over 8 lanes.
+// k_ssm_bwd needs h_{t-1} in reverse.  The forward leaves the state at every 16th token; a unit of 16
+// tokens is swept forward once from there, the states every 4 tokens kept in shared memory, and
+// each run of 4 tokens is recomputed from its start with states and decays in registers and walked
+// backwards.  Four lanes hold a channel's 16 states (four each), a warp 16 channels in two passes.
+// The channels' scalars (delta, delta u, dY) are computed once per token by lanes laid out as
+// channels and handed over through shared memory, one unit ahead of their use; the sums over a
+// channel's states go back the same way.  A lane's eight dB / dC terms per token are summed over
+// the two passes in registers before they cross lanes, and cross them by halving (each step a lane
+// gives away half of its values): 7 shuffles for 8 values over 8 lanes.
 #include "kda_ssm.cuh"
 #include "kda_ssm_launch.cuh"
 
@@ -24,9 +27,10 @@ namespace kda {
 
 namespace {
 
-constexpr int SB = 8;        // tokens per run
-constexpr int NSB = CH / SB; // runs per chunk
-constexpr int NP = 2;        // channel passes per warp
+constexpr int RT = 4;           // tokens per run
+constexpr int UT = SSM_UT;      // tokens per unit
+constexpr int NR = UT / RT;     // runs per unit
+constexpr int NP = 2;           // channel passes per warp
 constexpr int NW = SSM_THREADS / 32;
 constexpr int SPT = 4;       // states per lane
 
@@ -67,35 +71,46 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_rstate(SsmArgs a, int tiles
         acc[j] = 0;
     }
     const float bias = a.bias ? a.bias[c] : 0.f;
-    const int64_t id = int64_t(t.y) * a.lddt + c, iz = int64_t(t.y) * a.ldz + c;
-    const int64_t iy = int64_t(t.y) * a.C + c;
-    float rd[GR], rz[GR], ry[GR], sum = 0.f;
-    auto load = [&](int q) {
+    const bool gated = a.z;
+    float sum = 0.f;
+    Ahead<E, GR> d(a.dt, t.y, a.lddt, c), z(a.z, t.y, a.ldz, c), g_(a.dy, t.y, a.C, c);
+    d.load(len);
+    g_.load(len);
+    if (gated) z.load(len);
+    __syncthreads();
+    E cd[GR], cy[GR], cz[GR];
+    auto token = [&](int q, int i) {
+        sum += ssm_delta(ssm_f<E>(cd[i]) + bias, a.softplus);
+        float dY = ssm_f<E>(cy[i]);
+        if (gated) dY *= ssm_silu(ssm_f<E>(cz[i]));
+        const f2 s2 = pk2(sum, sum), d2 = pk2(dY, dY);
+        const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(sC + (q + i) * SP + s0);
 #pragma unroll
-        for (int i = 0; i < GR; ++i) {
-            const int r = min(q + i, len - 1);
-            rd[i] = ssm_ld<E>(a.dt, id + r * a.lddt);
-            ry[i] = ssm_ld<E>(a.dy, iy + int64_t(r) * a.C);
-            rz[i] = a.z ? ssm_ld<E>(a.z, iz + r * a.ldz) : 0.f;
+        for (int j = 0; j < H2; j += 2) {
+            const ulonglong2 c2 = Cp[j / 2];
+            acc[j] = fma2(ex2_2(mul2(A2[j], s2)), mul2(c2.x, d2), acc[j]);
+            acc[j + 1] = fma2(ex2_2(mul2(A2[j + 1], s2)), mul2(c2.y, d2), acc[j + 1]);
         }
     };
-    load(0);
-    __syncthreads();
+#pragma unroll 1
     for (int q = 0; q < len; q += GR) {
-        float cd[GR], cy[GR], cz[GR];
-#pragma unroll
-        for (int i = 0; i < GR; ++i) cd[i] = rd[i], cy[i] = ry[i], cz[i] = rz[i];
-        if (q + GR < len) load(q + GR);
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
-            if (q + i >= len) break;
-            sum += ssm_delta(cd[i] + bias, a.softplus);
-            const float dY = a.z ? cy[i] * ssm_silu(cz[i]) : cy[i];
-            const f2 s2 = pk2(sum, sum), d2 = pk2(dY, dY);
-            const f2* Cp = reinterpret_cast<const f2*>(sC + (q + i) * SP + s0);
+            cd[i] = d.raw[i], cy[i] = g_.raw[i];
+            if (gated) cz[i] = z.raw[i];
+        }
+        if (q + GR < len) {
+            d.load(len - q - GR);
+            g_.load(len - q - GR);
+            if (gated) z.load(len - q - GR);
+        }
+        if (q + GR <= len) {
 #pragma unroll
-            for (int j = 0; j < H2; ++j)
-                acc[j] = fma2(ex2_2(mul2(A2[j], s2)), mul2(Cp[j], d2), acc[j]);
+            for (int i = 0; i < GR; ++i) token(q, i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < GR - 1; ++i)
+                if (q + i < len) token(q, i);
         }
     }
     if (!on) return;
@@ -189,254 +204,283 @@ struct BwdShape {
     static constexpr int CW = NP * CL;      // channels of a warp
     static constexpr int CB = NW * CW;      // channels of a tile
     static constexpr int SP = SPT * P;      // state slots
+    static constexpr int NI = RT * CW > 32 ? RT * CW / 32 : 1;  // (token, channel) items of a run per lane
     // shared memory, in floats
     static constexpr int oB = 0, oC = oB + CH * SP, oPre = oC + CH * SP;
-    static constexpr int oCk = oPre + NW * SB * CW * 4;
-    static constexpr int oG = oCk + NSB * NP * SSM_THREADS * 4;
-    static constexpr int oRed = oG + 2 * NP * SSM_THREADS * 4;
-    static constexpr int oBC = oRed + NW * SB * 2 * SP;
-    static constexpr int floats = oBC + CH * 2 * SP;
+    static constexpr int oCk = oPre + 2 * NW * UT * CW * 4;
+    static constexpr int oSum = oCk + (NR - 1) * NP * SSM_THREADS * 4;
+    static constexpr int oRed = oSum + NW * RT * CW * P * 4;
+    static constexpr int floats = oRed + 2 * NW * RT * 2 * SP;
 };
 
 template <class E, int P>
-__global__ void __launch_bounds__(SSM_THREADS) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
+__global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
     using L = BwdShape<P>;
-    constexpr int CL = L::CL, CW = L::CW, SP = L::SP;
+    constexpr int CL = L::CL, CW = L::CW, SP = L::SP, NI = L::NI, NB = CW > 32 ? 2 : 1;
     extern __shared__ __align__(16) float sm[];
     const int per_chunk = a.G * pl.splits;
     const int k = blockIdx.x / per_chunk;
     if (k >= *a.nchunks) return;
     const int4 tab = a.chunk_tab[k];
-    const int t0 = tab.y, len = tab.z, nsub = (len + SB - 1) / SB;
+    const int t0 = tab.y, len = tab.z;
     const int gsp = blockIdx.x % per_chunk, g_ = gsp / pl.splits, split = gsp % pl.splits;
     const int Cg = a.C / a.G, S = a.S;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int p = lane % P, cl = lane / P, s0 = SPT * p;
-    float *sB = sm + L::oB, *sC = sm + L::oC, *sBC = sm + L::oBC;
-    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * SB * CW;  // [token][channel]
-    float4* ck = reinterpret_cast<float4*>(sm + L::oCk) + tid;            // [run][pass], stride 128
-    float4* gA = reinterpret_cast<float4*>(sm + L::oG) + tid;             // g, dA: [2][pass]
-    float* red = sm + L::oRed;                                            // [warp][token][2 SP]
+    float *sB = sm + L::oB, *sC = sm + L::oC;
+    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * 2 * UT * CW;    // [buffer][token][channel]
+    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;          // [run][pass], stride 128
+    float4* part = reinterpret_cast<float4*>(sm + L::oSum) + w * RT * CW * P;   // [token][channel][lane]
+    float* red = sm + L::oRed;                                                  // [parity][warp][token][2 SP]
     ssm_load_rows<E, SP>(sB, a.B, a.ldb, t0, len, g_ * S, S);
     ssm_load_rows<E, SP>(sC, a.Cm, a.ldc, t0, len, g_ * S, S);
-    if (pl.nl > 1)
-        for (int i = tid; i < CH * 2 * SP; i += SSM_THREADS) sBC[i] = 0.f;
     __syncthreads();
+    const int nu = (len + UT - 1) / UT;  // units
+    const bool gated = a.z;
+    int par = 0;
 
     for (int it = 0; it < pl.nl; ++it) {
         const int cb = (split * pl.nl + it) * L::CB;  // the tile's first channel in the group
         if (cb >= Cg) break;
-        const int cw = cb + w * CW;  // the warp's
+        const int cw = cb + w * CW;                                         // the warp's
         auto chan = [&](int j) { return g_ * Cg + min(cw + j, Cg - 1); };  // its j-th channel
-        float4 A4[NP];
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            A4[q] = ld4(a.A + int64_t(chan(q * CL + cl)) * S, s0, S);
-            // lanes past the group's channels stay zero: they add nothing to dB and dC
-            ck[q * SSM_THREADS] = ld4(a.hs + (int64_t(k) * a.C + chan(q * CL + cl)) * S, s0,
-                                      cw + q * CL + cl < Cg ? S : 0);
-        }
-        // the warp's delta, delta u and dY of run b; tokens past the chunk are the identity step
-        auto stage = [&](int b, bool grad) {
-#pragma unroll
-            for (int i = lane; i < SB * CW; i += 32) {
-                const int r = b * SB + i / CW, c = chan(i % CW);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < len && cw + i % CW < Cg) {
-                    const int64_t t = t0 + r;
-                    v.x = ssm_delta(ssm_ld<E>(a.dt, t * a.lddt + c) + (a.bias ? a.bias[c] : 0.f), a.softplus);
-                    v.y = v.x * ssm_ld<E>(a.u, t * a.ldu + c);
-                    if (grad) {
-                        v.z = ssm_ld<E>(a.dy, t * a.C + c);
-                        if (a.z) v.z *= ssm_silu(ssm_ld<E>(a.z, t * a.ldz + c));
-                    }
-                }
-                pre[i] = v;
-            }
-            __syncwarp();
+        // lanes as states: pass q's channel.  Lanes past the group's channels stay zero: they add
+        // nothing to dB and dC
+        f2 A2[NP][2], g[NP][2], dA[NP][2], hs[NP][2];
+        auto lim = [&](int q) { return cw + q * CL + cl < Cg ? S : 0; };
+        auto pair2 = [](float4 v, f2(&o)[2]) { o[0] = pk2(v.x, v.y), o[1] = pk2(v.z, v.w); };
+        auto start = [&](int u, int q) {  // the state at unit u's start
+            return ld4(a.hs + ((int64_t(k) * SSM_SUB + u) * a.C + chan(q * CL + cl)) * S, s0, lim(q));
         };
-        // forward sweep: the states at every run's start
-        for (int b = 0; b + 1 < nsub; ++b) {
-            stage(b, false);
-#pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                const float4 h4 = ck[(b * NP + q) * SSM_THREADS];
-                const f2 Aa = pk2(LOG2E * A4[q].x, LOG2E * A4[q].y), Ab = pk2(LOG2E * A4[q].z, LOG2E * A4[q].w);
-                f2 ha = pk2(h4.x, h4.y), hb = pk2(h4.z, h4.w);
-#pragma unroll
-                for (int i = 0; i < SB; ++i) {
-                    const float2 v = *reinterpret_cast<const float2*>(pre + i * CW + q * CL + cl);
-                    const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y);
-                    const f2* Bp = reinterpret_cast<const f2*>(sB + (b * SB + i) * SP + s0);
-                    ha = fma2(ex2_2(mul2(Aa, d2)), ha, mul2(Bp[0], u2));
-                    hb = fma2(ex2_2(mul2(Ab, d2)), hb, mul2(Bp[1], u2));
-                }
-                float4 o;
-                up2(ha, o.x, o.y);
-                up2(hb, o.z, o.w);
-                ck[((b + 1) * NP + q) * SSM_THREADS] = o;
-            }
-            __syncwarp();
-        }
+        float4 nh[NP];
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
-            gA[q * SSM_THREADS] = ld4(a.gs + (int64_t(k) * a.C + chan(q * CL + cl)) * S, s0,
-                                      cw + q * CL + cl < Cg ? S : 0);
-            gA[(NP + q) * SSM_THREADS] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int64_t row = int64_t(chan(q * CL + cl)) * S;
+            float4 v = ld4(a.A + row, s0, S);
+            v.x *= LOG2E, v.y *= LOG2E, v.z *= LOG2E, v.w *= LOG2E;
+            pair2(v, A2[q]);
+            pair2(ld4(a.gs + int64_t(k) * a.C * S + row, s0, lim(q)), g[q]);
+            dA[q][0] = dA[q][1] = 0;
+            nh[q] = start(nu - 1, q);
         }
-        float accD[CW > 32 ? 2 : 1] = {}, accb[CW > 32 ? 2 : 1] = {};
-        for (int b = nsub - 1; b >= 0; --b) {
-            stage(b, true);
-            float bc[SB][2 * SPT];  // dB, dC of the run's tokens, summed over the passes
+        // lanes as (token, channel) items of a run: item x is token (lane + 32 x) / CW of the run and
+        // channel (lane + 32 x) % CW of the warp
+        float bias[NB], skip[NB], accD[NB] = {}, accb[NB] = {};
 #pragma unroll
-            for (int i = 0; i < SB; ++i)
+        for (int x = 0; x < NB; ++x) {
+            const int c = chan(lane % CW + 32 * x);
+            bias[x] = a.bias ? a.bias[c] : 0.f;
+            skip[x] = a.D ? a.D[c] : 0.f;
+        }
+        struct Raw { E dt, u, dy, z; };
+        auto fetch = [&](Raw(&r)[NI], int row0) {
 #pragma unroll
-                for (int j = 0; j < 2 * SPT; ++j) bc[i][j] = 0.f;
+            for (int x = 0; x < NI; ++x) {
+                const int i = lane + 32 * x, c = chan(i % CW);
+                const int64_t t = t0 + min(row0 + i / CW, len - 1);
+                r[x].dt = static_cast<const E*>(a.dt)[t * a.lddt + c];
+                r[x].u = static_cast<const E*>(a.u)[t * a.ldu + c];
+                r[x].dy = static_cast<const E*>(a.dy)[t * a.C + c];
+                if (gated) r[x].z = static_cast<const E*>(a.z)[t * a.ldz + c];
+            }
+        };
+        // delta, delta u and dY of a run into a unit's buffer; tokens past the chunk are the identity step
+        auto stage = [&](const Raw(&r)[NI], int u, int run) {
+#pragma unroll
+            for (int x = 0; x < NI; ++x) {
+                const int i = lane + 32 * x;
+                if (RT * CW < 32 && i >= RT * CW) break;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (u * UT + run * RT + i / CW < len && cw + i % CW < Cg) {
+                    v.x = ssm_delta(ssm_f<E>(r[x].dt) + bias[x % NB], a.softplus);
+                    v.y = v.x * ssm_f<E>(r[x].u);
+                    v.z = ssm_f<E>(r[x].dy);
+                    if (gated) v.z *= ssm_silu(ssm_f<E>(r[x].z));
+                }
+                pre[((u & 1) * UT + run * RT) * CW + i] = v;
+            }
+        };
+        Raw nxt[NI], cur[NI];
 #pragma unroll 1
-            for (int q = 0; q < NP; ++q) {
-                const float4 A_ = A4[0], A__ = A4[NP - 1];
-                const float4 Aq = q ? A__ : A_;
-                const float* av = &Aq.x;
-                float h[SB + 1][SPT], dec[SB][SPT];
-                {
-                    const float4 h4 = ck[(b * NP + q) * SSM_THREADS];
-                    h[0][0] = h4.x, h[0][1] = h4.y, h[0][2] = h4.z, h[0][3] = h4.w;
-                }
-                const float4* pq = pre + q * CL + cl;
-#pragma unroll
-                for (int i = 0; i < SB; ++i) {
-                    const float2 v = *reinterpret_cast<const float2*>(pq + i * CW);
-                    const float4 B4 = *reinterpret_cast<const float4*>(sB + (b * SB + i) * SP + s0);
-                    const float* bv = &B4.x;
-#pragma unroll
-                    for (int j = 0; j < SPT; ++j) {
-                        dec[i][j] = ex2(av[j] * LOG2E * v.x);
-                        h[i + 1][j] = fmaf(dec[i][j], h[i][j], bv[j] * v.y);
-                    }
-                }
-                float4 g4 = gA[q * SSM_THREADS], dA4 = gA[(NP + q) * SSM_THREADS];
-                float *g = &g4.x, *dA = &dA4.x;
-                float sums[3][SB];
-#pragma unroll
-                for (int i = SB - 1; i >= 0; --i) {
-                    const float4 v = pq[i * CW];
-                    const float4 B4 = *reinterpret_cast<const float4*>(sB + (b * SB + i) * SP + s0);
-                    const float4 C4 = *reinterpret_cast<const float4*>(sC + (b * SB + i) * SP + s0);
-                    const float *bv = &B4.x, *cv = &C4.x;
-                    float xB = 0.f, xw = 0.f, xy = 0.f;
-#pragma unroll
-                    for (int j = 0; j < SPT; ++j) {
-                        const float G = fmaf(cv[j], v.z, g[j]);
-                        bc[i][j] = fmaf(G, v.y, bc[i][j]);
-                        bc[i][SPT + j] = fmaf(h[i + 1][j], v.z, bc[i][SPT + j]);
-                        xB = fmaf(G, bv[j], xB);
-                        xy = fmaf(cv[j], h[i + 1][j], xy);
-                        g[j] = dec[i][j] * G;
-                        const float wj = g[j] * h[i][j];
-                        xw = fmaf(wj, av[j], xw);
-                        dA[j] = fmaf(wj, v.x, dA[j]);
-                    }
-                    sums[0][i] = xB, sums[1][i] = xw, sums[2][i] = xy;
-                }
-                gA[q * SSM_THREADS] = g4;
-                gA[(NP + q) * SSM_THREADS] = dA4;
-                // sums over the channel's lanes
-#pragma unroll
-                for (int i = 0; i < SB; ++i)
-#pragma unroll
-                    for (int x = 0; x < 3; ++x)
-#pragma unroll
-                        for (int o = 1; o < P; o <<= 1)
-                            sums[x][i] += __shfl_xor_sync(0xffffffffu, sums[x][i], o);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < SB; ++i)
-                    if (p == i % P) {
-                        float* o = reinterpret_cast<float*>(pre + i * CW + q * CL + cl);
-                        o[1] = sums[0][i];
-                        o[2] = sums[1][i];
-                        o[3] = sums[2][i];
-                    }
-            }
-            // dB, dC of the run over the warp's channels
-#pragma unroll
-            for (int i = 0; i < SB; ++i) {
-                constexpr int NV = 2 * SPT, n = NV / CL > 1 ? NV / CL : 1;
-                reduce_lanes<NV, P>(bc[i], lane);
-                // (with more channel lanes than values, several lanes write the same sum)
-                const int idx = reduce_index<NV, P>(lane);
-#pragma unroll
-                for (int j = 0; j < n; ++j) {
-                    const int vi = idx + j;  // 0 .. 3: dB, 4 .. 7: dC
-                    red[(w * SB + i) * 2 * SP + (vi / SPT) * SP + s0 + vi % SPT] = bc[i][j];
-                }
-            }
+        for (int r = 0; r < NR; ++r) {
+            fetch(nxt, (nu - 1) * UT + r * RT);
+            stage(nxt, nu - 1, r);
+        }
+#pragma unroll 1
+        for (int u = nu - 1; u >= 0; --u) {
+            const float4* pu = pre + (u & 1) * UT * CW + cl;
+            const int nr = (min(UT, len - u * UT) + RT - 1) / RT;  // runs of the unit
             __syncwarp();
-            // the run's du, ddt, dz: lanes are channels again
 #pragma unroll
-            for (int i = lane, x = 0; i < SB * CW; i += 32, ++x) {
-                const int r = b * SB + i / CW, ci = cw + i % CW;
-                if (r < len && ci < Cg) {
-                    const int c = g_ * Cg + ci;
-                    const int64_t t = t0 + r;
-                    const float4 v = pre[i];  // delta, sum G B, sum A w, sum C h
-                    const float u = ssm_ld<E>(a.u, t * a.ldu + c), raw = ssm_ld<E>(a.dt, t * a.lddt + c) + (a.bias ? a.bias[c] : 0.f);
-                    const float skip = a.D ? a.D[c] : 0.f;
-                    float dY = ssm_ld<E>(a.dy, t * a.C + c);
-                    if (a.z) {
-                        const float z = ssm_ld<E>(a.z, t * a.ldz + c), sg = ssm_sigmoid(z);
-                        ssm_st<E>(a.dz, t * a.C + c, dY * fmaf(skip, u, v.w) * sg * fmaf(z, 1.f - sg, 1.f));
-                        dY *= ssm_silu(z);
+            for (int q = 0; q < NP; ++q) {
+                pair2(nh[q], hs[q]);
+                if (u > 0) nh[q] = start(u - 1, q);
+            }
+            // forward sweep: the states at every run's start
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                f2 ha = hs[q][0], hb = hs[q][1];
+#pragma unroll 1
+                for (int r = 0; r + 1 < nr; ++r) {
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const float2 v = *reinterpret_cast<const float2*>(pu + (r * RT + i) * CW + q * CL);
+                        const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y);
+                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(sB + (u * UT + r * RT + i) * SP + s0);
+                        ha = fma2(ex2_2(mul2(A2[q][0], d2)), ha, mul2(b2.x, u2));
+                        hb = fma2(ex2_2(mul2(A2[q][1], d2)), hb, mul2(b2.y, u2));
                     }
-                    ssm_st<E>(a.du, t * a.C + c, fmaf(v.x, v.y, skip * dY));
-                    float dd = fmaf(u, v.y, v.z);
-                    if (a.softplus) dd *= ssm_sigmoid(raw);
-                    ssm_st<E>(a.ddt, t * a.C + c, dd);
-                    accD[CW > 32 ? x & 1 : 0] += dY * u;
-                    accb[CW > 32 ? x & 1 : 0] += dd;
+                    ck[(r * NP + q) * SSM_THREADS] = make_ulonglong2(ha, hb);
                 }
             }
-            __syncthreads();  // every warp's sums are written
-            for (int i = tid; i < SB * 2 * SP; i += SSM_THREADS) {
-                float s = red[i];
-#pragma unroll
-                for (int j = 1; j < NW; ++j) s += red[j * SB * 2 * SP + i];
-                const int r = b * SB + i / (2 * SP), v = i % (2 * SP), x = v / SP, st = v % SP;
-                if (pl.nl > 1) sBC[r * 2 * SP + v] += s;
-                else if (r < len && st < S) a.pBC[(int64_t(gsp) * a.T + t0 + r) * 2 * S + x * S + st] = s;
+            // runs the unit lacks (its chunk ends inside it) still stage the next unit's tokens
+#pragma unroll 1
+            for (int r = nr; u > 0 && r < NR; ++r) {
+                fetch(nxt, (u - 1) * UT + r * RT);
+                stage(nxt, u - 1, r);
             }
-            __syncthreads();  // read before the next run's are written
+#pragma unroll 1
+            for (int r = nr - 1; r >= 0; --r) {
+                const int row0 = u * UT + r * RT;
+                if (u > 0) fetch(nxt, row0 - UT);
+                fetch(cur, row0);
+                f2 bc[RT][4];  // dB, dC of the run's tokens, summed over the passes
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) bc[i][j] = 0;
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    f2 h[RT + 1][2], dec[RT][2];
+                    h[0][0] = hs[q][0], h[0][1] = hs[q][1];
+                    if (r > 0) {
+                        const ulonglong2 v = ck[((r - 1) * NP + q) * SSM_THREADS];
+                        h[0][0] = v.x, h[0][1] = v.y;
+                    }
+                    const float4* pq = pu + r * RT * CW + q * CL;
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const float2 v = *reinterpret_cast<const float2*>(pq + i * CW);
+                        const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y);
+                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(sB + (row0 + i) * SP + s0);
+                        dec[i][0] = ex2_2(mul2(A2[q][0], d2));
+                        dec[i][1] = ex2_2(mul2(A2[q][1], d2));
+                        h[i + 1][0] = fma2(dec[i][0], h[i][0], mul2(b2.x, u2));
+                        h[i + 1][1] = fma2(dec[i][1], h[i][1], mul2(b2.y, u2));
+                    }
+#pragma unroll
+                    for (int i = RT - 1; i >= 0; --i) {
+                        const float4 v = pq[i * CW];
+                        const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y), y2 = pk2(v.z, v.z);
+                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(sB + (row0 + i) * SP + s0);
+                        const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(sC + (row0 + i) * SP + s0);
+                        const f2 G0 = fma2(c2.x, y2, g[q][0]), G1 = fma2(c2.y, y2, g[q][1]);
+                        bc[i][0] = fma2(G0, u2, bc[i][0]);
+                        bc[i][1] = fma2(G1, u2, bc[i][1]);
+                        bc[i][2] = fma2(h[i + 1][0], y2, bc[i][2]);
+                        bc[i][3] = fma2(h[i + 1][1], y2, bc[i][3]);
+                        const f2 xB = fma2(G1, b2.y, mul2(G0, b2.x));
+                        const f2 xy = fma2(h[i + 1][1], c2.y, mul2(h[i + 1][0], c2.x));
+                        g[q][0] = mul2(dec[i][0], G0);
+                        g[q][1] = mul2(dec[i][1], G1);
+                        const f2 w0 = mul2(g[q][0], h[i][0]), w1 = mul2(g[q][1], h[i][1]);
+                        const f2 xw = fma2(w1, A2[q][1], mul2(w0, A2[q][0]));
+                        dA[q][0] = fma2(w0, d2, dA[q][0]);
+                        dA[q][1] = fma2(w1, d2, dA[q][1]);
+                        part[(i * CW + q * CL) * P + lane] = make_float4(hsum2(xB), hsum2(xw), hsum2(xy), 0.f);
+                    }
+                }
+                // dB, dC of the run over the warp's channels
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    constexpr int NV = 2 * SPT, n = NV / CL > 1 ? NV / CL : 1;
+                    float v[NV];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) up2(bc[i][j], v[2 * j], v[2 * j + 1]);
+                    reduce_lanes<NV, P>(v, lane);
+                    // (with more channel lanes than values, several lanes write the same sum)
+                    const int idx = reduce_index<NV, P>(lane);
+#pragma unroll
+                    for (int j = 0; j < n; ++j) {
+                        const int vi = idx + j;  // 0 .. 3: dB, 4 .. 7: dC
+                        red[((par * NW + w) * RT + i) * 2 * SP + (vi / SPT) * SP + s0 + vi % SPT] = v[j];
+                    }
+                }
+                __syncwarp();
+                // the run's du, ddt, dz, and the next unit's scalars: lanes are channels
+#pragma unroll
+                for (int x = 0; x < NI; ++x) {
+                    const int i = lane + 32 * x, row = row0 + i / CW;
+                    if (row < len && cw + i % CW < Cg && (RT * CW >= 32 || i < RT * CW)) {
+                        float sB_ = 0.f, sw = 0.f, sy = 0.f;  // sum G B, log2(e) sum A w, sum C h
+#pragma unroll
+                        for (int j = 0; j < P; ++j) {
+                            const float4 v = part[i * P + j];
+                            sB_ += v.x, sw += v.y, sy += v.z;
+                        }
+                        const int64_t o = (int64_t(t0) + row) * a.C + g_ * Cg + cw + i % CW;
+                        const float4 v = pre[((u & 1) * UT + r * RT) * CW + i];  // delta, delta u, dY
+                        const float ux = ssm_f<E>(cur[x].u), sk = skip[x % NB];
+                        if (gated) {
+                            const float z = ssm_f<E>(cur[x].z), sg = ssm_sigmoid(z);
+                            ssm_st<E>(a.dz, o, ssm_f<E>(cur[x].dy) * fmaf(sk, ux, sy) * sg * fmaf(z, 1.f - sg, 1.f));
+                        }
+                        ssm_st<E>(a.du, o, fmaf(v.x, sB_, sk * v.z));
+                        float dd = fmaf(ux, sB_, sw * 0.6931471805599453f);
+                        if (a.softplus) dd *= ssm_sigmoid(ssm_f<E>(cur[x].dt) + bias[x % NB]);
+                        ssm_st<E>(a.ddt, o, dd);
+                        accD[x % NB] = fmaf(v.z, ux, accD[x % NB]);
+                        accb[x % NB] += dd;
+                    }
+                }
+                if (u > 0) stage(nxt, u - 1, r);
+                // the warps' sums are written; two buffers, so that one barrier a run is enough
+                __syncthreads();
+                for (int i = tid; i < RT * 2 * SP; i += SSM_THREADS) {
+                    const float* rp = red + par * NW * RT * 2 * SP + i;
+                    float s = rp[0];
+#pragma unroll
+                    for (int j = 1; j < NW; ++j) s += rp[j * RT * 2 * SP];
+                    const int row = row0 + i / (2 * SP), v = i % (2 * SP), x = v / SP, st = v % SP;
+                    if (row < len && st < S) {  // the same thread adds every tile of the block
+                        float* o = a.pBC + (int64_t(gsp) * a.T + t0 + row) * 2 * S + x * S + st;
+                        *o = it ? *o + s : s;
+                    }
+                }
+                par ^= 1;
+            }
         }
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             const int ci = cw + q * CL + cl;
             if (ci < Cg) {
                 const int c = g_ * Cg + ci;
-                st4(a.pA + (int64_t(k) * a.C + c) * (S + 2), s0, S, gA[(NP + q) * SSM_THREADS]);
-                if (a.dh0 && tab.w == 0) st4(a.dh0 + (int64_t(tab.x) * a.C + c) * S, s0, S, gA[q * SSM_THREADS]);
+                float4 v;
+                up2(dA[q][0], v.x, v.y);
+                up2(dA[q][1], v.z, v.w);
+                st4(a.pA + (int64_t(k) * a.C + c) * (S + 2), s0, S, v);
+                up2(g[q][0], v.x, v.y);
+                up2(g[q][1], v.z, v.w);
+                if (a.dh0 && tab.w == 0) st4(a.dh0 + (int64_t(tab.x) * a.C + c) * S, s0, S, v);
             }
         }
         // lanes that share a channel hold its tokens' terms of dD and dbias
 #pragma unroll
-        for (int x = 0; x < (CW > 32 ? 2 : 1); ++x) {
+        for (int x = 0; x < NB; ++x) {
 #pragma unroll
             for (int o = CW; o < 32; o <<= 1) {
                 accD[x] += __shfl_xor_sync(0xffffffffu, accD[x], o);
                 accb[x] += __shfl_xor_sync(0xffffffffu, accb[x], o);
             }
-            const int j = lane % CW + 32 * x, ci = cw + j;
+            const int ci = cw + lane % CW + 32 * x;
             if (ci < Cg && lane < CW) {
                 float* o = a.pA + (int64_t(k) * a.C + g_ * Cg + ci) * (S + 2) + S;
                 o[0] = accD[x];
                 o[1] = accb[x];
             }
         }
+        __syncwarp();
     }
-    if (pl.nl > 1)
-        for (int i = tid; i < len * 2 * S; i += SSM_THREADS) {
-            const int r = i / (2 * S), v = i % (2 * S);
-            a.pBC[(int64_t(gsp) * a.T + t0) * 2 * S + i] = sBC[r * 2 * SP + v / S * SP + v % S];
-        }
 }
 
 // dB, dC: the channel blocks' sums in order, in runs of SSM_QUAD tiles whatever a block covered

@@ -60,41 +60,37 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_state(SsmArgs a, int tiles)
 #pragma unroll
     for (int j = 0; j < H2; ++j) h[j] = 0;
     const float bias = a.bias ? a.bias[pl.c] : 0.f;
-    float ru[GR], rd[GR], sum = 0.f;
-    int64_t iu = int64_t(t.y) * a.ldu + pl.c, id = int64_t(t.y) * a.lddt + pl.c;
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-        ru[i] = ssm_ld<E>(a.u, iu + i * a.ldu);
-        rd[i] = ssm_ld<E>(a.dt, id + i * a.lddt);
-    }
+    float sum = 0.f;
+    Ahead<E, GR> u(a.u, t.y, a.ldu, pl.c), d(a.dt, t.y, a.lddt, pl.c);
+    u.load(GR);
+    d.load(GR);
     __syncthreads();
+#pragma unroll 1
     for (int q = 0; q < CH; q += GR) {  // a chunk with a successor is full
-        float cu[GR], cd[GR];
+        E cu[GR], cd[GR];
 #pragma unroll
-        for (int i = 0; i < GR; ++i) cu[i] = ru[i], cd[i] = rd[i];
+        for (int i = 0; i < GR; ++i) cu[i] = u.raw[i], cd[i] = d.raw[i];
         if (q + GR < CH) {
-            iu += GR * a.ldu;
-            id += GR * a.lddt;
-#pragma unroll
-            for (int i = 0; i < GR; ++i) {
-                ru[i] = ssm_ld<E>(a.u, iu + i * a.ldu);
-                rd[i] = ssm_ld<E>(a.dt, id + i * a.lddt);
-            }
+            u.load(GR);
+            d.load(GR);
         }
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
-            const float dl = ssm_delta(cd[i] + bias, a.softplus), du = dl * cu[i];
+            const float dl = ssm_delta(ssm_f<E>(cd[i]) + bias, a.softplus), du = dl * ssm_f<E>(cu[i]);
             sum += dl;
             const f2 dl2 = pk2(dl, dl), du2 = pk2(du, du);
-            const f2* Bp = reinterpret_cast<const f2*>(sB + (q + i) * SP + pl.s0);
+            const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(sB + (q + i) * SP + pl.s0);
 #pragma unroll
-            for (int j = 0; j < H2; ++j)
-                h[j] = fma2(ex2_2(mul2(A2[j], dl2)), h[j], mul2(Bp[j], du2));
+            for (int j = 0; j < H2; j += 2) {
+                const ulonglong2 b2 = Bp[j / 2];
+                h[j] = fma2(ex2_2(mul2(A2[j], dl2)), h[j], mul2(b2.x, du2));
+                h[j + 1] = fma2(ex2_2(mul2(A2[j + 1], dl2)), h[j + 1], mul2(b2.y, du2));
+            }
         }
     }
     if (!pl.on) return;
     if (pl.s0 == 0) a.sumdt[int64_t(k) * a.C + pl.c] = sum;
-    float* out = a.hs + (int64_t(k + 1) * a.C + pl.c) * a.S + pl.s0;  // the next chunk's slot
+    float* out = a.hs + (int64_t(k + 1) * a.sub * a.C + pl.c) * a.S + pl.s0;  // the next chunk's slot
 #pragma unroll
     for (int j = 0; j < H2; ++j) {
         float x, y;
@@ -104,8 +100,8 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_state(SsmArgs a, int tiles)
     }
 }
 
-// One thread per (document, channel, state).  hs[k + 1] holds chunk k's end from a zero start and
-// receives chunk k + 1's start state.
+// One thread per (document, channel, state).  Chunk k + 1's slot of hs holds chunk k's end from a zero
+// start and receives chunk k + 1's start state.
 constexpr int CARRY_THREADS = 128;
 __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_carry(SsmArgs a, int blocks_per_doc) {
     if (*a.status != KDA_OK) return;
@@ -121,7 +117,8 @@ __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_carry(SsmArgs a, int bloc
         return;
     }
     const float A2 = LOG2E * a.A[i];
-    float* hs = a.hs + int64_t(k0) * CS + i;
+    const int64_t hstep = CS * a.sub;
+    float* hs = a.hs + k0 * hstep + i;
     const float* sd = a.sumdt + int64_t(k0) * a.C + c;
     hs[0] = h;
     constexpr int U = 8;  // chunks loaded together
@@ -131,14 +128,14 @@ __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_carry(SsmArgs a, int bloc
 #pragma unroll
         for (int j = 0; j < U; ++j)
             if (j < m) {
-                e[j] = hs[(k + j + 1) * CS];
+                e[j] = hs[(k + j + 1) * hstep];
                 d[j] = sd[int64_t(k + j) * a.C];
             }
 #pragma unroll
         for (int j = 0; j < U; ++j)
             if (j < m) {
                 h = fmaf(ex2(A2 * d[j]), h, e[j]);
-                hs[(k + j + 1) * CS] = h;
+                hs[(k + j + 1) * hstep] = h;
             }
     }
 }
@@ -157,53 +154,83 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_out(SsmArgs a, int tiles) {
     f2 A2[H2], h[H2];
     load_A<SPT>(a, pl.c, pl.s0, A2);
     {
-        const float* in = a.hs + (int64_t(k) * a.C + pl.c) * a.S + pl.s0;
+        const float* in = a.hs + (int64_t(k) * a.sub * a.C + pl.c) * a.S + pl.s0;
 #pragma unroll
         for (int j = 0; j < H2; ++j)
             h[j] = pk2(FULL || pl.s0 + 2 * j < a.S ? in[2 * j] : 0.f,
                        FULL || pl.s0 + 2 * j + 1 < a.S ? in[2 * j + 1] : 0.f);
     }
     const float bias = a.bias ? a.bias[pl.c] : 0.f, skip = a.D ? a.D[pl.c] : 0.f;
-    float ru[GR], rd[GR], rz[GR];
-    int64_t iu = int64_t(t.y) * a.ldu + pl.c, id = int64_t(t.y) * a.lddt + pl.c;
-    int64_t iz = int64_t(t.y) * a.ldz + pl.c, iy = int64_t(t.y) * a.C + pl.c;
-    auto load = [&](int q) {  // rows q .. q + GR - 1 of the chunk (past its end: the last row again)
-#pragma unroll
-        for (int i = 0; i < GR; ++i) {
-            const int r = min(q + i, len - 1);
-            ru[i] = ssm_ld<E>(a.u, iu + r * a.ldu);
-            rd[i] = ssm_ld<E>(a.dt, id + r * a.lddt);
-            rz[i] = a.z ? ssm_ld<E>(a.z, iz + r * a.ldz) : 0.f;
-        }
-    };
-    load(0);
+    // (the backward's replay takes the states alone: no y, no ht)
+    const bool writer = a.y && pl.on && pl.s0 == 0, gated = a.z, keep = a.sub > 1;
+    Ahead<E, GR> u(a.u, t.y, a.ldu, pl.c), d(a.dt, t.y, a.lddt, pl.c), z(a.z, t.y, a.ldz, pl.c);
+    E* yp = static_cast<E*>(a.y) + int64_t(t.y) * a.C + pl.c;
+    u.load(len);
+    d.load(len);
+    if (gated) z.load(len);
     __syncthreads();
-    for (int q = 0; q < len; q += GR) {
-        float cu[GR], cd[GR], cz[GR];
+    E cu[GR], cd[GR], cz[GR];
+    auto token = [&](int q, int i) {
+        const float x = ssm_f<E>(cu[i]);
+        const float dl = ssm_delta(ssm_f<E>(cd[i]) + bias, a.softplus), du = dl * x;
+        const f2 dl2 = pk2(dl, dl), du2 = pk2(du, du);
+        const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(sB + (q + i) * SP + pl.s0);
+        const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(sC + (q + i) * SP + pl.s0);
+        f2 acc = 0;
 #pragma unroll
-        for (int i = 0; i < GR; ++i) cu[i] = ru[i], cd[i] = rd[i], cz[i] = rz[i];
-        if (q + GR < len) load(q + GR);
+        for (int j = 0; j < H2; j += 2) {
+            const ulonglong2 b2 = Bp[j / 2], c2 = Cp[j / 2];
+            h[j] = fma2(ex2_2(mul2(A2[j], dl2)), h[j], mul2(b2.x, du2));
+            h[j + 1] = fma2(ex2_2(mul2(A2[j + 1], dl2)), h[j + 1], mul2(b2.y, du2));
+            if (!FULL) {
+                h[j] = keep2(h[j], pl.s0 + 2 * j, a.S);
+                h[j + 1] = keep2(h[j + 1], pl.s0 + 2 * j + 2, a.S);
+            }
+            acc = fma2(h[j], c2.x, acc);
+            acc = fma2(h[j + 1], c2.y, acc);
+        }
+        float y = hsum2(acc);
+#pragma unroll
+        for (int o = 32 / P; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        y = fmaf(skip, x, y);
+        if (gated) y *= ssm_silu(ssm_f<E>(cz[i]));
+        if (writer) ssm_st<E>(yp, int64_t(i) * a.C, y);
+    };
+#pragma unroll 1
+    for (int q = 0; q < len; q += GR) {
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
-            if (q + i >= len) break;
-            const float dl = ssm_delta(cd[i] + bias, a.softplus), du = dl * cu[i];
-            const f2 dl2 = pk2(dl, dl), du2 = pk2(du, du);
-            const f2* Bp = reinterpret_cast<const f2*>(sB + (q + i) * SP + pl.s0);
-            const f2* Cp = reinterpret_cast<const f2*>(sC + (q + i) * SP + pl.s0);
-            f2 acc = 0;
+            cu[i] = u.raw[i], cd[i] = d.raw[i];
+            if (gated) cz[i] = z.raw[i];
+        }
+        if (q + GR < len) {
+            u.load(len - q - GR);
+            d.load(len - q - GR);
+            if (gated) z.load(len - q - GR);
+        }
+        if (keep && q % SSM_UT == 0 && q > 0 && pl.on) {
+            float* out = a.hs + ((int64_t(k) * a.sub + q / SSM_UT) * a.C + pl.c) * a.S + pl.s0;
 #pragma unroll
             for (int j = 0; j < H2; ++j) {
-                h[j] = fma2(ex2_2(mul2(A2[j], dl2)), h[j], mul2(Bp[j], du2));
-                if (!FULL) h[j] = keep2(h[j], pl.s0 + 2 * j, a.S);
-                acc = fma2(h[j], Cp[j], acc);
+                float x, y;
+                up2(h[j], x, y);
+                if (FULL) {
+                    *reinterpret_cast<float2*>(out + 2 * j) = make_float2(x, y);
+                } else {
+                    if (pl.s0 + 2 * j < a.S) out[2 * j] = x;
+                    if (pl.s0 + 2 * j + 1 < a.S) out[2 * j + 1] = y;
+                }
             }
-            float y = hsum2(acc);
-#pragma unroll
-            for (int o = 32 / P; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            y = fmaf(skip, cu[i], y);
-            if (a.z) y *= ssm_silu(cz[i]);
-            if (pl.on && pl.s0 == 0) ssm_st<E>(a.y, iy + int64_t(q + i) * a.C, y);
         }
+        if (q + GR <= len) {
+#pragma unroll
+            for (int i = 0; i < GR; ++i) token(q, i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < GR - 1; ++i)
+                if (q + i < len) token(q, i);
+        }
+        yp += GR * int64_t(a.C);
     }
     if (a.ht && pl.on && t.y + len == a.cu[t.x + 1]) {  // the document's last chunk
         float* out = a.ht + (int64_t(t.x) * a.C + pl.c) * a.S + pl.s0;
@@ -218,7 +245,7 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_out(SsmArgs a, int tiles) {
 }
 
 template <class E, int SPT, int P, bool FULL>
-void launch(const SsmArgs& a, bool out, cudaStream_t st) {
+void launch(const SsmArgs& a, cudaStream_t st) {
     const int Cg = a.C / a.G, CB = SSM_THREADS / P;
     const int tiles = a.G * ((Cg + CB - 1) / CB);
     const unsigned grid = unsigned(a.maxC * tiles);
@@ -232,34 +259,34 @@ void launch(const SsmArgs& a, bool out, cudaStream_t st) {
         const int bpd = int((CS + CARRY_THREADS - 1) / CARRY_THREADS);
         k_ssm_carry<<<unsigned(int64_t(bpd) * a.N), CARRY_THREADS, 0, st>>>(a, bpd);
     }
-    if (out && grid) {
+    if (grid) {
         ProfScope ps(KK_SSM_OUT, st);
         k_ssm_out<E, SPT, P, FULL><<<grid, SSM_THREADS, 0, st>>>(a, tiles);
     }
 }
 
 template <class E>
-void launch_e(const SsmArgs& a, bool out, cudaStream_t st) {
+void launch_e(const SsmArgs& a, cudaStream_t st) {
     switch (a.S) {  // the usual state counts fill their lanes; others are padded to the next one
-        case 4: return launch<E, 4, 1, true>(a, out, st);
-        case 8: return launch<E, 8, 1, true>(a, out, st);
-        case 16: return launch<E, 16, 1, true>(a, out, st);
-        case 32: return launch<E, 16, 2, true>(a, out, st);
-        case 64: return launch<E, 16, 4, true>(a, out, st);
+        case 4: return launch<E, 4, 1, true>(a, st);
+        case 8: return launch<E, 8, 1, true>(a, st);
+        case 16: return launch<E, 16, 1, true>(a, st);
+        case 32: return launch<E, 16, 2, true>(a, st);
+        case 64: return launch<E, 16, 4, true>(a, st);
         default: break;
     }
-    if (a.S < 8) return launch<E, 8, 1, false>(a, out, st);
-    if (a.S < 16) return launch<E, 16, 1, false>(a, out, st);
-    if (a.S < 32) return launch<E, 16, 2, false>(a, out, st);
-    return launch<E, 16, 4, false>(a, out, st);
+    if (a.S < 8) return launch<E, 8, 1, false>(a, st);
+    if (a.S < 16) return launch<E, 16, 1, false>(a, st);
+    if (a.S < 32) return launch<E, 16, 2, false>(a, st);
+    return launch<E, 16, 4, false>(a, st);
 }
 
 }  // namespace
 
-void launch_ssm_scan(const SsmArgs& a, int dtype, bool out, cudaStream_t st) {
-    if (dtype == KDA_DT_BF16) launch_e<__nv_bfloat16>(a, out, st);
-    else if (dtype == KDA_DT_FP16) launch_e<__half>(a, out, st);
-    else launch_e<float>(a, out, st);
+void launch_ssm_scan(const SsmArgs& a, int dtype, cudaStream_t st) {
+    if (dtype == KDA_DT_BF16) launch_e<__nv_bfloat16>(a, st);
+    else if (dtype == KDA_DT_FP16) launch_e<__half>(a, st);
+    else launch_e<float>(a, st);
 }
 
 }  // namespace kda

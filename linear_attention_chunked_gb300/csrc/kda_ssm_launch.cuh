@@ -5,8 +5,8 @@
 
 namespace kda {
 
-// chunk start states into a.hs and, with out, y and the final states (kda_ssm_fwd.cu)
-void launch_ssm_scan(const SsmArgs& a, int dtype, bool out, cudaStream_t st);
+// states into a.hs and, where given, y and the final states (kda_ssm_fwd.cu)
+void launch_ssm_scan(const SsmArgs& a, int dtype, cudaStream_t st);
 
 // backward from a.hs (kda_ssm_bwd.cu)
 struct SsmBwdPlan {
