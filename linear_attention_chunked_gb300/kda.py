@@ -393,10 +393,10 @@ def kda_conv_bwd(x, w, cu_seqlens, dy, *, bias=None, halo=None, activation=True,
     return out
 
 
-def _check_tensor(fn, name, t, shape, dtype, device, *, strided=False):
+def _check_tensor(fn, name, t, shape, dtype, device, strided=False):
     """A tensor handed to the library has the shape, type and device the call works on and dense
     rows; `strided` ones (views of a projection) may have any row stride."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     if t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
@@ -405,8 +405,12 @@ def _check_tensor(fn, name, t, shape, dtype, device, *, strided=False):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
-        inner = t[0] if strided and t.shape[0] else None
-        if inner is None or not inner.is_contiguous() or (t.shape[0] > 1 and t.stride(0) < inner.numel()):
+        dims, st, inner = t.shape, t.stride(), 1
+        rows = strided and t.numel() > 0
+        for k in range(t.dim() - 1, 0, -1):  # the inner dimensions lie dense
+            rows = rows and (dims[k] == 1 or st[k] == inner)
+            inner *= dims[k]
+        if not rows or (dims[0] > 1 and st[0] < inner):
             raise ValueError(f"{fn}: {name} has strides {t.stride()}, expected dense "
                              f"{'rows' if strided else 'storage'}")
 
@@ -425,6 +429,25 @@ def _slots(fn, slots, rows, pool, dev):
         _check_tensor(fn, "slots", slots, (rows,), torch.int32, dev)
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, dev, *args):
+    """Calls an entry point on dev's current stream.  A decode step is a handful of such calls of a
+    few microseconds each, so the device is only switched when it is not the current one."""
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: the tensors are on {dev}, expected a CUDA device")
+    f = getattr(_lib or lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != KDA_OK:
+        raise KdaError(fn, st)
+
+
 def kda_conv_tail(x, cu_seqlens, *, halo=None, tail=None):
     """The conv window that a prompt leaves: tail [N, 3, C] bf16, the three rows before each
     document's end (from halo [N, 3, C], or zero, where the document is shorter)."""
@@ -437,9 +460,7 @@ def kda_conv_tail(x, cu_seqlens, *, halo=None, tail=None):
     _check_tensor(fn, "halo", halo, (N, 3, C), torch.bfloat16, dev)
     _check_tensor(fn, "tail", tail, (N, 3, C), torch.bfloat16, dev)
     pr = make_conv_problem(T, N, C, cu_seqlens)
-    with torch.cuda.device(dev):
-        st = lib().kda_conv_tail(ctypes.byref(pr), _ptr(x), _ptr(halo), _ptr(tail), _stream(dev))
-    _check(fn, st)
+    _call(fn, dev, ctypes.byref(pr), x.data_ptr(), _at(halo), tail.data_ptr())
     return tail
 
 
@@ -456,19 +477,18 @@ def kda_conv_step(x, w, win, *, bias=None, activation=True, slots=None, out_dtyp
         win_out = win
     if y is None:
         y = torch.empty((N, C), dtype=out_dtype, device=dev)
+    else:
+        _check_tensor(fn, "y", y, (N, C), out_dtype, dev)
     _check_tensor(fn, "x", x, (N, C), torch.bfloat16, dev)
     _check_tensor(fn, "w", w, (C, 4), torch.float32, dev)
     _check_tensor(fn, "bias", bias, (C,), torch.float32, dev)
     _check_tensor(fn, "win", win, (win.shape[0], 3, C), torch.bfloat16, dev)
-    _check_tensor(fn, "win_out", win_out, win.shape, torch.bfloat16, dev)
-    _check_tensor(fn, "y", y, (N, C), out_dtype, dev)
+    if win_out is not win:
+        _check_tensor(fn, "win_out", win_out, win.shape, torch.bfloat16, dev)
     _slots(fn, slots, N, win.shape[0], dev)
     pr = make_conv_problem(N, N, C, activation=activation, out_dtype=out_dtype)
-    with torch.cuda.device(dev):
-        st = lib().kda_conv_step(ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(bias), _ptr(slots),
-                                 win.shape[0], _ptr(win), _ptr(win_out), _ptr(y), _ptr(ws),
-                                 _stream(dev))
-    _check(fn, st)
+    _call(fn, dev, ctypes.byref(pr), x.data_ptr(), w.data_ptr(), _at(bias), _at(slots), win.shape[0],
+          win.data_ptr(), win_out.data_ptr(), y.data_ptr(), _at(ws))
     return y, win_out
 
 
@@ -479,12 +499,12 @@ def _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens):
     G = B.shape[1] if B.dim() == 3 else 1
     if dtype not in _DTYPES:
         raise ValueError(f"{fn}: u is {dtype}, expected one of bfloat16, float16, float32")
-    _check_tensor(fn, "u", u, (T, ch), dtype, dev, strided=True)
-    _check_tensor(fn, "dt", dt, (T, ch), dtype, dev, strided=True)
-    _check_tensor(fn, "z", z, (T, ch), dtype, dev, strided=True)
+    _check_tensor(fn, "u", u, (T, ch), dtype, dev, True)
+    _check_tensor(fn, "dt", dt, (T, ch), dtype, dev, True)
+    _check_tensor(fn, "z", z, (T, ch), dtype, dev, True)
     bc = (T, G, S) if B.dim() == 3 else (T, S)
-    _check_tensor(fn, "B", B, bc, dtype, dev, strided=True)
-    _check_tensor(fn, "C", C, bc, dtype, dev, strided=True)
+    _check_tensor(fn, "B", B, bc, dtype, dev, True)
+    _check_tensor(fn, "C", C, bc, dtype, dev, True)
     _check_tensor(fn, "A", A, (ch, S), torch.float32, dev)
     _check_tensor(fn, "D", D, (ch,), torch.float32, dev)
     _check_tensor(fn, "dt_bias", dt_bias, (ch,), torch.float32, dev)
@@ -527,18 +547,18 @@ def kda_ssm_fwd(u, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, z=None, h0=
         saved = _empty_bytes(sv_b, dev)
     elif saved.numel() * saved.element_size() < sv_b:
         raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
-    if y is None:
-        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    if y is None:  # dense rows, whatever u's strides are
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+    else:
+        _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
     if ht is None:
         ht = torch.empty(state, dtype=torch.float32, device=dev)
-    _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
-    _check_tensor(fn, "ht", ht, state, torch.float32, dev)
+    else:
+        _check_tensor(fn, "ht", ht, state, torch.float32, dev)
     _check_tensor(fn, "h0", h0, state, torch.float32, dev)
-    with torch.cuda.device(dev):
-        st = lib().kda_ssm_fwd(ctypes.byref(pr), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                               _ptr(dt_bias), _ptr(z), _ptr(h0), _ptr(y), _ptr(ht), _ptr(saved),
-                               _ptr(ws), ws.numel(), _stream(dev))
-    _check(fn, st)
+    _call(fn, dev, ctypes.byref(pr), u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+          _at(D), _at(dt_bias), _at(z), _at(h0), y.data_ptr(), ht.data_ptr(), _at(saved), ws.data_ptr(),
+          ws.numel())
     return y, ht, saved
 
 
@@ -559,26 +579,22 @@ def kda_ssm_bwd(u, dt, A, B, C, cu_seqlens, dy, *, saved=None, D=None, dt_bias=N
         raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
     if ws is None:
         ws = _empty_bytes(ws_b, dev)
-    rows, par = dict(dtype=dtype, device=dev), dict(dtype=torch.float32, device=dev)
-    out = dict(du=torch.empty(u.shape, **rows), ddt=torch.empty(u.shape, **rows),
-               dA=torch.empty(A.shape, **par), dB=torch.empty(B.shape, **rows),
-               dC=torch.empty(B.shape, **rows))
+    # (like dy: dense rows whatever the inputs' strides are)
+    out = dict(du=torch.empty_like(dy), ddt=torch.empty_like(dy), dA=torch.empty_like(A),
+               dB=torch.empty(B.shape, dtype=dtype, device=dev),
+               dC=torch.empty(B.shape, dtype=dtype, device=dev))
     if D is not None:
-        out["dD"] = torch.empty(D.shape, **par)
+        out["dD"] = torch.empty_like(D)
     if dt_bias is not None:
-        out["ddt_bias"] = torch.empty(dt_bias.shape, **par)
+        out["ddt_bias"] = torch.empty_like(dt_bias)
     if z is not None:
-        out["dz"] = torch.empty(u.shape, **rows)
+        out["dz"] = torch.empty_like(dy)
     if want_dh0:
-        out["dh0"] = torch.empty(state, **par)
-    with torch.cuda.device(dev):
-        st = lib().kda_ssm_bwd(ctypes.byref(pr), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                               _ptr(dt_bias), _ptr(z), _ptr(h0), _ptr(dy), _ptr(dht), _ptr(saved),
-                               _ptr(out["du"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
-                               _ptr(out["dC"]), _ptr(out.get("dD")), _ptr(out.get("ddt_bias")),
-                               _ptr(out.get("dz")), _ptr(out.get("dh0")), _ptr(ws), ws.numel(),
-                               _stream(dev))
-    _check(fn, st)
+        out["dh0"] = torch.empty(state, dtype=torch.float32, device=dev)
+    _call(fn, dev, ctypes.byref(pr), u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+          _at(D), _at(dt_bias), _at(z), _at(h0), dy.data_ptr(), _at(dht), _at(saved),
+          *(_at(out.get(k)) for k in ("du", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dz", "dh0")),
+          ws.data_ptr(), ws.numel())
     return out
 
 
@@ -593,17 +609,17 @@ def kda_ssm_step(u, dt, A, B, C, h, *, D=None, dt_bias=None, z=None, softplus=Tr
     pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, None)
     if h_out is None:
         h_out = h
-    if y is None:
-        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    else:
+        _check_tensor(fn, "h_out", h_out, h.shape, torch.float32, dev)
+    if y is None:  # dense rows, whatever u's strides are
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+    else:
+        _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
     _check_tensor(fn, "h", h, (h.shape[0], pr.C, pr.S), torch.float32, dev)
-    _check_tensor(fn, "h_out", h_out, h.shape, torch.float32, dev)
-    _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
     _slots(fn, slots, N, h.shape[0], dev)
-    with torch.cuda.device(dev):
-        st = lib().kda_ssm_step(ctypes.byref(pr), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                _ptr(dt_bias), _ptr(z), _ptr(slots), h.shape[0], _ptr(h), _ptr(h_out),
-                                _ptr(y), _ptr(ws), _stream(dev))
-    _check(fn, st)
+    _call(fn, dev, ctypes.byref(pr), u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+          _at(D), _at(dt_bias), _at(z), _at(slots), h.shape[0], h.data_ptr(), h_out.data_ptr(),
+          y.data_ptr(), _at(ws))
     return y, h_out
 
 
@@ -631,23 +647,24 @@ def kda_layernorm_fwd(x, w=None, b=None, *, res=None, eps=1e-5, y=None, sum=None
     pr = _layernorm_problem(fn, x, eps)
     dev = x.device
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = torch.empty_like(x)
+    else:
+        _check_tensor(fn, "y", y, x.shape, x.dtype, dev)
     if res is None:
         if sum is not None:
             raise ValueError(f"{fn}: a sum needs a residual")
-    elif sum is None:
-        sum = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _check_tensor(fn, "res", res, x.shape, x.dtype, dev)
-    _check_tensor(fn, "sum", sum, x.shape, x.dtype, dev)
-    _check_tensor(fn, "y", y, x.shape, x.dtype, dev)
+    else:
+        _check_tensor(fn, "res", res, x.shape, x.dtype, dev)
+        if sum is None:
+            sum = torch.empty_like(x)
+        else:
+            _check_tensor(fn, "sum", sum, x.shape, x.dtype, dev)
     _check_tensor(fn, "w", w, (pr.C,), torch.float32, dev)
     _check_tensor(fn, "b", b, (pr.C,), torch.float32, dev)
     mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        st = lib().kda_layernorm_fwd(ctypes.byref(pr), _ptr(x), _ptr(res), _ptr(w), _ptr(b), _ptr(sum),
-                                     _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev))
-    _check(fn, st)
+    _call(fn, dev, ctypes.byref(pr), x.data_ptr(), _at(res), _at(w), _at(b), _at(sum), y.data_ptr(),
+          mean.data_ptr(), rstd.data_ptr())
     return y, x if res is None else sum, mean, rstd
 
 
@@ -664,14 +681,12 @@ def kda_layernorm_bwd(x, w, mean, rstd, dy, *, dsum=None, ws=None):
     _check_tensor(fn, "rstd", rstd, x.shape[:-1], torch.float32, dev)
     if ws is None:
         ws = _empty_bytes(kda_layernorm_workspace_size(pr.T, pr.C, dtype=x.dtype), dev)
-    out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev),
+    out = dict(dx=torch.empty_like(x),
                dw=torch.empty((pr.C,), dtype=torch.float32, device=dev),
                db=torch.empty((pr.C,), dtype=torch.float32, device=dev))
-    with torch.cuda.device(dev):
-        st = lib().kda_layernorm_bwd(ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dy),
-                                     _ptr(dsum), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["db"]),
-                                     _ptr(ws), ws.numel(), _stream(dev))
-    _check(fn, st)
+    _call(fn, dev, ctypes.byref(pr), x.data_ptr(), _at(w), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
+          _at(dsum), out["dx"].data_ptr(), out["dw"].data_ptr(), out["db"].data_ptr(), ws.data_ptr(),
+          ws.numel())
     return out
 
 
