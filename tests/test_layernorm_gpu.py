@@ -57,6 +57,30 @@ def test_layernorm(shape, dtype):
             assert all(torch.equal(again[k], g[k]) for k in g)
 
 
+# more rows than the machine holds at once: blocks walk several rows (a row count that leaves a last
+# step short), for a warp, 128, 256 and 512 threads a row, one, two and four vectors a thread
+@pytest.mark.parametrize("dtype,T,C", [("bf16", 9999, 136), ("fp32", 9731, 200), ("fp16", 7500, 1000), ("bf16", 2501, 1032),
+                                       ("fp32", 2437, 1024), ("bf16", 2000, 4096), ("bf16", 701, 8192), ("fp32", 1300, 2048),
+                                       ("fp32", 613, 4096), ("bf16", 611, 16384), ("fp32", 620, 8192), ("bf16", 1500, 3001)])
+def test_layernorm_many_rows(dtype, T, C):
+    gen, dt = torch.Generator("cuda").manual_seed(T), DT[dtype]
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, r, dy, ds = ((2 * rn(T, C) + 0.5).to(dt), rn(T, C).to(dt), rn(T, C).to(dt), rn(T, C).to(dt))
+    w, b = 1 + 0.1 * rn(C), 0.1 * rn(C)
+    for res, dsum in ((None, None), (r, ds)):
+        y, total, mean, rstd = kda.kda_layernorm_fwd(x, w, b, res=res)
+        if res is not None:
+            assert torch.equal(total, (x.float() + r.float()).to(dt))
+        yr, mr, rr = layernorm.layernorm_fwd(_np(total), _np(w), _np(b))
+        _close("y", y, yr, TOL)
+        _close("mean", mean, mr, TOL)
+        _close("rstd", rstd, rr, TOL)
+        g = kda.kda_layernorm_bwd(total, w, mean, rstd, dy, dsum=dsum)
+        ref = layernorm.layernorm_bwd(_np(total), _np(dy), _np(w), _np(dsum))
+        for k in g:
+            _close(k, g[k], ref[k], TOL)
+
+
 def test_large_offset_keeps_the_variance():
     # variance about the mean, not E[v^2] - mean^2: rows at 1000 with unit spread (the inputs' own fp32
     # rounding is part of the reference's input; subtracting the mean costs 1000 2^-24 of a unit)
