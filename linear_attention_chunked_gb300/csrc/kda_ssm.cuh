@@ -38,6 +38,7 @@ struct SsmArgs {
     float* hs;        // [maxC][sub][C][S] states at the chunks' starts (a document's first chunk: h0)
                       // and, with sub = SSM_SUB, at every SSM_UT-th token (the backward's set)
     int sub;
+    int direct;  // every document fits one chunk: no plan, no carry
     float* gs;        // [maxC][C][S] gradient of the state at each chunk's end (last chunk: dht)
     float* pBC;       // [channel blocks][T][2 S] partial sums of dB and dC
     float* pA;        // [maxC][C][S + 2] partial sums of dA, dD, dbias
@@ -122,20 +123,44 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ float ssm_sigmoid(float z) { return rcp(1.f + ex2(-LOG2E * z)); }
 // z sigmoid(z).  Past z = -87 the divisor leaves the range of its reciprocal: the limit there is 0
 __device__ __forceinline__ float ssm_silu(float z) {
-    return z * (z < -87.f ? 0.f : rcp(1.f + ex2(-LOG2E * z)));
+    return __fmul_rn(z, z < -87.f ? 0.f : rcp(__fadd_rn(1.f, ex2(-LOG2E * z))));
 }
 
-// softplus(x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], with log1p(u) = 2 atanh(u / (2 + u)) as its
-// odd series (argument at most 1/3: the terms past the 13th power are below 1e-7 of the sum)
+__device__ __forceinline__ f2 ssm_silu2(f2 z) {
+    float x, y;
+    up2(z, x, y);
+    const f2 e = mul2(z, pk2(-LOG2E, -LOG2E));
+    float p, q;
+    up2(e, p, q);
+    up2(add2(pk2(ex2(p), ex2(q)), pk2(1.f, 1.f)), p, q);
+    return mul2(z, pk2(x < -87.f ? 0.f : rcp(p), y < -87.f ? 0.f : rcp(q)));
+}
+
+// softplus(x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], with log1p(u) = 2 atanh(z), z = u / (2 + u) in
+// (0, 1/3].  2 atanh(z) / z is a polynomial in z^2 (its minimax fit on [0, 1/9] by Remez exchange:
+// relative error 4e-9, below fp32's rounding).  Two values at a time.
+__device__ __forceinline__ f2 ssm_delta2(f2 raw, int softplus) {
+    if (!softplus) return raw;
+    float x, y;
+    up2(raw, x, y);
+    const f2 u = pk2(ex2(-LOG2E * fabsf(x)), ex2(-LOG2E * fabsf(y)));
+    float d, e;
+    up2(add2(u, pk2(2.f, 2.f)), d, e);
+    const f2 z = mul2(u, pk2(rcp(d), rcp(e))), z2 = mul2(z, z);
+    f2 p = fma2(z2, pk2(0.28178334f, 0.28178334f), pk2(0.279606f, 0.279606f));
+    p = fma2(z2, p, pk2(0.4002491f, 0.4002491f));
+    p = fma2(z2, p, pk2(0.66666317f, 0.66666317f));
+    p = fma2(z2, p, pk2(2.f, 2.f));
+    return fma2(z, p, pk2(fmaxf(x, 0.f), fmaxf(y, 0.f)));
+}
+// one value (the same operations)
 __device__ __forceinline__ float ssm_delta(float raw, int softplus) {
     if (!softplus) return raw;
     const float u = ex2(-LOG2E * fabsf(raw));
-    const float z = u * rcp(2.f + u), z2 = z * z;
-    float p = fmaf(z2, 2.f / 13.f, 2.f / 11.f);
-    p = fmaf(z2, p, 2.f / 9.f);
-    p = fmaf(z2, p, 2.f / 7.f);
-    p = fmaf(z2, p, 2.f / 5.f);
-    p = fmaf(z2, p, 2.f / 3.f);
+    const float z = __fmul_rn(u, rcp(__fadd_rn(u, 2.f))), z2 = __fmul_rn(z, z);
+    float p = fmaf(z2, 0.28178334f, 0.279606f);
+    p = fmaf(z2, p, 0.4002491f);
+    p = fmaf(z2, p, 0.66666317f);
     p = fmaf(z2, p, 2.f);
     return fmaf(z, p, fmaxf(raw, 0.f));
 }
@@ -148,32 +173,22 @@ template <class E> __device__ __forceinline__ float ssm_f(E v) { return ssm_ld<E
 template <class E, int SP, int NTH = SSM_THREADS>
 __device__ __forceinline__ void ssm_load_rows(float* s, const void* g, int64_t ld, int64_t t0,
                                               int len, int col0, int S) {
-    for (int i = threadIdx.x; i < CH * SP; i += NTH) {
-        const int r = i / SP, k = i % SP;
-        s[i] = r < len && k < S ? ssm_ld<E>(g, (t0 + r) * ld + col0 + k) : 0.f;
+    constexpr int N = CH * SP / NTH, U = N < 8 ? N : 8;  // loads of a thread, in flight together
+    const E* p = static_cast<const E*>(g) + t0 * ld + col0;
+#pragma unroll
+    for (int j = 0; j < N; j += U) {
+        E raw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int e = threadIdx.x + (j + i) * NTH, r = e / SP, k = e % SP;
+            if (r < len && k < S) raw[i] = p[r * ld + k];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int e = threadIdx.x + (j + i) * NTH, r = e / SP, k = e % SP;
+            s[e] = r < len && k < S ? ssm_f<E>(raw[i]) : 0.f;
+        }
     }
 }
-
-// Rows of one channel, read GR tokens ahead of their use.  The rows past the chunk's end repeat its
-// last one.
-template <class E, int GR>
-struct Ahead {
-    const E* p;  // the next group's first row
-    int64_t ld;
-    E raw[GR];
-    __device__ __forceinline__ Ahead(const void* base, int64_t row, int64_t ld_, int c)
-        : p(static_cast<const E*>(base) + row * ld_ + c), ld(ld_) {}
-    // left: rows from the group's first to the chunk's end
-    __device__ __forceinline__ void load(int left) {
-        if (left >= GR) {
-#pragma unroll
-            for (int i = 0; i < GR; ++i) raw[i] = p[i * ld];
-        } else {
-#pragma unroll
-            for (int i = 0; i < GR; ++i) raw[i] = p[min(i, left - 1) * ld];
-        }
-        p += GR * ld;
-    }
-};
 
 }  // namespace kda

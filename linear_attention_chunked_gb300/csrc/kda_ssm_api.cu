@@ -175,7 +175,9 @@ kda_status kda_ssm_fwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     a.ht = ht;
     a.hs = static_cast<float*>(saved ? saved : static_cast<char*>(ws) + r.head);
     a.sub = saved ? SSM_SUB : 1;
-    launch_plan(a, r, ws, st);
+    // a short prompt (every document within one chunk, few of them): one launch, no plan, no carry
+    a.direct = !saved && a.T <= CH && a.N <= 64;
+    if (!a.direct) launch_plan(a, r, ws, st);
     launch_ssm_scan(a, p->dtype, st);
     return launched();
 }

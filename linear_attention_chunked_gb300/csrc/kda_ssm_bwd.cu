@@ -5,8 +5,7 @@
 //   dA = sum_t delta w,  dD = sum_t dY u,  ddt = ddelta softplus'(dt + bias),  dbias = sum_t ddt
 //   dz = dy y0 silu'(z),  y0 = sum_s C h + D u,  dh0 = a_1 G_1
 //
-//   k_ssm_rstate   per chunk with a predecessor: its start gradient from a zero end,
-//                  sum_t exp(A (delta_1 + .. + delta_t)) C_t dY_t, and sum(delta)
+//   k_ssm_rstate   per chunk with a predecessor: its start gradient from a zero end (kda_ssm_fwd.cu)
 //   k_ssm_rcarry   per (document, channel, state): the chunks' end gradients, last to first
 //   k_ssm_bwd      per (chunk, channel tile): the gradients
 //   k_ssm_reduce_* the sums over channel tiles (dB, dC) and over chunks (dA, dD, dbias), in order
@@ -43,86 +42,6 @@ __device__ __forceinline__ void st4(float* p, int s, int S, float4 v) {
     if (s + 1 < S) p[s + 1] = v.y;
     if (s + 2 < S) p[s + 2] = v.z;
     if (s + 3 < S) p[s + 3] = v.w;
-}
-
-// ---- gradient at a chunk's start from a zero end ----
-
-template <class E, int SPTR, int P>
-__global__ void __launch_bounds__(SSM_THREADS) k_ssm_rstate(SsmArgs a, int tiles) {
-    constexpr int SP = SPTR * P, H2 = SPTR / 2, CB = SSM_THREADS / P, CW = 32 / P, GR = 8;
-    __shared__ __align__(16) float sC[CH * SP];
-    const int k = blockIdx.x / tiles;
-    if (k >= *a.nchunks) return;
-    const int4 t = a.chunk_tab[k];
-    if (t.w == 0) return;  // no predecessor
-    const int len = t.z;
-    const int Cg = a.C / a.G, tg = (Cg + CB - 1) / CB, tile = blockIdx.x % tiles, g = tile / tg;
-    const int lane = threadIdx.x & 31;
-    const int ci = (tile - g * tg) * CB + (threadIdx.x >> 5) * CW + lane % CW;
-    const bool on = ci < Cg;
-    const int c = g * Cg + (on ? ci : Cg - 1), s0 = lane / CW * SPTR;
-    ssm_load_rows<E, SP>(sC, a.Cm, a.ldc, t.y, len, g * a.S, a.S);
-    f2 A2[H2], acc[H2];
-#pragma unroll
-    for (int j = 0; j < H2; ++j) {
-        const int s = s0 + 2 * j;
-        const float* row = a.A + int64_t(c) * a.S;
-        A2[j] = pk2(s < a.S ? LOG2E * row[s] : 0.f, s + 1 < a.S ? LOG2E * row[s + 1] : 0.f);
-        acc[j] = 0;
-    }
-    const float bias = a.bias ? a.bias[c] : 0.f;
-    const bool gated = a.z;
-    float sum = 0.f;
-    Ahead<E, GR> d(a.dt, t.y, a.lddt, c), z(a.z, t.y, a.ldz, c), g_(a.dy, t.y, a.C, c);
-    d.load(len);
-    g_.load(len);
-    if (gated) z.load(len);
-    __syncthreads();
-    E cd[GR], cy[GR], cz[GR];
-    auto token = [&](int q, int i) {
-        sum += ssm_delta(ssm_f<E>(cd[i]) + bias, a.softplus);
-        float dY = ssm_f<E>(cy[i]);
-        if (gated) dY *= ssm_silu(ssm_f<E>(cz[i]));
-        const f2 s2 = pk2(sum, sum), d2 = pk2(dY, dY);
-        const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(sC + (q + i) * SP + s0);
-#pragma unroll
-        for (int j = 0; j < H2; j += 2) {
-            const ulonglong2 c2 = Cp[j / 2];
-            acc[j] = fma2(ex2_2(mul2(A2[j], s2)), mul2(c2.x, d2), acc[j]);
-            acc[j + 1] = fma2(ex2_2(mul2(A2[j + 1], s2)), mul2(c2.y, d2), acc[j + 1]);
-        }
-    };
-#pragma unroll 1
-    for (int q = 0; q < len; q += GR) {
-#pragma unroll
-        for (int i = 0; i < GR; ++i) {
-            cd[i] = d.raw[i], cy[i] = g_.raw[i];
-            if (gated) cz[i] = z.raw[i];
-        }
-        if (q + GR < len) {
-            d.load(len - q - GR);
-            g_.load(len - q - GR);
-            if (gated) z.load(len - q - GR);
-        }
-        if (q + GR <= len) {
-#pragma unroll
-            for (int i = 0; i < GR; ++i) token(q, i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < GR - 1; ++i)
-                if (q + i < len) token(q, i);
-        }
-    }
-    if (!on) return;
-    if (s0 == 0) a.sumdt[int64_t(k) * a.C + c] = sum;
-    float* out = a.gs + (int64_t(k - 1) * a.C + c) * a.S;  // the chunk before: its end
-#pragma unroll
-    for (int j = 0; j < H2; ++j) {
-        float x, y;
-        up2(acc[j], x, y);
-        if (s0 + 2 * j < a.S) out[s0 + 2 * j] = x;
-        if (s0 + 2 * j + 1 < a.S) out[s0 + 2 * j + 1] = y;
-    }
 }
 
 constexpr int CARRY_THREADS = 128;
@@ -523,19 +442,6 @@ __global__ void k_ssm_reduce_par(SsmArgs a) {
     else if (a.dbias) a.dbias[c] = sum;
 }
 
-template <class E, int SPTR, int P>
-void launch_rstate(const SsmArgs& a, cudaStream_t st) {
-    const int Cg = a.C / a.G, CB = SSM_THREADS / P, tiles = a.G * ((Cg + CB - 1) / CB);
-    if (a.T > CH) {
-        ProfScope ps(KK_SSM_RSTATE, st);
-        k_ssm_rstate<E, SPTR, P><<<unsigned(a.maxC * tiles), SSM_THREADS, 0, st>>>(a, tiles);
-    }
-    ProfScope ps(KK_SSM_RCARRY, st);
-    const int64_t CS = int64_t(a.C) * a.S;
-    const int bpd = int((CS + CARRY_THREADS - 1) / CARRY_THREADS);
-    k_ssm_rcarry<<<unsigned(int64_t(bpd) * a.N), CARRY_THREADS, 0, st>>>(a, bpd);
-}
-
 template <class E, int P>
 void launch_main(const SsmArgs& a, const SsmBwdPlan& pl, cudaStream_t st) {
     const unsigned grid = unsigned(a.maxC * a.G * pl.splits);
@@ -557,10 +463,6 @@ void launch_main(const SsmArgs& a, const SsmBwdPlan& pl, cudaStream_t st) {
 
 template <class E>
 void launch_e(const SsmArgs& a, cudaStream_t st) {
-    if (a.S <= 8) launch_rstate<E, 8, 1>(a, st);
-    else if (a.S <= 16) launch_rstate<E, 16, 1>(a, st);
-    else if (a.S <= 32) launch_rstate<E, 16, 2>(a, st);
-    else launch_rstate<E, 16, 4>(a, st);
     const SsmBwdPlan pl = ssm_bwd_plan(a.maxC, a.C, a.S, a.G);
     switch (pl.lanes) {
         case 1: return launch_main<E, 1>(a, pl, st);
@@ -604,6 +506,13 @@ cudaError_t ssm_bwd_setup() {
 }
 
 void launch_ssm_bwd(const SsmArgs& a, int dtype, cudaStream_t st) {
+    launch_ssm_rstate(a, dtype, st);
+    {
+        ProfScope ps(KK_SSM_RCARRY, st);
+        const int64_t CS = int64_t(a.C) * a.S;
+        const int bpd = int((CS + CARRY_THREADS - 1) / CARRY_THREADS);
+        k_ssm_rcarry<<<unsigned(int64_t(bpd) * a.N), CARRY_THREADS, 0, st>>>(a, bpd);
+    }
     if (dtype == KDA_DT_BF16) launch_e<__nv_bfloat16>(a, st);
     else if (dtype == KDA_DT_FP16) launch_e<__half>(a, st);
     else launch_e<float>(a, st);

@@ -7,6 +7,8 @@ namespace kda {
 
 // states into a.hs and, where given, y and the final states (kda_ssm_fwd.cu)
 void launch_ssm_scan(const SsmArgs& a, int dtype, cudaStream_t st);
+// the chunks' start gradients from zero ends into a.gs
+void launch_ssm_rstate(const SsmArgs& a, int dtype, cudaStream_t st);
 
 // backward from a.hs (kda_ssm_bwd.cu)
 struct SsmBwdPlan {
