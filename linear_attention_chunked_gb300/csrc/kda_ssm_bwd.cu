@@ -14,11 +14,12 @@
 // tokens is swept forward once from there, the states every 4 tokens kept in shared memory, and
 // each run of 4 tokens is recomputed from its start with states and decays in registers and walked
 // backwards.  Four lanes hold a channel's 16 states (four each), a warp 16 channels in two passes.
-// The channels' scalars (delta, delta u, dY) are computed once per token by lanes laid out as
-// channels and handed over through shared memory, one unit ahead of their use; the sums over a
-// channel's states go back the same way.  A lane's eight dB / dC terms per token are summed over
-// the two passes in registers before they cross lanes, and cross them by halving (each step a lane
-// gives away half of its values): 7 shuffles for 8 values over 8 lanes.
+// The channels' scalars (delta, delta u, dY, u and what the gradients are multiplied with at the end) are
+// computed once per token by lanes laid out as (token, channel) items and handed over through shared
+// memory, one unit ahead of their use.  Sums cross lanes by halving (each step a lane gives away half
+// of its values): a channel's three sums over states for 4 tokens leave each of its four lanes with one
+// token, whose du, ddt and dz that lane finishes; the eight dB / dC terms per token, summed over the two
+// passes in registers first, take 7 shuffles over 8 lanes.
 #include "kda_ssm.cuh"
 #include "kda_ssm_launch.cuh"
 
@@ -117,6 +118,32 @@ __device__ __forceinline__ int reduce_index(int lane) {
     return idx;
 }
 
+// Sums of a run's three values per token over the P lanes of a channel, halving over the tokens: on return
+// a lane holds its tokens' sums in v[.][0 .. NT-1], the first of them token first_token(p).
+template <int P> __device__ constexpr int lane_tokens() { return P == 1 ? 4 : P == 2 ? 2 : 1; }
+template <int P> __device__ __forceinline__ int first_token(int p) {
+    return (P > 1 && (p & 1) ? 2 : 0) + (P > 2 && (p & 2) ? 1 : 0);
+}
+template <int P>
+__device__ __forceinline__ void reduce_tokens(float (&v)[3][RT], int p) {
+    static_assert(RT == 4, "two halvings");
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        if (P > 1)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float give = p & 1 ? v[x][i] : v[x][i + 2], keep = p & 1 ? v[x][i + 2] : v[x][i];
+                v[x][i] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+            }
+        if (P > 2) {
+            const float give = p & 2 ? v[x][0] : v[x][1], keep = p & 2 ? v[x][1] : v[x][0];
+            v[x][0] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+        }
+#pragma unroll
+        for (int o = 4; o < P; o <<= 1) v[x][0] += __shfl_xor_sync(0xffffffffu, v[x][0], o);
+    }
+}
+
 template <int P>
 struct BwdShape {
     static constexpr int CL = 32 / P;       // channels of a pass
@@ -126,16 +153,16 @@ struct BwdShape {
     static constexpr int NI = RT * CW > 32 ? RT * CW / 32 : 1;  // (token, channel) items of a run per lane
     // shared memory, in floats
     static constexpr int oB = 0, oC = oB + CH * SP, oPre = oC + CH * SP;
-    static constexpr int oCk = oPre + 2 * NW * UT * CW * 4;
-    static constexpr int oSum = oCk + (NR - 1) * NP * SSM_THREADS * 4;
-    static constexpr int oRed = oSum + NW * RT * CW * P * 4;
+    static constexpr int oFin = oPre + 2 * NW * UT * CW * 4;
+    static constexpr int oCk = oFin + 2 * NW * UT * CW * 2;
+    static constexpr int oRed = oCk + (NR - 1) * NP * SSM_THREADS * 4;
     static constexpr int floats = oRed + 2 * NW * RT * 2 * SP;
 };
 
 template <class E, int P>
 __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
     using L = BwdShape<P>;
-    constexpr int CL = L::CL, CW = L::CW, SP = L::SP, NI = L::NI, NB = CW > 32 ? 2 : 1;
+    constexpr int CL = L::CL, CW = L::CW, SP = L::SP, NI = L::NI, NB = CW > 32 ? 2 : 1, LT = lane_tokens<P>();
     extern __shared__ __align__(16) float sm[];
     const int per_chunk = a.G * pl.splits;
     const int k = blockIdx.x / per_chunk;
@@ -147,10 +174,10 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int p = lane % P, cl = lane / P, s0 = SPT * p;
     float *sB = sm + L::oB, *sC = sm + L::oC;
-    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * 2 * UT * CW;    // [buffer][token][channel]
-    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;          // [run][pass], stride 128
-    float4* part = reinterpret_cast<float4*>(sm + L::oSum) + w * RT * CW * P;   // [token][channel][lane]
-    float* red = sm + L::oRed;                                                  // [parity][warp][token][2 SP]
+    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * 2 * UT * CW;  // [buffer][token][channel]: delta, delta u, dY, u
+    float2* fin = reinterpret_cast<float2*>(sm + L::oFin) + w * 2 * UT * CW;  // d delta / d dt, dz / y0
+    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;        // [run][pass], stride 128
+    float* red = sm + L::oRed;                                                // [parity][warp][token][2 SP]
     ssm_load_rows<E, SP>(sB, a.B, a.ldb, t0, len, g_ * S, S);
     ssm_load_rows<E, SP>(sC, a.Cm, a.ldc, t0, len, g_ * S, S);
     __syncthreads();
@@ -166,6 +193,7 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
         // lanes as states: pass q's channel.  Lanes past the group's channels stay zero: they add
         // nothing to dB and dC
         f2 A2[NP][2], g[NP][2], dA[NP][2], hs[NP][2];
+        float skip[NP], accD[NP] = {}, accb[NP] = {};
         auto lim = [&](int q) { return cw + q * CL + cl < Cg ? S : 0; };
         auto pair2 = [](float4 v, f2(&o)[2]) { o[0] = pk2(v.x, v.y), o[1] = pk2(v.z, v.w); };
         auto start = [&](int u, int q) {  // the state at unit u's start
@@ -181,45 +209,53 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
             pair2(ld4(a.gs + int64_t(k) * a.C * S + row, s0, lim(q)), g[q]);
             dA[q][0] = dA[q][1] = 0;
             nh[q] = start(nu - 1, q);
+            skip[q] = a.D ? a.D[chan(q * CL + cl)] : 0.f;
         }
         // lanes as (token, channel) items of a run: item x is token (lane + 32 x) / CW of the run and
         // channel (lane + 32 x) % CW of the warp
-        float bias[NB], skip[NB], accD[NB] = {}, accb[NB] = {};
+        float bias[NB];
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-            const int c = chan(lane % CW + 32 * x);
-            bias[x] = a.bias ? a.bias[c] : 0.f;
-            skip[x] = a.D ? a.D[c] : 0.f;
-        }
+        for (int x = 0; x < NB; ++x) bias[x] = a.bias ? a.bias[chan(lane % CW + 32 * x)] : 0.f;
         struct Raw { E dt, u, dy, z; };
+        auto at = [&](const void* base, int64_t ld, int row, int c) {
+            return static_cast<const E*>(base)[(int64_t(t0) + row) * ld + c];
+        };
         auto fetch = [&](Raw(&r)[NI], int row0) {
 #pragma unroll
             for (int x = 0; x < NI; ++x) {
-                const int i = lane + 32 * x, c = chan(i % CW);
-                const int64_t t = t0 + min(row0 + i / CW, len - 1);
-                r[x].dt = static_cast<const E*>(a.dt)[t * a.lddt + c];
-                r[x].u = static_cast<const E*>(a.u)[t * a.ldu + c];
-                r[x].dy = static_cast<const E*>(a.dy)[t * a.C + c];
-                if (gated) r[x].z = static_cast<const E*>(a.z)[t * a.ldz + c];
+                const int i = lane + 32 * x, c = chan(i % CW), row = min(row0 + i / CW, len - 1);
+                r[x].dt = at(a.dt, a.lddt, row, c);
+                r[x].u = at(a.u, a.ldu, row, c);
+                r[x].dy = at(a.dy, a.C, row, c);
+                if (gated) r[x].z = at(a.z, a.ldz, row, c);
             }
         };
-        // delta, delta u and dY of a run into a unit's buffer; tokens past the chunk are the identity step
+        // the scalars of a run into a unit's buffer; tokens past the chunk are the identity step
         auto stage = [&](const Raw(&r)[NI], int u, int run) {
 #pragma unroll
             for (int x = 0; x < NI; ++x) {
                 const int i = lane + 32 * x;
                 if (RT * CW < 32 && i >= RT * CW) break;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                float2 f = make_float2(0.f, 0.f);
                 if (u * UT + run * RT + i / CW < len && cw + i % CW < Cg) {
-                    v.x = ssm_delta(ssm_f<E>(r[x].dt) + bias[x % NB], a.softplus);
-                    v.y = v.x * ssm_f<E>(r[x].u);
+                    const float raw = __fadd_rn(ssm_f<E>(r[x].dt), bias[x % NB]);
+                    v.x = ssm_delta(raw, a.softplus);
+                    v.w = ssm_f<E>(r[x].u);
+                    v.y = __fmul_rn(v.x, v.w);
                     v.z = ssm_f<E>(r[x].dy);
-                    if (gated) v.z *= ssm_silu(ssm_f<E>(r[x].z));
+                    f.x = a.softplus ? ssm_sigmoid(raw) : 1.f;
+                    if (gated) {
+                        const float z = ssm_f<E>(r[x].z), sg = z < -87.f ? 0.f : ssm_sigmoid(z), zs = z * sg;
+                        f.y = v.z * fmaf(zs, 1.f - sg, sg);  // silu'(z) = sg + z sg (1 - sg)
+                        v.z = __fmul_rn(v.z, zs);
+                    }
                 }
                 pre[((u & 1) * UT + run * RT) * CW + i] = v;
+                fin[((u & 1) * UT + run * RT) * CW + i] = f;
             }
         };
-        Raw nxt[NI], cur[NI];
+        Raw nxt[NI];
 #pragma unroll 1
         for (int r = 0; r < NR; ++r) {
             fetch(nxt, (nu - 1) * UT + r * RT);
@@ -228,6 +264,7 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
 #pragma unroll 1
         for (int u = nu - 1; u >= 0; --u) {
             const float4* pu = pre + (u & 1) * UT * CW + cl;
+            const float2* fu = fin + (u & 1) * UT * CW + cl;
             const int nr = (min(UT, len - u * UT) + RT - 1) / RT;  // runs of the unit
             __syncwarp();
 #pragma unroll
@@ -262,7 +299,6 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
             for (int r = nr - 1; r >= 0; --r) {
                 const int row0 = u * UT + r * RT;
                 if (u > 0) fetch(nxt, row0 - UT);
-                fetch(cur, row0);
                 f2 bc[RT][4];  // dB, dC of the run's tokens, summed over the passes
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
@@ -287,6 +323,7 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
                         h[i + 1][0] = fma2(dec[i][0], h[i][0], mul2(b2.x, u2));
                         h[i + 1][1] = fma2(dec[i][1], h[i][1], mul2(b2.y, u2));
                     }
+                    float sums[3][RT];  // over the states: G B, log2(e) A w, C h
 #pragma unroll
                     for (int i = RT - 1; i >= 0; --i) {
                         const float4 v = pq[i * CW];
@@ -298,16 +335,32 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
                         bc[i][1] = fma2(G1, u2, bc[i][1]);
                         bc[i][2] = fma2(h[i + 1][0], y2, bc[i][2]);
                         bc[i][3] = fma2(h[i + 1][1], y2, bc[i][3]);
-                        const f2 xB = fma2(G1, b2.y, mul2(G0, b2.x));
-                        const f2 xy = fma2(h[i + 1][1], c2.y, mul2(h[i + 1][0], c2.x));
+                        sums[0][i] = hsum2(fma2(G1, b2.y, mul2(G0, b2.x)));
+                        sums[2][i] = hsum2(fma2(h[i + 1][1], c2.y, mul2(h[i + 1][0], c2.x)));
                         g[q][0] = mul2(dec[i][0], G0);
                         g[q][1] = mul2(dec[i][1], G1);
                         const f2 w0 = mul2(g[q][0], h[i][0]), w1 = mul2(g[q][1], h[i][1]);
-                        const f2 xw = fma2(w1, A2[q][1], mul2(w0, A2[q][0]));
+                        sums[1][i] = hsum2(fma2(w1, A2[q][1], mul2(w0, A2[q][0])));
                         dA[q][0] = fma2(w0, d2, dA[q][0]);
                         dA[q][1] = fma2(w1, d2, dA[q][1]);
-                        part[(i * CW + q * CL) * P + lane] = make_float4(hsum2(xB), hsum2(xw), hsum2(xy), 0.f);
                     }
+                    reduce_tokens<P>(sums, p);
+                    if (P <= 4 || p < 4)
+#pragma unroll
+                        for (int i = 0; i < LT; ++i) {
+                            const int tk = first_token<P>(p) + i, row = row0 + tk, ci = cw + q * CL + cl;
+                            if (row < len && ci < Cg) {
+                                const int64_t o = (int64_t(t0) + row) * a.C + g_ * Cg + ci;
+                                const float4 v = pq[tk * CW];
+                                const float2 f = fu[(r * RT + tk) * CW + q * CL];
+                                const float dd = fmaf(v.w, sums[0][i], sums[1][i] * 0.6931471805599453f) * f.x;
+                                ssm_st<E>(a.du, o, fmaf(v.x, sums[0][i], skip[q] * v.z));
+                                ssm_st<E>(a.ddt, o, dd);
+                                if (gated) ssm_st<E>(a.dz, o, f.y * fmaf(skip[q], v.w, sums[2][i]));
+                                accD[q] = fmaf(v.z, v.w, accD[q]);
+                                accb[q] += dd;
+                            }
+                        }
                 }
                 // dB, dC of the run over the warp's channels
 #pragma unroll
@@ -323,33 +376,6 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
                     for (int j = 0; j < n; ++j) {
                         const int vi = idx + j;  // 0 .. 3: dB, 4 .. 7: dC
                         red[((par * NW + w) * RT + i) * 2 * SP + (vi / SPT) * SP + s0 + vi % SPT] = v[j];
-                    }
-                }
-                __syncwarp();
-                // the run's du, ddt, dz, and the next unit's scalars: lanes are channels
-#pragma unroll
-                for (int x = 0; x < NI; ++x) {
-                    const int i = lane + 32 * x, row = row0 + i / CW;
-                    if (row < len && cw + i % CW < Cg && (RT * CW >= 32 || i < RT * CW)) {
-                        float sB_ = 0.f, sw = 0.f, sy = 0.f;  // sum G B, log2(e) sum A w, sum C h
-#pragma unroll
-                        for (int j = 0; j < P; ++j) {
-                            const float4 v = part[i * P + j];
-                            sB_ += v.x, sw += v.y, sy += v.z;
-                        }
-                        const int64_t o = (int64_t(t0) + row) * a.C + g_ * Cg + cw + i % CW;
-                        const float4 v = pre[((u & 1) * UT + r * RT) * CW + i];  // delta, delta u, dY
-                        const float ux = ssm_f<E>(cur[x].u), sk = skip[x % NB];
-                        if (gated) {
-                            const float z = ssm_f<E>(cur[x].z), sg = ssm_sigmoid(z);
-                            ssm_st<E>(a.dz, o, ssm_f<E>(cur[x].dy) * fmaf(sk, ux, sy) * sg * fmaf(z, 1.f - sg, 1.f));
-                        }
-                        ssm_st<E>(a.du, o, fmaf(v.x, sB_, sk * v.z));
-                        float dd = fmaf(ux, sB_, sw * 0.6931471805599453f);
-                        if (a.softplus) dd *= ssm_sigmoid(ssm_f<E>(cur[x].dt) + bias[x % NB]);
-                        ssm_st<E>(a.ddt, o, dd);
-                        accD[x % NB] = fmaf(v.z, ux, accD[x % NB]);
-                        accb[x % NB] += dd;
                     }
                 }
                 if (u > 0) stage(nxt, u - 1, r);
@@ -371,31 +397,24 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
         }
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
+            // the channel's lanes hold its tokens' terms of dD and dbias
+#pragma unroll
+            for (int o = 1; o < P; o <<= 1) {
+                accD[q] += __shfl_xor_sync(0xffffffffu, accD[q], o);
+                accb[q] += __shfl_xor_sync(0xffffffffu, accb[q], o);
+            }
             const int ci = cw + q * CL + cl;
             if (ci < Cg) {
                 const int c = g_ * Cg + ci;
+                float* row = a.pA + (int64_t(k) * a.C + c) * (S + 2);
                 float4 v;
                 up2(dA[q][0], v.x, v.y);
                 up2(dA[q][1], v.z, v.w);
-                st4(a.pA + (int64_t(k) * a.C + c) * (S + 2), s0, S, v);
+                st4(row, s0, S, v);
+                if (p == 0) row[S] = accD[q], row[S + 1] = accb[q];
                 up2(g[q][0], v.x, v.y);
                 up2(g[q][1], v.z, v.w);
                 if (a.dh0 && tab.w == 0) st4(a.dh0 + (int64_t(tab.x) * a.C + c) * S, s0, S, v);
-            }
-        }
-        // lanes that share a channel hold its tokens' terms of dD and dbias
-#pragma unroll
-        for (int x = 0; x < NB; ++x) {
-#pragma unroll
-            for (int o = CW; o < 32; o <<= 1) {
-                accD[x] += __shfl_xor_sync(0xffffffffu, accD[x], o);
-                accb[x] += __shfl_xor_sync(0xffffffffu, accb[x], o);
-            }
-            const int ci = cw + lane % CW + 32 * x;
-            if (ci < Cg && lane < CW) {
-                float* o = a.pA + (int64_t(k) * a.C + g_ * Cg + ci) * (S + 2) + S;
-                o[0] = accD[x];
-                o[1] = accb[x];
             }
         }
         __syncwarp();
