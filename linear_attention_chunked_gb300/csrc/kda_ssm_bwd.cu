@@ -27,6 +27,9 @@ namespace kda {
 
 namespace {
 
+#ifndef BB
+#define BB (P <= 4 ? 3 : 2)
+#endif
 constexpr int RT = 4;           // tokens per run
 constexpr int UT = SSM_UT;      // tokens per unit
 constexpr int NR = UT / RT;     // runs per unit
@@ -153,14 +156,15 @@ struct BwdShape {
     static constexpr int NI = RT * CW > 32 ? RT * CW / 32 : 1;  // (token, channel) items of a run per lane
     // shared memory, in floats
     static constexpr int oB = 0, oC = oB + CH * SP, oPre = oC + CH * SP;
-    static constexpr int oFin = oPre + 2 * NW * UT * CW * 4;
-    static constexpr int oCk = oFin + 2 * NW * UT * CW * 2;
+    static constexpr int oFin = oPre + NW * UT * CW * 4;
+    static constexpr int oCk = oFin + NW * UT * CW * 2;
     static constexpr int oRed = oCk + (NR - 1) * NP * SSM_THREADS * 4;
-    static constexpr int floats = oRed + 2 * NW * RT * 2 * SP;
+    static constexpr int oBC = oRed + 2 * NW * RT * 2 * SP;
+    static constexpr int floats = oBC + CH * 2 * SP;
 };
 
 template <class E, int P>
-__global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
+__global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
     using L = BwdShape<P>;
     constexpr int CL = L::CL, CW = L::CW, SP = L::SP, NI = L::NI, NB = CW > 32 ? 2 : 1, LT = lane_tokens<P>();
     extern __shared__ __align__(16) float sm[];
@@ -174,10 +178,11 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int p = lane % P, cl = lane / P, s0 = SPT * p;
     float *sB = sm + L::oB, *sC = sm + L::oC;
-    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * 2 * UT * CW;  // [buffer][token][channel]: delta, delta u, dY, u
-    float2* fin = reinterpret_cast<float2*>(sm + L::oFin) + w * 2 * UT * CW;  // d delta / d dt, dz / y0
-    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;        // [run][pass], stride 128
-    float* red = sm + L::oRed;                                                // [parity][warp][token][2 SP]
+    // a unit's scalars; a run's give way to the next unit's as soon as it is done
+    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * UT * CW;  // [token][channel]: delta, delta u, dY, u
+    float2* fin = reinterpret_cast<float2*>(sm + L::oFin) + w * UT * CW;  // d delta / d dt, dz / y0
+    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;    // [run][pass], stride 128
+    float *red = sm + L::oRed, *sBC = sm + L::oBC;                        // [parity][warp][token][2 SP]; [token][2 SP]
     ssm_load_rows<E, SP>(sB, a.B, a.ldb, t0, len, g_ * S, S);
     ssm_load_rows<E, SP>(sC, a.Cm, a.ldc, t0, len, g_ * S, S);
     __syncthreads();
@@ -251,8 +256,8 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
                         v.z = __fmul_rn(v.z, zs);
                     }
                 }
-                pre[((u & 1) * UT + run * RT) * CW + i] = v;
-                fin[((u & 1) * UT + run * RT) * CW + i] = f;
+                pre[run * RT * CW + i] = v;
+                fin[run * RT * CW + i] = f;
             }
         };
         Raw nxt[NI];
@@ -263,8 +268,8 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
         }
 #pragma unroll 1
         for (int u = nu - 1; u >= 0; --u) {
-            const float4* pu = pre + (u & 1) * UT * CW + cl;
-            const float2* fu = fin + (u & 1) * UT * CW + cl;
+            const float4* pu = pre + cl;
+            const float2* fu = fin + cl;
             const int nr = (min(UT, len - u * UT) + RT - 1) / RT;  // runs of the unit
             __syncwarp();
 #pragma unroll
@@ -378,6 +383,7 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
                         red[((par * NW + w) * RT + i) * 2 * SP + (vi / SPT) * SP + s0 + vi % SPT] = v[j];
                     }
                 }
+                __syncwarp();
                 if (u > 0) stage(nxt, u - 1, r);
                 // the warps' sums are written; two buffers, so that one barrier a run is enough
                 __syncthreads();
@@ -386,11 +392,8 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
                     float s = rp[0];
 #pragma unroll
                     for (int j = 1; j < NW; ++j) s += rp[j * RT * 2 * SP];
-                    const int row = row0 + i / (2 * SP), v = i % (2 * SP), x = v / SP, st = v % SP;
-                    if (row < len && st < S) {  // the same thread adds every tile of the block
-                        float* o = a.pBC + (int64_t(gsp) * a.T + t0 + row) * 2 * S + x * S + st;
-                        *o = it ? *o + s : s;
-                    }
+                    float* o = sBC + row0 * 2 * SP + i;  // the same thread adds every tile of the block
+                    *o = it ? *o + s : s;
                 }
                 par ^= 1;
             }
@@ -418,6 +421,11 @@ __global__ void __launch_bounds__(SSM_THREADS, P <= 4 ? 3 : 2) k_ssm_bwd(SsmArgs
             }
         }
         __syncwarp();
+    }
+    __syncthreads();
+    for (int i = tid; i < len * 2 * S; i += SSM_THREADS) {
+        const int r = i / (2 * S), v = i % (2 * S);
+        a.pBC[(int64_t(gsp) * a.T + t0) * 2 * S + i] = sBC[r * 2 * SP + v / S * SP + v % S];
     }
 }
 
