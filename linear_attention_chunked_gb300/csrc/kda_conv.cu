@@ -436,8 +436,8 @@ __global__ void k_conv_tail(ConvArgs a, __nv_bfloat16* tail) {
 }
 
 // step: one token of every sequence.  A thread owns 8 channels (16-byte rows) and walks `rpt`
-// sequences with the channels' taps in registers, so that large batches read the taps once per
-// rpt sequences and small ones still spread over the machine.
+// sequences, two of them in flight, with the channels' taps in registers, so that large batches read
+// the taps once per rpt sequences and small ones still spread over the machine.
 struct ConvStepArgs {
     int N, C, act, out_fp32, rpt;
     int64_t nslots;
@@ -461,6 +461,7 @@ __device__ __forceinline__ void bf8_to_f(const uint4& u, float (&f)[8]) {
     }
 }
 
+template <int R>
 __global__ void __launch_bounds__(CS_THREADS) k_conv_step(ConvStepArgs a) {
     const int G = a.C / 8, cg = blockIdx.x * CS_THREADS + threadIdx.x;
     if (cg >= G) return;
@@ -473,42 +474,55 @@ __global__ void __launch_bounds__(CS_THREADS) k_conv_step(ConvStepArgs a) {
         b[k] = a.bias ? a.bias[c0 + k] : 0.f;
     }
     const int n1 = min(int(blockIdx.y + 1) * a.rpt, a.N);
-#pragma unroll 2
-    for (int n = blockIdx.y * a.rpt; n < n1; ++n) {
-        int64_t slot = n;
-        bool use = true;
-        if (a.slots) {
-            slot = a.slots[n];
-            use = slot >= 0 && slot < a.nslots;
-            if (slot >= a.nslots && a.status && cg == 0) *a.status = KDA_ERR_DEVICE_CHECK;
-        }
-        float out[8];
+    for (int n0 = blockIdx.y * a.rpt; n0 < n1; n0 += R) {
+        uint4 raw[R][4];
+        int64_t at[R];
+        bool use[R];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = 0.f;
-        if (use) {
-            uint4 raw[4];
+        for (int r = 0; r < R; ++r) {  // every row's loads before the first is used
+            const int64_t n = n0 + r;
+            int64_t slot = n;
+            use[r] = n < n1;
+            if (use[r] && a.slots) {
+                slot = a.slots[n];
+                if (slot >= a.nslots && a.status && cg == 0) *a.status = KDA_ERR_DEVICE_CHECK;
+                use[r] = slot >= 0 && slot < a.nslots;
+            }
+            at[r] = slot * 3 * C + c0;
+            if (use[r]) {
 #pragma unroll
-            for (int j = 0; j < 3; ++j) raw[j] = *reinterpret_cast<const uint4*>(a.win + (slot * 3 + j) * C + c0);
-            raw[3] = *reinterpret_cast<const uint4*>(a.x + n * C + c0);
-#pragma unroll
-            for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(a.wout + (slot * 3 + j) * C + c0) = raw[j + 1];
-            float f[4][8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bf8_to_f(raw[j], f[j]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float z = b[k] + w[0][k] * f[0][k] + w[1][k] * f[1][k] + w[2][k] * f[2][k] + w[3][k] * f[3][k];
-                // the fast division returns 0 past 2^126, the limit for z < -87
-                out[k] = a.act ? __fdividef(z, 1.f + __expf(-z)) : z;
+                for (int j = 0; j < 3; ++j) raw[r][j] = *reinterpret_cast<const uint4*>(a.win + at[r] + j * C);
+                raw[r][3] = *reinterpret_cast<const uint4*>(a.x + n * C + c0);
             }
         }
-        if (a.out_fp32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.y) + n * C + c0);
-            o[0] = make_float4(out[0], out[1], out[2], out[3]);
-            o[1] = make_float4(out[4], out[5], out[6], out[7]);
-        } else {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + n * C + c0) =
-                make_uint4(pack2(out[0], out[1]), pack2(out[2], out[3]), pack2(out[4], out[5]), pack2(out[6], out[7]));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t n = n0 + r;
+            if (n >= n1) break;
+            float out[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[k] = 0.f;
+            if (use[r]) {
+#pragma unroll
+                for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(a.wout + at[r] + j * C) = raw[r][j + 1];
+                float f[4][8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bf8_to_f(raw[r][j], f[j]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float z = b[k] + w[0][k] * f[0][k] + w[1][k] * f[1][k] + w[2][k] * f[2][k] + w[3][k] * f[3][k];
+                    // the fast division returns 0 past 2^126, the limit for z < -87
+                    out[k] = a.act ? __fdividef(z, 1.f + __expf(-z)) : z;
+                }
+            }
+            if (a.out_fp32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.y) + n * C + c0);
+                o[0] = make_float4(out[0], out[1], out[2], out[3]);
+                o[1] = make_float4(out[4], out[5], out[6], out[7]);
+            } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + n * C + c0) =
+                    make_uint4(pack2(out[0], out[1]), pack2(out[2], out[3]), pack2(out[4], out[5]), pack2(out[6], out[7]));
+            }
         }
     }
 }
@@ -659,7 +673,9 @@ kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     {
         ProfScope ps(KK_CONV_STEP, st);
-        k_conv_step<<<dim3(gx, unsigned((q.N + a.rpt - 1) / a.rpt)), CS_THREADS, 0, st>>>(a);
+        const dim3 grid(gx, unsigned((q.N + a.rpt - 1) / a.rpt));
+        if (a.rpt == 1) k_conv_step<1><<<grid, CS_THREADS, 0, st>>>(a);
+        else k_conv_step<2><<<grid, CS_THREADS, 0, st>>>(a);
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

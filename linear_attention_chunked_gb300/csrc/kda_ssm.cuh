@@ -126,15 +126,16 @@ __device__ __forceinline__ float ssm_silu(float z) {
     return __fmul_rn(z, z < -87.f ? 0.f : rcp(__fadd_rn(1.f, ex2(-LOG2E * z))));
 }
 
-__device__ __forceinline__ f2 ssm_silu2(f2 z) {
-    float x, y;
+// two logistic functions; gate: exactly 0 below -87, so that z times it has silu's limit
+template <bool GATE = false>
+__device__ __forceinline__ f2 ssm_sigmoid2(f2 z) {
+    float x, y, p, q;
     up2(z, x, y);
-    const f2 e = mul2(z, pk2(-LOG2E, -LOG2E));
-    float p, q;
-    up2(e, p, q);
+    up2(mul2(z, pk2(-LOG2E, -LOG2E)), p, q);
     up2(add2(pk2(ex2(p), ex2(q)), pk2(1.f, 1.f)), p, q);
-    return mul2(z, pk2(x < -87.f ? 0.f : rcp(p), y < -87.f ? 0.f : rcp(q)));
+    return GATE ? pk2(x < -87.f ? 0.f : rcp(p), y < -87.f ? 0.f : rcp(q)) : pk2(rcp(p), rcp(q));
 }
+__device__ __forceinline__ f2 ssm_gate2(f2 z) { return ssm_sigmoid2<true>(z); }
 
 // softplus(x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], with log1p(u) = 2 atanh(z), z = u / (2 + u) in
 // (0, 1/3].  2 atanh(z) / z is a polynomial in z^2 (its minimax fit on [0, 1/9] by Remez exchange:

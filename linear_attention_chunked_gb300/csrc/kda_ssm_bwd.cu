@@ -13,13 +13,15 @@
 // k_ssm_bwd needs h_{t-1} in reverse.  The forward leaves the state at every 16th token; a unit of 16
 // tokens is swept forward once from there, the states every 4 tokens kept in shared memory, and
 // each run of 4 tokens is recomputed from its start with states and decays in registers and walked
-// backwards.  Four lanes hold a channel's 16 states (four each), a warp 16 channels in two passes.
-// The channels' scalars (delta, delta u, dY, u and what the gradients are multiplied with at the end) are
-// computed once per token by lanes laid out as (token, channel) items and handed over through shared
-// memory, one unit ahead of their use.  Sums cross lanes by halving (each step a lane gives away half
-// of its values): a channel's three sums over states for 4 tokens leave each of its four lanes with one
-// token, whose du, ddt and dz that lane finishes; the eight dB / dC terms per token, summed over the two
-// passes in registers first, take 7 shuffles over 8 lanes.
+// backwards.  Four lanes hold a channel's 16 states (four each), and a lane holds two channels, as the two
+// halves of packed arithmetic: the channels' scalars are pairs as they lie, and B and C are read once for
+// both.  The scalars (delta, delta u, dY, u and
+// what the gradients are multiplied with at the end) are computed once per token by lanes laid out as
+// (token, channel pair) items and handed over through shared memory, one unit ahead of their use.  Sums
+// cross lanes by halving (each step a lane gives away half of its values): a channel's three sums over
+// states for 4 tokens leave each of its four lanes with one token, whose du, ddt and dz that lane
+// finishes; the eight dB / dC terms per token, summed over the two channels first, take 7 shuffles
+// over 8 lanes.
 #include "kda_ssm.cuh"
 #include "kda_ssm_launch.cuh"
 
@@ -27,13 +29,9 @@ namespace kda {
 
 namespace {
 
-#ifndef BB
-#define BB (P <= 4 ? 3 : 2)
-#endif
 constexpr int RT = 4;           // tokens per run
 constexpr int UT = SSM_UT;      // tokens per unit
 constexpr int NR = UT / RT;     // runs per unit
-constexpr int NP = 2;           // channel passes per warp
 constexpr int NW = SSM_THREADS / 32;
 constexpr int SPT = 4;       // states per lane
 
@@ -122,51 +120,50 @@ __device__ __forceinline__ int reduce_index(int lane) {
 }
 
 // Sums of a run's three values per token over the P lanes of a channel, halving over the tokens: on return
-// a lane holds its tokens' sums in v[.][0 .. NT-1], the first of them token first_token(p).
+// a lane holds its tokens' sums in v[.][0 .. lane_tokens - 1], the first of them token first_token(p).
 template <int P> __device__ constexpr int lane_tokens() { return P == 1 ? 4 : P == 2 ? 2 : 1; }
 template <int P> __device__ __forceinline__ int first_token(int p) {
     return (P > 1 && (p & 1) ? 2 : 0) + (P > 2 && (p & 2) ? 1 : 0);
 }
 template <int P>
-__device__ __forceinline__ void reduce_tokens(float (&v)[3][RT], int p) {
+__device__ __forceinline__ void reduce_tokens(f2 (&v)[3][RT], int p) {
     static_assert(RT == 4, "two halvings");
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (P > 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float give = p & 1 ? v[x][i] : v[x][i + 2], keep = p & 1 ? v[x][i + 2] : v[x][i];
-                v[x][i] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+                const f2 give = p & 1 ? v[x][i] : v[x][i + 2], keep = p & 1 ? v[x][i + 2] : v[x][i];
+                v[x][i] = add2(keep, __shfl_xor_sync(0xffffffffu, give, 1));
             }
         if (P > 2) {
-            const float give = p & 2 ? v[x][0] : v[x][1], keep = p & 2 ? v[x][1] : v[x][0];
-            v[x][0] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+            const f2 give = p & 2 ? v[x][0] : v[x][1], keep = p & 2 ? v[x][1] : v[x][0];
+            v[x][0] = add2(keep, __shfl_xor_sync(0xffffffffu, give, 2));
         }
 #pragma unroll
-        for (int o = 4; o < P; o <<= 1) v[x][0] += __shfl_xor_sync(0xffffffffu, v[x][0], o);
+        for (int o = 4; o < P; o <<= 1) v[x][0] = add2(v[x][0], __shfl_xor_sync(0xffffffffu, v[x][0], o));
     }
 }
 
 template <int P>
 struct BwdShape {
-    static constexpr int CL = 32 / P;       // channels of a pass
-    static constexpr int CW = NP * CL;      // channels of a warp
-    static constexpr int CB = NW * CW;      // channels of a tile
+    static constexpr int CL = 32 / P;       // channel pairs of a warp: channels i and i + CL
+    static constexpr int CB = NW * 2 * CL;  // channels of a tile
     static constexpr int SP = SPT * P;      // state slots
-    static constexpr int NI = RT * CW > 32 ? RT * CW / 32 : 1;  // (token, channel) items of a run per lane
-    // shared memory, in floats
+    static constexpr int NI = RT * CL > 32 ? RT * CL / 32 : 1;  // (token, channel pair) items of a run per lane
+    // shared memory, in floats: B and C rows; three vectors of scalars per item; states at the
+    // runs' starts; the warps' dB, dC; the chunk's
     static constexpr int oB = 0, oC = oB + CH * SP, oPre = oC + CH * SP;
-    static constexpr int oFin = oPre + NW * UT * CW * 4;
-    static constexpr int oCk = oFin + NW * UT * CW * 2;
-    static constexpr int oRed = oCk + (NR - 1) * NP * SSM_THREADS * 4;
+    static constexpr int oCk = oPre + 3 * NW * UT * CL * 4;
+    static constexpr int oRed = oCk + (NR - 1) * 2 * SSM_THREADS * 4;
     static constexpr int oBC = oRed + 2 * NW * RT * 2 * SP;
     static constexpr int floats = oBC + CH * 2 * SP;
 };
 
 template <class E, int P>
-__global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
+__global__ void __launch_bounds__(SSM_THREADS, P == 1 ? 2 : P <= 4 ? 3 : 1) k_ssm_bwd(SsmArgs a, SsmBwdPlan pl) {
     using L = BwdShape<P>;
-    constexpr int CL = L::CL, CW = L::CW, SP = L::SP, NI = L::NI, NB = CW > 32 ? 2 : 1, LT = lane_tokens<P>();
+    constexpr int CL = L::CL, SP = L::SP, NI = L::NI, LT = lane_tokens<P>();
     extern __shared__ __align__(16) float sm[];
     const int per_chunk = a.G * pl.splits;
     const int k = blockIdx.x / per_chunk;
@@ -178,11 +175,16 @@ __global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPl
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int p = lane % P, cl = lane / P, s0 = SPT * p;
     float *sB = sm + L::oB, *sC = sm + L::oC;
-    // a unit's scalars; a run's give way to the next unit's as soon as it is done
-    float4* pre = reinterpret_cast<float4*>(sm + L::oPre) + w * UT * CW;  // [token][channel]: delta, delta u, dY, u
-    float2* fin = reinterpret_cast<float2*>(sm + L::oFin) + w * UT * CW;  // d delta / d dt, dz / y0
-    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;    // [run][pass], stride 128
-    float *red = sm + L::oRed, *sBC = sm + L::oBC;                        // [parity][warp][token][2 SP]; [token][2 SP]
+    auto four = [&](const float* rows, int row, f2(&o)[SPT]) {  // the lane's states of a row, doubled
+        const float4 v = *reinterpret_cast<const float4*>(rows + row * SP + s0);
+        o[0] = pk2(v.x, v.x), o[1] = pk2(v.y, v.y), o[2] = pk2(v.z, v.z), o[3] = pk2(v.w, v.w);
+    };
+    // a unit's scalars [token][pair]; a run's give way to the next unit's as soon as it is done
+    ulonglong2* pX = reinterpret_cast<ulonglong2*>(sm + L::oPre) + w * UT * CL;  // delta, delta u
+    ulonglong2* pY = pX + NW * UT * CL;                                          // dY, u
+    ulonglong2* pF = pY + NW * UT * CL;                                          // d delta / d dt, dz / y0
+    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + L::oCk) + tid;           // [run][2], stride 128
+    float *red = sm + L::oRed, *sBC = sm + L::oBC;                               // [parity][warp][token][2 SP]; [token][2 SP]
     ssm_load_rows<E, SP>(sB, a.B, a.ldb, t0, len, g_ * S, S);
     ssm_load_rows<E, SP>(sC, a.Cm, a.ldc, t0, len, g_ * S, S);
     __syncthreads();
@@ -193,105 +195,129 @@ __global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPl
     for (int it = 0; it < pl.nl; ++it) {
         const int cb = (split * pl.nl + it) * L::CB;  // the tile's first channel in the group
         if (cb >= Cg) break;
-        const int cw = cb + w * CW;                                         // the warp's
+        const int cw = cb + w * 2 * CL;                                    // the warp's
         auto chan = [&](int j) { return g_ * Cg + min(cw + j, Cg - 1); };  // its j-th channel
-        // lanes as states: pass q's channel.  Lanes past the group's channels stay zero: they add
+        // lanes as states: channels cl and cl + CL.  Lanes past the group's channels stay zero: they add
         // nothing to dB and dC
-        f2 A2[NP][2], g[NP][2], dA[NP][2], hs[NP][2];
-        float skip[NP], accD[NP] = {}, accb[NP] = {};
-        auto lim = [&](int q) { return cw + q * CL + cl < Cg ? S : 0; };
-        auto pair2 = [](float4 v, f2(&o)[2]) { o[0] = pk2(v.x, v.y), o[1] = pk2(v.z, v.w); };
-        auto start = [&](int u, int q) {  // the state at unit u's start
-            return ld4(a.hs + ((int64_t(k) * SSM_SUB + u) * a.C + chan(q * CL + cl)) * S, s0, lim(q));
+        const int c0 = chan(cl), c1 = chan(cl + CL);
+        const bool on0 = cw + cl < Cg, on1 = cw + cl + CL < Cg;
+        f2 A2[SPT], g[SPT], dA[SPT], hs[SPT];
+        auto both4 = [&](const float* base, bool mask, float4(&o)[2]) {
+            o[0] = ld4(base + int64_t(c0) * S, s0, !mask || on0 ? S : 0);
+            o[1] = ld4(base + int64_t(c1) * S, s0, !mask || on1 ? S : 0);
         };
-        float4 nh[NP];
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const int64_t row = int64_t(chan(q * CL + cl)) * S;
-            float4 v = ld4(a.A + row, s0, S);
-            v.x *= LOG2E, v.y *= LOG2E, v.z *= LOG2E, v.w *= LOG2E;
-            pair2(v, A2[q]);
-            pair2(ld4(a.gs + int64_t(k) * a.C * S + row, s0, lim(q)), g[q]);
-            dA[q][0] = dA[q][1] = 0;
-            nh[q] = start(nu - 1, q);
-            skip[q] = a.D ? a.D[chan(q * CL + cl)] : 0.f;
+        auto paired = [](const float4(&v)[2], f2(&o)[SPT]) {
+            o[0] = pk2(v[0].x, v[1].x), o[1] = pk2(v[0].y, v[1].y), o[2] = pk2(v[0].z, v[1].z), o[3] = pk2(v[0].w, v[1].w);
+        };
+        float4 nh[2];                  // the next unit's states, paired where they are used (pairing waits for them)
+        auto start = [&](int u) {  // the states at unit u's start
+            both4(a.hs + (int64_t(k) * SSM_SUB + u) * a.C * S, true, nh);
+        };
+        {
+            float4 va[2], vg[2];
+            both4(a.A, false, va);
+            both4(a.gs + int64_t(k) * a.C * S, true, vg);
+            start(nu - 1);
+            paired(va, A2);
+            paired(vg, g);
         }
-        // lanes as (token, channel) items of a run: item x is token (lane + 32 x) / CW of the run and
-        // channel (lane + 32 x) % CW of the warp
-        float bias[NB];
 #pragma unroll
-        for (int x = 0; x < NB; ++x) bias[x] = a.bias ? a.bias[chan(lane % CW + 32 * x)] : 0.f;
-        struct Raw { E dt, u, dy, z; };
-        auto at = [&](const void* base, int64_t ld, int row, int c) {
-            return static_cast<const E*>(base)[(int64_t(t0) + row) * ld + c];
-        };
+        for (int j = 0; j < SPT; ++j) A2[j] = mul2(A2[j], pk2(LOG2E, LOG2E)), dA[j] = 0;
+        const f2 skip = a.D ? pk2(a.D[c0], a.D[c1]) : 0;
+        f2 accD = 0, accb = 0;
+        // lanes as items: item x of a run is token (lane + 32 x) / CL, channels lane % CL and lane % CL + CL
+        const int ic = lane % CL, i0 = chan(ic), i1 = chan(ic + CL);
+        const f2 bias = a.bias ? pk2(a.bias[i0], a.bias[i1]) : 0;
+        const bool ion0 = cw + ic < Cg, ion1 = cw + ic + CL < Cg;
+        struct Raw { E dt[2], u[2], dy[2], z[2]; };
         auto fetch = [&](Raw(&r)[NI], int row0) {
 #pragma unroll
             for (int x = 0; x < NI; ++x) {
-                const int i = lane + 32 * x, c = chan(i % CW), row = min(row0 + i / CW, len - 1);
-                r[x].dt = at(a.dt, a.lddt, row, c);
-                r[x].u = at(a.u, a.ldu, row, c);
-                r[x].dy = at(a.dy, a.C, row, c);
-                if (gated) r[x].z = at(a.z, a.ldz, row, c);
+                const int64_t t = t0 + min(row0 + (lane + 32 * x) / CL, len - 1);
+                auto two = [&](E(&o)[2], const void* base, int64_t ld) {
+                    const E* q = static_cast<const E*>(base) + t * ld;
+                    o[0] = q[i0], o[1] = q[i1];
+                };
+                two(r[x].dt, a.dt, a.lddt);
+                two(r[x].u, a.u, a.ldu);
+                two(r[x].dy, a.dy, a.C);
+                if (gated) two(r[x].z, a.z, a.ldz);
             }
         };
-        // the scalars of a run into a unit's buffer; tokens past the chunk are the identity step
+        auto wide = [](const E(&v)[2]) { return pk2(ssm_f<E>(v[0]), ssm_f<E>(v[1])); };
+        // the scalars of a run; tokens past the chunk are the identity step
         auto stage = [&](const Raw(&r)[NI], int u, int run) {
 #pragma unroll
             for (int x = 0; x < NI; ++x) {
                 const int i = lane + 32 * x;
-                if (RT * CW < 32 && i >= RT * CW) break;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                float2 f = make_float2(0.f, 0.f);
-                if (u * UT + run * RT + i / CW < len && cw + i % CW < Cg) {
-                    const float raw = __fadd_rn(ssm_f<E>(r[x].dt), bias[x % NB]);
-                    v.x = ssm_delta(raw, a.softplus);
-                    v.w = ssm_f<E>(r[x].u);
-                    v.y = __fmul_rn(v.x, v.w);
-                    v.z = ssm_f<E>(r[x].dy);
-                    f.x = a.softplus ? ssm_sigmoid(raw) : 1.f;
-                    if (gated) {
-                        const float z = ssm_f<E>(r[x].z), sg = z < -87.f ? 0.f : ssm_sigmoid(z), zs = z * sg;
-                        f.y = v.z * fmaf(zs, 1.f - sg, sg);  // silu'(z) = sg + z sg (1 - sg)
-                        v.z = __fmul_rn(v.z, zs);
-                    }
+                if (RT * CL < 32 && i >= RT * CL) break;
+                const bool in = u * UT + run * RT + i / CL < len;
+                const f2 raw = add2(wide(r[x].dt), bias), dl = ssm_delta2(raw, a.softplus);
+                f2 uu = wide(r[x].u), dY = wide(r[x].dy), sg = pk2(1.f, 1.f), F = 0;
+                if (a.softplus) sg = ssm_sigmoid2(raw);
+                if (gated) {
+                    const f2 z = wide(r[x].z), q = ssm_gate2(z), zs = mul2(z, q);
+                    // silu'(z) = q + z q (1 - q)
+                    F = mul2(dY, fma2(zs, fma2(q, pk2(-1.f, -1.f), pk2(1.f, 1.f)), q));
+                    dY = mul2(dY, zs);
                 }
-                pre[run * RT * CW + i] = v;
-                fin[run * RT * CW + i] = f;
+                auto only = [&](f2 v) {
+                    float y0, y1;
+                    up2(v, y0, y1);
+                    return pk2(in && ion0 ? y0 : 0.f, in && ion1 ? y1 : 0.f);
+                };
+                const int o = run * RT * CL + i;
+                if (in && ion0 && ion1) {
+                    pX[o] = make_ulonglong2(dl, mul2(dl, uu));
+                    pY[o] = make_ulonglong2(dY, uu);
+                    pF[o] = make_ulonglong2(sg, F);
+                } else {
+                    pX[o] = make_ulonglong2(only(dl), only(mul2(dl, uu)));
+                    pY[o] = make_ulonglong2(only(dY), only(uu));
+                    pF[o] = make_ulonglong2(only(sg), only(F));
+                }
             }
         };
+        {
+            constexpr int NF = NI <= 2 ? NR : 1;  // runs in flight
+            Raw first[NF][NI];
+#pragma unroll
+            for (int r0 = 0; r0 < NR; r0 += NF) {
+#pragma unroll
+                for (int r = 0; r < NF; ++r) fetch(first[r], (nu - 1) * UT + (r0 + r) * RT);
+#pragma unroll
+                for (int r = 0; r < NF; ++r) stage(first[r], nu - 1, r0 + r);
+            }
+        }
         Raw nxt[NI];
 #pragma unroll 1
-        for (int r = 0; r < NR; ++r) {
-            fetch(nxt, (nu - 1) * UT + r * RT);
-            stage(nxt, nu - 1, r);
-        }
-#pragma unroll 1
         for (int u = nu - 1; u >= 0; --u) {
-            const float4* pu = pre + cl;
-            const float2* fu = fin + cl;
             const int nr = (min(UT, len - u * UT) + RT - 1) / RT;  // runs of the unit
             __syncwarp();
+            paired(nh, hs);
+            if (u > 0) start(u - 1);
+            // one token forward: decays and states
+            auto ahead = [&](int i, int row, const f2(&h)[SPT], f2(&dec)[SPT], f2(&o)[SPT]) {
+                const ulonglong2 v = pX[i * CL + cl];
+                f2 b[SPT];
+                four(sB, row, b);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                pair2(nh[q], hs[q]);
-                if (u > 0) nh[q] = start(u - 1, q);
-            }
+                for (int j = 0; j < SPT; ++j) {
+                    dec[j] = ex2_2(mul2(A2[j], v.x));
+                    o[j] = fma2(dec[j], h[j], mul2(b[j], v.y));
+                }
+            };
             // forward sweep: the states at every run's start
+            {
+                f2 h[SPT], d[SPT];
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                f2 ha = hs[q][0], hb = hs[q][1];
+                for (int j = 0; j < SPT; ++j) h[j] = hs[j];
 #pragma unroll 1
                 for (int r = 0; r + 1 < nr; ++r) {
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        const float2 v = *reinterpret_cast<const float2*>(pu + (r * RT + i) * CW + q * CL);
-                        const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y);
-                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(sB + (u * UT + r * RT + i) * SP + s0);
-                        ha = fma2(ex2_2(mul2(A2[q][0], d2)), ha, mul2(b2.x, u2));
-                        hb = fma2(ex2_2(mul2(A2[q][1], d2)), hb, mul2(b2.y, u2));
-                    }
-                    ck[(r * NP + q) * SSM_THREADS] = make_ulonglong2(ha, hb);
+                    for (int i = 0; i < RT; ++i) ahead(r * RT + i, u * UT + r * RT + i, h, d, h);
+                    ck[(2 * r) * SSM_THREADS] = make_ulonglong2(h[0], h[1]);
+                    ck[(2 * r + 1) * SSM_THREADS] = make_ulonglong2(h[2], h[3]);
                 }
             }
             // runs the unit lacks (its chunk ends inside it) still stage the next unit's tokens
@@ -304,76 +330,38 @@ __global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPl
             for (int r = nr - 1; r >= 0; --r) {
                 const int row0 = u * UT + r * RT;
                 if (u > 0) fetch(nxt, row0 - UT);
-                f2 bc[RT][4];  // dB, dC of the run's tokens, summed over the passes
+                f2 h[RT + 1][SPT], dec[RT][SPT];
+                if (r > 0) {
+                    const ulonglong2 x = ck[(2 * r - 2) * SSM_THREADS], y = ck[(2 * r - 1) * SSM_THREADS];
+                    h[0][0] = x.x, h[0][1] = x.y, h[0][2] = y.x, h[0][3] = y.y;
+                } else {
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) bc[i][j] = 0;
-#pragma unroll
-                for (int q = 0; q < NP; ++q) {
-                    f2 h[RT + 1][2], dec[RT][2];
-                    h[0][0] = hs[q][0], h[0][1] = hs[q][1];
-                    if (r > 0) {
-                        const ulonglong2 v = ck[((r - 1) * NP + q) * SSM_THREADS];
-                        h[0][0] = v.x, h[0][1] = v.y;
-                    }
-                    const float4* pq = pu + r * RT * CW + q * CL;
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        const float2 v = *reinterpret_cast<const float2*>(pq + i * CW);
-                        const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y);
-                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(sB + (row0 + i) * SP + s0);
-                        dec[i][0] = ex2_2(mul2(A2[q][0], d2));
-                        dec[i][1] = ex2_2(mul2(A2[q][1], d2));
-                        h[i + 1][0] = fma2(dec[i][0], h[i][0], mul2(b2.x, u2));
-                        h[i + 1][1] = fma2(dec[i][1], h[i][1], mul2(b2.y, u2));
-                    }
-                    float sums[3][RT];  // over the states: G B, log2(e) A w, C h
-#pragma unroll
-                    for (int i = RT - 1; i >= 0; --i) {
-                        const float4 v = pq[i * CW];
-                        const f2 d2 = pk2(v.x, v.x), u2 = pk2(v.y, v.y), y2 = pk2(v.z, v.z);
-                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(sB + (row0 + i) * SP + s0);
-                        const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(sC + (row0 + i) * SP + s0);
-                        const f2 G0 = fma2(c2.x, y2, g[q][0]), G1 = fma2(c2.y, y2, g[q][1]);
-                        bc[i][0] = fma2(G0, u2, bc[i][0]);
-                        bc[i][1] = fma2(G1, u2, bc[i][1]);
-                        bc[i][2] = fma2(h[i + 1][0], y2, bc[i][2]);
-                        bc[i][3] = fma2(h[i + 1][1], y2, bc[i][3]);
-                        sums[0][i] = hsum2(fma2(G1, b2.y, mul2(G0, b2.x)));
-                        sums[2][i] = hsum2(fma2(h[i + 1][1], c2.y, mul2(h[i + 1][0], c2.x)));
-                        g[q][0] = mul2(dec[i][0], G0);
-                        g[q][1] = mul2(dec[i][1], G1);
-                        const f2 w0 = mul2(g[q][0], h[i][0]), w1 = mul2(g[q][1], h[i][1]);
-                        sums[1][i] = hsum2(fma2(w1, A2[q][1], mul2(w0, A2[q][0])));
-                        dA[q][0] = fma2(w0, d2, dA[q][0]);
-                        dA[q][1] = fma2(w1, d2, dA[q][1]);
-                    }
-                    reduce_tokens<P>(sums, p);
-                    if (P <= 4 || p < 4)
-#pragma unroll
-                        for (int i = 0; i < LT; ++i) {
-                            const int tk = first_token<P>(p) + i, row = row0 + tk, ci = cw + q * CL + cl;
-                            if (row < len && ci < Cg) {
-                                const int64_t o = (int64_t(t0) + row) * a.C + g_ * Cg + ci;
-                                const float4 v = pq[tk * CW];
-                                const float2 f = fu[(r * RT + tk) * CW + q * CL];
-                                const float dd = fmaf(v.w, sums[0][i], sums[1][i] * 0.6931471805599453f) * f.x;
-                                ssm_st<E>(a.du, o, fmaf(v.x, sums[0][i], skip[q] * v.z));
-                                ssm_st<E>(a.ddt, o, dd);
-                                if (gated) ssm_st<E>(a.dz, o, f.y * fmaf(skip[q], v.w, sums[2][i]));
-                                accD[q] = fmaf(v.z, v.w, accD[q]);
-                                accb[q] += dd;
-                            }
-                        }
+                    for (int j = 0; j < SPT; ++j) h[0][j] = hs[j];
                 }
-                // dB, dC of the run over the warp's channels
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
+                for (int i = 0; i < RT; ++i) ahead(r * RT + i, row0 + i, h[i], dec[i], h[i + 1]);
+                f2 sums[3][RT];  // over the states: G B, log2(e) A w, C h
+#pragma unroll
+                for (int i = RT - 1; i >= 0; --i) {
+                    const ulonglong2 x = pX[(r * RT + i) * CL + cl];
+                    const f2 dY = pY[(r * RT + i) * CL + cl].x;
+                    f2 b[SPT], c[SPT];
+                    four(sB, row0 + i, b);
+                    four(sC, row0 + i, c);
                     constexpr int NV = 2 * SPT, n = NV / CL > 1 ? NV / CL : 1;
-                    float v[NV];
+                    float v[NV];  // dB, dC terms of the two channels
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) up2(bc[i][j], v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < SPT; ++j) {
+                        const f2 G = fma2(c[j], dY, g[j]);
+                        v[j] = hsum2(mul2(G, x.y));
+                        v[SPT + j] = hsum2(mul2(h[i + 1][j], dY));
+                        sums[0][i] = j ? fma2(G, b[j], sums[0][i]) : mul2(G, b[j]);
+                        sums[2][i] = j ? fma2(h[i + 1][j], c[j], sums[2][i]) : mul2(h[i + 1][j], c[j]);
+                        g[j] = mul2(dec[i][j], G);
+                        const f2 wj = mul2(g[j], h[i][j]);
+                        sums[1][i] = j ? fma2(wj, A2[j], sums[1][i]) : mul2(wj, A2[j]);
+                        dA[j] = fma2(wj, x.x, dA[j]);
+                    }
                     reduce_lanes<NV, P>(v, lane);
                     // (with more channel lanes than values, several lanes write the same sum)
                     const int idx = reduce_index<NV, P>(lane);
@@ -383,6 +371,31 @@ __global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPl
                         red[((par * NW + w) * RT + i) * 2 * SP + (vi / SPT) * SP + s0 + vi % SPT] = v[j];
                     }
                 }
+                reduce_tokens<P>(sums, p);
+                if (P <= 4 || p < 4)
+#pragma unroll
+                    for (int i = 0; i < LT; ++i) {
+                        const int tk = first_token<P>(p) + i, row = row0 + tk;
+                        if (row < len && on0) {
+                            const ulonglong2 x = pX[(r * RT + tk) * CL + cl], y = pY[(r * RT + tk) * CL + cl];
+                            const ulonglong2 f = pF[(r * RT + tk) * CL + cl];
+                            const f2 du = fma2(x.x, sums[0][i], mul2(skip, y.x));
+                            const f2 dd = mul2(fma2(y.y, sums[0][i], mul2(sums[1][i], pk2(0.6931471805599453f, 0.6931471805599453f))), f.x);
+                            const f2 dz = mul2(f.y, fma2(skip, y.y, sums[2][i]));
+                            accD = fma2(y.x, y.y, accD);
+                            accb = add2(accb, dd);
+                            const int64_t o = (int64_t(t0) + row) * a.C + g_ * Cg + cw + cl;
+                            auto put = [&](void* base, f2 val) {
+                                float q0, q1;
+                                up2(val, q0, q1);
+                                ssm_st<E>(base, o, q0);
+                                if (on1) ssm_st<E>(base, o + CL, q1);
+                            };
+                            put(a.du, du);
+                            put(a.ddt, dd);
+                            if (gated) put(a.dz, dz);
+                        }
+                    }
                 __syncwarp();
                 if (u > 0) stage(nxt, u - 1, r);
                 // the warps' sums are written; two buffers, so that one barrier a run is enough
@@ -398,28 +411,30 @@ __global__ void __launch_bounds__(SSM_THREADS, BB) k_ssm_bwd(SsmArgs a, SsmBwdPl
                 par ^= 1;
             }
         }
+        // the channel's lanes hold its tokens' terms of dD and dbias
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            // the channel's lanes hold its tokens' terms of dD and dbias
-#pragma unroll
-            for (int o = 1; o < P; o <<= 1) {
-                accD[q] += __shfl_xor_sync(0xffffffffu, accD[q], o);
-                accb[q] += __shfl_xor_sync(0xffffffffu, accb[q], o);
-            }
-            const int ci = cw + q * CL + cl;
-            if (ci < Cg) {
-                const int c = g_ * Cg + ci;
-                float* row = a.pA + (int64_t(k) * a.C + c) * (S + 2);
-                float4 v;
-                up2(dA[q][0], v.x, v.y);
-                up2(dA[q][1], v.z, v.w);
-                st4(row, s0, S, v);
-                if (p == 0) row[S] = accD[q], row[S + 1] = accb[q];
-                up2(g[q][0], v.x, v.y);
-                up2(g[q][1], v.z, v.w);
-                if (a.dh0 && tab.w == 0) st4(a.dh0 + (int64_t(tab.x) * a.C + c) * S, s0, S, v);
-            }
+        for (int o = 1; o < P; o <<= 1) {
+            accD = add2(accD, __shfl_xor_sync(0xffffffffu, accD, o));
+            accb = add2(accb, __shfl_xor_sync(0xffffffffu, accb, o));
         }
+        float v[2][4], e[2][4], d[2], b[2];
+#pragma unroll
+        for (int j = 0; j < SPT; ++j) {
+            up2(dA[j], v[0][j], v[1][j]);
+            up2(g[j], e[0][j], e[1][j]);
+        }
+        up2(accD, d[0], d[1]);
+        up2(accb, b[0], b[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (q ? on1 : on0) {
+                const int c = q ? c1 : c0;
+                float* row = a.pA + (int64_t(k) * a.C + c) * (S + 2);
+                st4(row, s0, S, make_float4(v[q][0], v[q][1], v[q][2], v[q][3]));
+                if (p == 0) row[S] = d[q], row[S + 1] = b[q];
+                if (a.dh0 && tab.w == 0)
+                    st4(a.dh0 + (int64_t(tab.x) * a.C + c) * S, s0, S, make_float4(e[q][0], e[q][1], e[q][2], e[q][3]));
+            }
         __syncwarp();
     }
     __syncthreads();
@@ -453,16 +468,23 @@ __global__ void k_ssm_reduce_bc(SsmArgs a, SsmBwdPlan pl) {
     }
 }
 
-// dA, dD, dbias: the chunks' sums in order
-__global__ void k_ssm_reduce_par(SsmArgs a) {
+// dA, dD, dbias: the chunks' sums.  32 values x 16 strands of chunks per block; a strand's chunks are added
+// in order, then the strands.
+constexpr int PAR_STRANDS = 16;
+__global__ void __launch_bounds__(32 * PAR_STRANDS) k_ssm_reduce_par(SsmArgs a) {
+    __shared__ float part[PAR_STRANDS][33];
     if (*a.status != KDA_OK) return;
-    const int W = a.S + 2;
-    const int64_t n = int64_t(a.C) * W, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= n) return;
-    const int nc = *a.nchunks;
+    const int W = a.S + 2, x = threadIdx.x & 31, st = threadIdx.x >> 5, nc = *a.nchunks;
+    const int64_t n = int64_t(a.C) * W, i = int64_t(blockIdx.x) * 32 + x;
     float sum = 0.f;
+    if (i < n)
 #pragma unroll 8
-    for (int k = 0; k < nc; ++k) sum += a.pA[k * n + i];
+        for (int k = st; k < nc; k += PAR_STRANDS) sum += a.pA[k * n + i];
+    part[st][x] = sum;
+    __syncthreads();
+    if (st || i >= n) return;
+#pragma unroll
+    for (int j = 1; j < PAR_STRANDS; ++j) sum += part[j][x];
     const int c = int(i / W), s = int(i % W);
     if (s < a.S) a.dA[int64_t(c) * a.S + s] = sum;
     else if (s == a.S) { if (a.dD) a.dD[c] = sum; }
@@ -484,7 +506,7 @@ void launch_main(const SsmArgs& a, const SsmBwdPlan& pl, cudaStream_t st) {
     {
         ProfScope ps(KK_SSM_REDUCE, st);
         const int64_t n = int64_t(a.C) * (a.S + 2);
-        k_ssm_reduce_par<<<unsigned((n + 127) / 128), 128, 0, st>>>(a);
+        k_ssm_reduce_par<<<unsigned((n + 31) / 32), 32 * PAR_STRANDS, 0, st>>>(a);
     }
 }
 
@@ -516,7 +538,7 @@ cudaError_t setup_e() {
 SsmBwdPlan ssm_bwd_plan(int64_t maxC, int C, int S, int G) {
     SsmBwdPlan pl{};
     pl.lanes = S <= 4 ? 1 : S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16;
-    const int CB = NW * NP * (32 / pl.lanes), Cg = C / G;
+    const int CB = NW * 2 * (32 / pl.lanes), Cg = C / G;
     pl.tiles = (Cg + CB - 1) / CB;
     // four tiles per block keep the partial sums of dB and dC small; with fewer blocks than the
     // machine holds at once, one tile per block spreads the work
