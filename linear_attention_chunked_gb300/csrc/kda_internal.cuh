@@ -397,6 +397,17 @@ void launch_walk_tc(int precision, int N, const int* doc_frag, int F, int H, con
                     const float* B, const float* S0, int reverse, float* S_in, float* S_final,
                     int* status, cudaStream_t st);
 
+// Raises a kernel's dynamic shared memory limit to `bytes`, once per kernel and device (`done` is a static
+// of the caller's template instance).  A failure shows at the launch.
+inline void allow_smem(const void* kernel, size_t bytes, unsigned long long* done) {
+    int dev = 0;
+    if (bytes <= 40 * 1024 || cudaGetDevice(&dev) != cudaSuccess) return;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (__atomic_load_n(done, __ATOMIC_RELAXED) & bit)) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess)
+        __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
+}
+
 // Launch accounting: every kernel launch of the library sits inside a ProfScope, which counts it
 // and, while profiling is enabled (kda_profile_enable), brackets it with CUDA events on its stream.
 enum KernelKind {

@@ -630,11 +630,11 @@ int parts_of(int64_t T, const Shape& s) {
     return int(want < 1 ? 1 : want < slots ? want : slots);
 }
 
-template <class F>
-void ring_launch(F* f, unsigned blocks, int threads, size_t smem, const LnArgs& a, cudaStream_t st) {
-    // (idempotent; a launch that it cannot serve reports the error)
-    if (smem > 40 * 1024) cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    f<<<blocks, threads, smem, st>>>(a);
+template <auto* F>
+void ring_launch(unsigned blocks, int threads, size_t smem, const LnArgs& a, cudaStream_t st) {
+    static unsigned long long done;
+    allow_smem((const void*)F, smem, &done);
+    F<<<blocks, threads, smem, st>>>(a);
 }
 
 template <class E, int V, int K, int NT>
@@ -645,8 +645,8 @@ void fwd(LnArgs a, const Shape& s, cudaStream_t st) {
         if (a.T >= 4 * int64_t(parts)) {
             a.parts = parts;
             const unsigned blocks = unsigned(NT == 32 ? (parts + LN_WARP_ROWS - 1) / LN_WARP_ROWS : parts);
-            if (a.res) ring_launch(k_ln_fwd_walk<E, V, K, NT, true>, blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
-            else ring_launch(k_ln_fwd_walk<E, V, K, NT, false>, blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 1>(), a, st);
+            if (a.res) ring_launch<k_ln_fwd_walk<E, V, K, NT, true>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
+            else ring_launch<k_ln_fwd_walk<E, V, K, NT, false>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 1>(), a, st);
             return;
         }
     }
@@ -656,8 +656,8 @@ void fwd(LnArgs a, const Shape& s, cudaStream_t st) {
 template <class E, int V, int K, int NT>
 void bwd(const LnArgs& a, cudaStream_t st) {
     const unsigned blocks = unsigned(NT == 32 ? (a.parts + LN_WARP_ROWS - 1) / LN_WARP_ROWS : a.parts);
-    if (a.dsum) ring_launch(k_ln_bwd<E, V, K, NT, true>, blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 3>(), a, st);
-    else ring_launch(k_ln_bwd<E, V, K, NT, false>, blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
+    if (a.dsum) ring_launch<k_ln_bwd<E, V, K, NT, true>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 3>(), a, st);
+    else ring_launch<k_ln_bwd<E, V, K, NT, false>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
 }
 template <class E, int V, int K, int NT>
 void run(const LnArgs& a, const Shape& s, bool back, cudaStream_t st) {

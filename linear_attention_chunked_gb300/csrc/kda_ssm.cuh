@@ -32,7 +32,8 @@ struct SsmArgs {
     void *y, *du, *ddt, *dB, *dC, *dz;  // dense rows
     float *ht, *dA, *dD, *dbias, *dh0;
     // workspace
-    int *status, *nchunks, *doc_off;
+    int *status, *nchunks, *doc_off;  // the chunk plan's (a saved set holds its forward's plan)
+    int* call_status;                 // the first word of this call's workspace
     int4* chunk_tab;  // {doc, first token, length, chunk index within the doc}
     float* sumdt;     // [maxC][C] sum of delta over the chunk
     float* hs;        // [maxC][sub][C][S] states at the chunks' starts (a document's first chunk: h0)

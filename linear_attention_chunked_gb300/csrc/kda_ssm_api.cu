@@ -59,9 +59,11 @@ kda_status check_problem(const kda_ssm_problem* p) {
     return KDA_OK;
 }
 
+// The chunk plan (its bytes first in a saved set, or in the workspace), and what follows.
 struct Regions {
-    size_t status, nchunks, doc_off, doc_order, chunk_tab, sumdt, hs, gs, pBC, pA;
-    size_t head, fwd, bwd_saved, bwd_replay, saved;
+    size_t status, nchunks, doc_off, doc_order, chunk_tab, plan;  // inside the plan; its size
+    size_t sumdt, hs, gs, pBC, pA;                                // inside the workspace
+    size_t head, fwd, bwd_saved, bwd_replay, states, saved;
 };
 
 Regions regions(const kda_ssm_problem* p) {
@@ -75,17 +77,27 @@ Regions regions(const kda_ssm_problem* p) {
     r.doc_off = take(sizeof(int) * size_t(p->N + 1));
     r.doc_order = take(sizeof(int) * size_t(p->N));
     r.chunk_tab = take(sizeof(int4) * nc);
+    r.plan = o;
     r.sumdt = take(nc * p->C * 4);
     r.head = o;
-    r.saved = align256(nc * SSM_SUB * CS * 4);
+    r.states = align256(nc * SSM_SUB * CS * 4);
+    r.saved = r.plan + r.states;
     r.fwd = r.head + align256(nc * CS * 4);  // without a saved set the chunks' states lie behind the header
     r.gs = take(nc * CS * 4);
     r.pBC = take(size_t(p->G) * pl.splits * size_t(p->T) * 2 * p->S * 4);
     r.pA = take(nc * p->C * size_t(p->S + 2) * 4);
     r.bwd_saved = o;
-    r.hs = take(r.saved);  // replay's states
+    r.hs = take(r.states);  // replay's
     r.bwd_replay = o;
     return r;
+}
+
+// the chunk plan at `base`
+void use_plan(SsmArgs& a, const Regions& r, char* base) {
+    a.status = reinterpret_cast<int*>(base + r.status);
+    a.nchunks = reinterpret_cast<int*>(base + r.nchunks);
+    a.doc_off = reinterpret_cast<int*>(base + r.doc_off);
+    a.chunk_tab = reinterpret_cast<int4*>(base + r.chunk_tab);
 }
 
 SsmArgs make_args(const kda_ssm_problem* p, const Regions& r, void* ws) {
@@ -105,10 +117,8 @@ SsmArgs make_args(const kda_ssm_problem* p, const Regions& r, void* ws) {
     a.ldc = ld_or(p->ld_c, GS);
     a.cu = p->cu_seqlens;
     char* w = static_cast<char*>(ws);
-    a.status = reinterpret_cast<int*>(w + r.status);
-    a.nchunks = reinterpret_cast<int*>(w + r.nchunks);
-    a.doc_off = reinterpret_cast<int*>(w + r.doc_off);
-    a.chunk_tab = reinterpret_cast<int4*>(w + r.chunk_tab);
+    a.call_status = static_cast<int*>(ws);
+    use_plan(a, r, w);
     a.sumdt = reinterpret_cast<float*>(w + r.sumdt);
     a.gs = reinterpret_cast<float*>(w + r.gs);
     a.pBC = reinterpret_cast<float*>(w + r.pBC);
@@ -125,7 +135,7 @@ kda_status check_inputs(const kda_ssm_problem* p, const void* u, const void* dt,
     return KDA_OK;
 }
 
-void launch_plan(const SsmArgs& a, const Regions& r, void* ws, cudaStream_t st) {
+void launch_plan(const SsmArgs& a, const Regions& r, cudaStream_t st) {
     Params q{};
     q.T = a.T;
     q.N = a.N;
@@ -134,7 +144,7 @@ void launch_plan(const SsmArgs& a, const Regions& r, void* ws, cudaStream_t st) 
     q.status = a.status;
     q.nchunks = a.nchunks;
     q.doc_off = a.doc_off;
-    q.doc_order = reinterpret_cast<int*>(static_cast<char*>(ws) + r.doc_order);
+    q.doc_order = reinterpret_cast<int*>(reinterpret_cast<char*>(a.status) - r.status + r.doc_order);
     q.chunk_tab = a.chunk_tab;
     ProfScope ps(KK_PLAN, st);
     k_plan<<<1, NTHR, 0, st>>>(q);
@@ -173,11 +183,13 @@ kda_status kda_ssm_fwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     a.u = u, a.dt = dt, a.A = A, a.B = B, a.Cm = Cm, a.D = D_, a.bias = dt_bias, a.z = z, a.h0 = h0;
     a.y = y;
     a.ht = ht;
-    a.hs = static_cast<float*>(saved ? saved : static_cast<char*>(ws) + r.head);
+    // a saved set holds the plan and the states of every 16th token
+    a.hs = reinterpret_cast<float*>(saved ? static_cast<char*>(saved) + r.plan : static_cast<char*>(ws) + r.head);
+    if (saved) use_plan(a, r, static_cast<char*>(saved));
     a.sub = saved ? SSM_SUB : 1;
     // a short prompt (every document within one chunk, few of them): one launch, no plan, no carry
     a.direct = !saved && a.T <= CH && a.N <= 64;
-    if (!a.direct) launch_plan(a, r, ws, st);
+    if (!a.direct) launch_plan(a, r, st);
     launch_ssm_scan(a, p->dtype, st);
     return launched();
 }
@@ -200,10 +212,12 @@ kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     SsmArgs a = make_args(p, r, ws);
     a.u = u, a.dt = dt, a.A = A, a.B = B, a.Cm = Cm, a.D = D_, a.bias = dt_bias, a.z = z, a.h0 = h0;
     a.sub = SSM_SUB;
-    launch_plan(a, r, ws, st);
     if (saved) {
-        a.hs = static_cast<float*>(const_cast<void*>(saved));
+        char* set = static_cast<char*>(const_cast<void*>(saved));
+        use_plan(a, r, set);
+        a.hs = reinterpret_cast<float*>(set + r.plan);
     } else {  // recompute the states (no y, no final state)
+        launch_plan(a, r, st);
         a.hs = reinterpret_cast<float*>(static_cast<char*>(ws) + r.hs);
         launch_ssm_scan(a, p->dtype, st);
     }
@@ -225,7 +239,6 @@ kda_status kda_ssm_step(const kda_ssm_problem* p, const void* u, const void* dt,
     if (!req(h_in) || !req(h_out) || !req(y) || !al(slots, 4) || !opt(ws) || n_slots < 1 ||
         (!slots && n_slots < q.N))
         return KDA_ERR_INVALID_ARG;
-    if ((int64_t(q.C) * 16 + 255) / 256 * q.N > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     const Regions none{};
     const SsmArgs t = make_args(&q, none, ws);
     SsmStepArgs a{q.N, q.C, q.S, q.G, q.dt_softplus, t.ldu, t.lddt, t.ldb, t.ldc, t.ldz, n_slots,

@@ -48,6 +48,7 @@ __device__ __forceinline__ void st4(float* p, int s, int S, float4 v) {
 
 constexpr int CARRY_THREADS = 128;
 __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_rcarry(SsmArgs a, int blocks_per_doc) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.call_status = *a.status;  // (the plan may be a saved one)
     if (*a.status != KDA_OK) return;
     const int n = blockIdx.x / blocks_per_doc;
     const int64_t CS = int64_t(a.C) * a.S;
@@ -447,11 +448,10 @@ __global__ void __launch_bounds__(SSM_THREADS, P == 1 ? 2 : P <= 4 ? 3 : 1) k_ss
 // dB, dC: the channel blocks' sums in order, in runs of SSM_QUAD tiles whatever a block covered
 // (so that a document's gradients do not depend on the rest of its pack)
 template <class E>
-__global__ void k_ssm_reduce_bc(SsmArgs a, SsmBwdPlan pl) {
-    if (*a.status != KDA_OK) return;
+__device__ __forceinline__ void reduce_bc(const SsmArgs& a, const SsmBwdPlan& pl, int block, int blocks) {
     const int64_t n = a.T * a.G * 2 * a.S;
     const int per = pl.nl > 1 ? 1 : SSM_QUAD;
-    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+    for (int64_t i = int64_t(block) * blockDim.x + threadIdx.x; i < n; i += int64_t(blocks) * blockDim.x) {
         const int v = int(i % (2 * a.S));
         const int64_t tg = i / (2 * a.S);
         const int g = int(tg % a.G);
@@ -471,11 +471,10 @@ __global__ void k_ssm_reduce_bc(SsmArgs a, SsmBwdPlan pl) {
 // dA, dD, dbias: the chunks' sums.  32 values x 16 strands of chunks per block; a strand's chunks are added
 // in order, then the strands.
 constexpr int PAR_STRANDS = 16;
-__global__ void __launch_bounds__(32 * PAR_STRANDS) k_ssm_reduce_par(SsmArgs a) {
+__device__ __forceinline__ void reduce_par(const SsmArgs& a, int block) {
     __shared__ float part[PAR_STRANDS][33];
-    if (*a.status != KDA_OK) return;
     const int W = a.S + 2, x = threadIdx.x & 31, st = threadIdx.x >> 5, nc = *a.nchunks;
-    const int64_t n = int64_t(a.C) * W, i = int64_t(blockIdx.x) * 32 + x;
+    const int64_t n = int64_t(a.C) * W, i = int64_t(block) * 32 + x;
     float sum = 0.f;
     if (i < n)
 #pragma unroll 8
@@ -491,6 +490,14 @@ __global__ void __launch_bounds__(32 * PAR_STRANDS) k_ssm_reduce_par(SsmArgs a) 
     else if (a.dbias) a.dbias[c] = sum;
 }
 
+// the first par_blocks blocks take the parameters, the others dB and dC
+template <class E>
+__global__ void __launch_bounds__(32 * PAR_STRANDS) k_ssm_reduce(SsmArgs a, SsmBwdPlan pl, int par_blocks) {
+    if (*a.status != KDA_OK) return;
+    if (int(blockIdx.x) < par_blocks) reduce_par(a, blockIdx.x);
+    else reduce_bc<E>(a, pl, blockIdx.x - par_blocks, gridDim.x - par_blocks);
+}
+
 template <class E, int P>
 void launch_main(const SsmArgs& a, const SsmBwdPlan& pl, cudaStream_t st) {
     const unsigned grid = unsigned(a.maxC * a.G * pl.splits);
@@ -498,16 +505,11 @@ void launch_main(const SsmArgs& a, const SsmBwdPlan& pl, cudaStream_t st) {
         ProfScope ps(KK_SSM_BWD, st);
         k_ssm_bwd<E, P><<<grid, SSM_THREADS, BwdShape<P>::floats * 4, st>>>(a, pl);
     }
-    {
-        ProfScope ps(KK_SSM_REDUCE, st);
-        const int64_t n = a.T * a.G * 2 * a.S, blocks = (n + 255) / 256;
-        if (blocks) k_ssm_reduce_bc<E><<<unsigned(blocks < 8192 ? blocks : 8192), 256, 0, st>>>(a, pl);
-    }
-    {
-        ProfScope ps(KK_SSM_REDUCE, st);
-        const int64_t n = int64_t(a.C) * (a.S + 2);
-        k_ssm_reduce_par<<<unsigned((n + 31) / 32), 32 * PAR_STRANDS, 0, st>>>(a);
-    }
+    constexpr int NT = 32 * PAR_STRANDS;
+    const int64_t n = a.T * a.G * 2 * a.S, bc = (n + NT - 1) / NT;
+    const int par_blocks = int((int64_t(a.C) * (a.S + 2) + 31) / 32);
+    ProfScope ps(KK_SSM_REDUCE, st);
+    k_ssm_reduce<E><<<unsigned(par_blocks + (bc < 4096 ? bc : 4096)), NT, 0, st>>>(a, pl, par_blocks);
 }
 
 template <class E>

@@ -73,6 +73,7 @@ __device__ __forceinline__ void load_A(const SsmArgs& a, int c, int s0, f2 (&A2)
 // start and receives chunk k + 1's start state.
 constexpr int CARRY_THREADS = 128;
 __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_carry(SsmArgs a, int blocks_per_doc) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.call_status = *a.status;  // (the plan may lie in the saved set)
     if (*a.status != KDA_OK) return;
     const int n = blockIdx.x / blocks_per_doc;
     const int64_t CS = int64_t(a.C) * a.S;
@@ -417,10 +418,11 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_small(SsmArgs a, int tiles,
     }
 }
 
-template <class F>
-void small_launch(F* f, int64_t blocks, size_t smem, const SsmArgs& a, int tiles, int direct, cudaStream_t st) {
-    if (smem > 40 * 1024) cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    f<<<unsigned(blocks), SSM_THREADS, smem, st>>>(a, tiles, direct);
+template <auto* F>
+void small_launch(int64_t blocks, size_t smem, const SsmArgs& a, int tiles, int direct, cudaStream_t st) {
+    static unsigned long long done;
+    allow_smem((const void*)F, smem, &done);
+    F<<<unsigned(blocks), SSM_THREADS, smem, st>>>(a, tiles, direct);
 }
 
 int tiles_of(const SsmArgs& a, int CB) {
@@ -440,7 +442,7 @@ void launch(const SsmArgs& a, cudaStream_t st) {
     // 256; state 26.7 / 26.7 at 512, 49 / 43 at 1024; rstate 51 / 59 at 1024, 94 / 96 at 2048
     constexpr int limit = MODE == OUT ? 160 : MODE == STATE ? 512 : 2048;
     if (a.direct || a.maxC * wide < limit)
-        small_launch(k_ssm_small<E, PS, FULL, MODE>, rows * narrow, S::floats * sizeof(float), a, narrow, a.direct, st);
+        small_launch<k_ssm_small<E, PS, FULL, MODE>>(rows * narrow, S::floats * sizeof(float), a, narrow, a.direct, st);
     else
         k_ssm_walk<E, SPT, P, FULL, MODE><<<unsigned(a.maxC * wide), SSM_THREADS, 0, st>>>(a, wide);
 }
