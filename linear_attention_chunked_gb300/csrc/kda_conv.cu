@@ -666,9 +666,10 @@ kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* 
     a.y = y;
     a.status = static_cast<int*>(ws);
     const unsigned gx = unsigned((q.C / 8 + CS_THREADS - 1) / CS_THREADS);
-    // one sequence per thread until the grid holds about four blocks per multiprocessor (152 of
-    // them); then four, and more only to keep the grid's second dimension within its limit
-    a.rpt = int64_t(gx) * q.N < 4 * 608 ? 1 : 4;
+    // one sequence per thread until the 152 multiprocessors hold their four blocks each; then as many as
+    // make one wave (512 x 8192: 19.3 us with four sequences a thread in 1.7 waves, 16.9 us so)
+    const int64_t rpt = (int64_t(gx) * q.N + 607) / 608;
+    a.rpt = int(rpt > 1 ? rpt : 1);
     while ((q.N + a.rpt - 1) / a.rpt > 65535) a.rpt *= 2;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     {
