@@ -349,3 +349,135 @@ def test_conv_step_large_batch_takes_the_same_rows():
     for n in (0, 1, 2, 3, 4, 698, 699):
         y1, o1 = kda.kda_conv_step(x[n:n + 1], w, win[n:n + 1], win_out=torch.empty_like(win[:1]))
         assert torch.equal(y1[0], y[n]) and torch.equal(o1[0], out[n])
+
+
+# ---- forms of the kernels, and long offsets ----
+
+@pytest.mark.parametrize("S,G,dtype", [(1, 1, "fp32"), (4, 2, "bf16"), (7, 1, "fp16"), (16, 1, "bf16"), (24, 3, "fp32"), (64, 1, "bf16")])
+def test_short_prompt_in_one_launch(S, G, dtype):
+    # a pack of at most 64 tokens without a saved set: no plan, no carry; the same bits as with one
+    for h0 in (False, True):
+        a, kw, _, _ = _inputs([5, 0, 1, 37, 0], 12 * G + 3 * G, S, G, dtype, S, h0=h0, strided=True)
+        ra, rk = _ref_args(a, kw)
+        y_ref, ht_ref = ssm.ssm_fwd(**ra, **rk)
+        before = kda.kda_launch_counter()
+        y, ht, _ = kda.kda_ssm_fwd(**a, **kw, save=False)
+        assert kda.kda_launch_counter() == before + 1
+        _close("y", y, y_ref)
+        _close("ht", ht, ht_ref)
+        y2, ht2, _ = kda.kda_ssm_fwd(**a, **kw)
+        assert torch.equal(y, y2) and torch.equal(ht, ht2)
+
+
+def test_short_prompt_with_malformed_offsets():
+    a, kw, _, _ = _inputs([30, 10], 24, 16, 1, "bf16", 11)
+    for cu in ([0, 50, 40], [1, 30, 40], [0, 30, 39], [0, -1, 40]):
+        a["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        ws = torch.empty(kda.kda_ssm_workspace_size(40, 2, 24, 16, 1, kda.KDA_OP_FWD)[0], dtype=torch.uint8, device="cuda")
+        y = torch.full((40, 24), 7.0, dtype=torch.bfloat16, device="cuda")
+        ht = torch.full((2, 24, 16), 7.0, device="cuda")
+        kda.kda_ssm_fwd(**a, **kw, save=False, ws=ws, y=y, ht=ht)
+        assert kda.kda_read_device_status(ws) == kda.KDA_ERR_DEVICE_CHECK
+        assert bool((y == 7).all()) and bool((ht == 7).all())
+
+
+def test_backward_reports_malformed_offsets():
+    a, kw, dy, _ = _inputs([40, 30], 24, 16, 1, "bf16", 12)
+    a["cu_seqlens"] = torch.tensor([0, 80, 70], dtype=torch.int32, device="cuda")
+    _, _, saved = kda.kda_ssm_fwd(**a, **kw)
+    for s, op in ((saved, kda.KDA_OP_BWD_SAVED), (None, kda.KDA_OP_BWD_REPLAY)):
+        ws = torch.empty(kda.kda_ssm_workspace_size(70, 2, 24, 16, 1, op)[0], dtype=torch.uint8, device="cuda")
+        kda.kda_ssm_bwd(**a, dy=dy, saved=s, ws=ws, **kw)
+        assert kda.kda_read_device_status(ws) == kda.KDA_ERR_DEVICE_CHECK
+
+
+def test_a_document_alone_equals_it_in_a_large_pack():
+    # the pack takes the throughput forms (and four channel tiles a block in the backward), the document
+    # alone the latency forms: the same bits
+    lens = [2500, 100, 1900]
+    a, kw, dy, dht = _inputs(lens, 4096, 16, 1, "bf16", 16, h0=True)
+    y, ht, saved = kda.kda_ssm_fwd(**a, **kw)
+    g = kda.kda_ssm_bwd(**a, dy=dy, dht=dht, saved=saved, **kw)
+    s, e = 2500, 2600
+    pa = dict({k: a[k][s:e].contiguous() for k in ("u", "dt", "B", "C")}, A=a["A"], cu_seqlens=torch.tensor([0, 100], dtype=torch.int32, device="cuda"))
+    pk = dict(kw, z=kw["z"][s:e].contiguous(), h0=kw["h0"][1:2].contiguous())
+    y1, h1, saved1 = kda.kda_ssm_fwd(**pa, **pk)
+    g1 = kda.kda_ssm_bwd(**pa, dy=dy[s:e].contiguous(), dht=dht[1:2].contiguous(), saved=saved1, **pk)
+    assert torch.equal(y1, y[s:e]) and torch.equal(h1[0], ht[1])
+    for k in ("du", "ddt", "dB", "dC", "dz"):
+        assert torch.equal(g1[k], g[k][s:e]), k
+    assert torch.equal(g1["dh0"][0], g["dh0"][1])
+
+
+def test_rows_beyond_32_bit_offsets():
+    # 300 rows of one projection 2^23 columns wide: the last rows start past 2^31 elements
+    T, C, S = 300, 24, 16
+    a, kw, dy, _ = _inputs([T], C, S, 1, "bf16", 17)
+    want_y, want_h, _ = kda.kda_ssm_fwd(**a, **kw)
+    want = kda.kda_ssm_bwd(**a, dy=dy, **kw)
+    wide = torch.empty((T, 1 << 23), dtype=torch.bfloat16, device="cuda")
+    at = 0
+    far = {}
+    for name, t in (("u", a["u"]), ("dt", a["dt"]), ("z", kw["z"]), ("B", a["B"]), ("C", a["C"])):
+        n = t[0].numel()
+        wide[:, at:at + n] = t.reshape(T, n)
+        far[name] = wide[:, at:at + n].unflatten(1, t.shape[1:]) if t.dim() > 2 else wide[:, at:at + n]
+        at += n
+    fa, fk = dict(a, **{k: far[k] for k in ("u", "dt", "B", "C")}), dict(kw, z=far["z"])
+    y, h, _ = kda.kda_ssm_fwd(**fa, **fk)
+    assert torch.equal(y, want_y) and torch.equal(h, want_h)
+    g = kda.kda_ssm_bwd(**fa, dy=dy, **fk)
+    assert all(torch.equal(g[k], want[k]) for k in want)
+
+
+def test_slots_beyond_32_bit_offsets():
+    C, S, n = 4096, 16, (1 << 31) // (4096 * 16) + 10  # the last states start past 2^31 elements
+    a, kw, _, _ = _inputs([1, 1], C, S, 1, "bf16", 18, h0=True)
+    h = kw.pop("h0")
+    a.pop("cu_seqlens")
+    y, h1 = kda.kda_ssm_step(**a, h=h, **kw, h_out=torch.empty_like(h))
+    pool = torch.empty((n, C, S), device="cuda")
+    slots = torch.tensor([n - 1, 3], dtype=torch.int32, device="cuda")
+    pool[n - 1], pool[3] = h[0], h[1]
+    y2, _ = kda.kda_ssm_step(**a, h=pool, **kw, slots=slots)
+    assert torch.equal(y2, y) and torch.equal(pool[n - 1], h1[0]) and torch.equal(pool[3], h1[1])
+    del pool
+    m = (1 << 31) // (3 * 8192) + 10
+    x = torch.randn((2, 8192), device="cuda").bfloat16()
+    win, w = torch.randn((2, 3, 8192), device="cuda").bfloat16(), torch.randn((8192, 4), device="cuda")
+    yc, wc = kda.kda_conv_step(x, w, win, win_out=torch.empty_like(win))
+    pool = torch.empty((m, 3, 8192), dtype=torch.bfloat16, device="cuda")
+    pool[m - 1], pool[3] = win[0], win[1]
+    yc2, _ = kda.kda_conv_step(x, w, pool, slots=torch.tensor([m - 1, 3], dtype=torch.int32, device="cuda"))
+    assert torch.equal(yc2, yc) and torch.equal(pool[m - 1], wc[0]) and torch.equal(pool[3], wc[1])
+
+
+@pytest.mark.parametrize("S,C,dtype,G", [(1, 16384, "fp32", 1), (4, 16384, "bf16", 2), (7, 16384, "fp16", 1), (8, 16400, "fp32", 1),
+                                         (12, 16384, "bf16", 4), (16, 16300, "fp32", 1), (16, 16384, "fp16", 1), (24, 8192, "fp32", 1),
+                                         (32, 8192, "bf16", 2), (48, 4096, "fp32", 1), (64, 4096, "bf16", 1)])
+def test_throughput_forms(S, C, dtype, G):
+    # wide enough for the throughput forms of every kernel; the oracle takes the first and last channels of
+    # each group, which alone have gradients (channels meet only in dB and dC)
+    lens = [700, 0, 300]
+    a, kw, dy, _ = _inputs(lens, C, S, G, dtype, S + G)
+    Cg = C // G
+    ch = np.concatenate([np.r_[g * Cg:g * Cg + 5, (g + 1) * Cg - 3:(g + 1) * Cg] for g in range(G)])
+    mask = torch.zeros(C, dtype=dy.dtype, device="cuda")
+    mask[torch.from_numpy(ch).cuda()] = 1
+    dy = dy * mask
+    pick = lambda t: None if t is None else _np(t)[..., ch]  # noqa: E731
+    ra = dict(u=pick(a["u"]), dt=pick(a["dt"]), A=_np(a["A"])[ch], B=_np(a["B"]), Cm=_np(a["C"]), cu_seqlens=a["cu_seqlens"].cpu().numpy())
+    rk = dict(D=pick(kw["D"]), dt_bias=pick(kw["dt_bias"]), z=pick(kw["z"]))
+    y_ref, ht_ref = ssm.ssm_fwd(**ra, **rk)
+    y, ht, saved = kda.kda_ssm_fwd(**a, **kw)
+    idx = torch.from_numpy(ch).cuda()
+    _close("y", y[:, idx], y_ref)
+    _close("ht", ht[:, idx], ht_ref)
+    ref = ssm.ssm_bwd(**ra, dy=_np(dy)[:, ch], **rk)
+    got = kda.kda_ssm_bwd(**a, dy=dy, saved=saved, **kw)
+    for k in ("du", "ddt", "dz", "dD", "ddt_bias"):
+        _close(k, got[k][..., idx], ref[k])
+    _close("dA", got["dA"][idx], ref["dA"])
+    _close("dh0", got["dh0"][:, idx], ref["dh0"])
+    _close("dB", got["dB"], ref["dB"])
+    _close("dC", got["dC"], ref["dC"])
