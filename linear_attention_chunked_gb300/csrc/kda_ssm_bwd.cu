@@ -8,20 +8,25 @@
 //   k_ssm_rstate   per chunk with a predecessor: its start gradient from a zero end (kda_ssm_fwd.cu)
 //   k_ssm_rcarry   per (document, channel, state): the chunks' end gradients, last to first
 //   k_ssm_bwd      per (chunk, channel tile): the gradients
-//   k_ssm_reduce_* the sums over channel tiles (dB, dC) and over chunks (dA, dD, dbias), in order
+//   k_ssm_reduce   the sums over channel tiles (dB, dC) and over chunks (dA, dD, dbias), in a fixed order
 //
 // k_ssm_bwd needs h_{t-1} in reverse.  The forward leaves the state at every 16th token; a unit of 16
 // tokens is swept forward once from there, the states every 4 tokens kept in shared memory, and
 // each run of 4 tokens is recomputed from its start with states and decays in registers and walked
 // backwards.  Four lanes hold a channel's 16 states (four each), and a lane holds two channels, as the two
 // halves of packed arithmetic: the channels' scalars are pairs as they lie, and B and C are read once for
-// both.  The scalars (delta, delta u, dY, u and
-// what the gradients are multiplied with at the end) are computed once per token by lanes laid out as
-// (token, channel pair) items and handed over through shared memory, one unit ahead of their use.  Sums
-// cross lanes by halving (each step a lane gives away half of its values): a channel's three sums over
-// states for 4 tokens leave each of its four lanes with one token, whose du, ddt and dz that lane
-// finishes; the eight dB / dC terms per token, summed over the two channels first, take 7 shuffles
-// over 8 lanes.
+// both.  The scalars (delta, delta u, dY, u and what the gradients are multiplied with at the end) are
+// computed once per token by lanes laid out as (token, channel pair) items and handed over through
+// shared memory, one unit ahead of their use.  Sums cross lanes by halving (each step a lane gives away
+// half of its values): a channel's three sums over states for 4 tokens leave each of its four lanes with
+// one token, whose du, ddt and dz that lane finishes; the eight dB / dC terms per token, summed over the
+// two channels first, take 7 shuffles over 8 lanes.
+//
+// Bound by instruction issue and shared-memory operands together (16384 x 2048 x 16: 760 us, about 29
+// instructions per channel, state and token, half of the issue slots, 12 warps per multiprocessor by
+// registers).  Measured and worse: B and C doubled in shared memory, which saves the copies into
+// pairs (+51 us: the operand reads double); their products as two scalar instructions (+24 us); four
+// blocks per multiprocessor (spills, +380 us); two channel tiles a block (+20 us with the larger reduction).
 #include "kda_ssm.cuh"
 #include "kda_ssm_launch.cuh"
 
@@ -33,9 +38,11 @@ constexpr int RT = 4;           // tokens per run
 constexpr int UT = SSM_UT;      // tokens per unit
 constexpr int NR = UT / RT;     // runs per unit
 constexpr int NW = SSM_THREADS / 32;
-constexpr int SPT = 4;       // states per lane
+constexpr int SPT = 4;          // states per lane
 
-__device__ __forceinline__ float4 ld4(const float* p, int s, int S) {
+// four states from s of a row of S (those past S: zero, unwritten); vec: rows are whole vectors
+__device__ __forceinline__ float4 ld4(const float* p, int s, int S, bool vec) {
+    if (vec) return s < S ? *reinterpret_cast<const float4*>(p + s) : make_float4(0.f, 0.f, 0.f, 0.f);
     return make_float4(s < S ? p[s] : 0.f, s + 1 < S ? p[s + 1] : 0.f, s + 2 < S ? p[s + 2] : 0.f,
                        s + 3 < S ? p[s + 3] : 0.f);
 }
@@ -204,8 +211,8 @@ __global__ void __launch_bounds__(SSM_THREADS, P == 1 ? 2 : P <= 4 ? 3 : 1) k_ss
         const bool on0 = cw + cl < Cg, on1 = cw + cl + CL < Cg;
         f2 A2[SPT], g[SPT], dA[SPT], hs[SPT];
         auto both4 = [&](const float* base, bool mask, float4(&o)[2]) {
-            o[0] = ld4(base + int64_t(c0) * S, s0, !mask || on0 ? S : 0);
-            o[1] = ld4(base + int64_t(c1) * S, s0, !mask || on1 ? S : 0);
+            o[0] = ld4(base + int64_t(c0) * S, s0, !mask || on0 ? S : 0, S % 4 == 0);
+            o[1] = ld4(base + int64_t(c1) * S, s0, !mask || on1 ? S : 0, S % 4 == 0);
         };
         auto paired = [](const float4(&v)[2], f2(&o)[SPT]) {
             o[0] = pk2(v[0].x, v[1].x), o[1] = pk2(v[0].y, v[1].y), o[2] = pk2(v[0].z, v[1].z), o[3] = pk2(v[0].w, v[1].w);
