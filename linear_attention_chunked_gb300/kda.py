@@ -7,6 +7,7 @@ library has not been built this module raises -- there is no fallback of any kin
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -515,7 +516,9 @@ def _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens):
                            None if cu_seqlens is None else cu_seqlens.data_ptr())
 
 
-def _ssm_sizes(pr, op):
+@functools.lru_cache(maxsize=256)  # the sizes are a function of these numbers alone
+def _ssm_sizes(T, N, C, S, G, op):
+    pr = kda_ssm_problem(T, N, C, S, G, KDA_DT_BF16, 1, 0, 0, 0, 0, 0, 16)  # cu_seqlens is not read
     ws, sv = ctypes.c_size_t(0), ctypes.c_size_t(0)
     _check("kda_ssm_workspace_size",
            lib().kda_ssm_workspace_size(ctypes.byref(pr), int(op), ctypes.byref(ws), ctypes.byref(sv)))
@@ -523,9 +526,10 @@ def _ssm_sizes(pr, op):
 
 
 def kda_ssm_workspace_size(T, N, C, S, G, op, *, dtype=torch.bfloat16):
-    """Returns (workspace bytes, saved-set bytes) of the scan's op."""
-    pr = kda_ssm_problem(T, N, C, S, G, _DTYPES[dtype], 1, 0, 0, 0, 0, 0, 16)  # cu_seqlens is not read
-    return _ssm_sizes(pr, op)
+    """Returns (workspace bytes, saved-set bytes) of the scan's op (whatever its type)."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"kda_ssm_workspace_size: dtype is {dtype}, expected one of bfloat16, float16, float32")
+    return _ssm_sizes(T, N, C, S, G, op)
 
 
 def kda_ssm_fwd(u, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, z=None, h0=None,
@@ -537,7 +541,7 @@ def kda_ssm_fwd(u, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, z=None, h0=
     fn = "kda_ssm_fwd"
     N, dev = cu_seqlens.numel() - 1, u.device
     pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens)
-    ws_b, sv_b = _ssm_sizes(pr, KDA_OP_FWD)
+    ws_b, sv_b = _ssm_sizes(pr.T, N, pr.C, pr.S, pr.G, KDA_OP_FWD)
     state = (N, pr.C, pr.S)
     if ws is None:
         ws = _empty_bytes(ws_b, dev)
@@ -574,7 +578,7 @@ def kda_ssm_bwd(u, dt, A, B, C, cu_seqlens, dy, *, saved=None, D=None, dt_bias=N
     _check_tensor(fn, "dy", dy, u.shape, dtype, dev)
     _check_tensor(fn, "h0", h0, state, torch.float32, dev)
     _check_tensor(fn, "dht", dht, state, torch.float32, dev)
-    ws_b, sv_b = _ssm_sizes(pr, KDA_OP_BWD_REPLAY if saved is None else KDA_OP_BWD_SAVED)
+    ws_b, sv_b = _ssm_sizes(pr.T, N, pr.C, pr.S, pr.G, KDA_OP_BWD_REPLAY if saved is None else KDA_OP_BWD_SAVED)
     if saved is not None and saved.numel() * saved.element_size() < sv_b:
         raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
     if ws is None:
@@ -631,6 +635,7 @@ def _layernorm_problem(fn, x, eps):
     return kda_layernorm_problem(x.numel() // max(C, 1), C, _DTYPES[x.dtype], float(eps))
 
 
+@functools.lru_cache(maxsize=256)  # a function of these numbers alone
 def kda_layernorm_workspace_size(T, C, *, dtype=torch.bfloat16):
     pr = kda_layernorm_problem(int(T), int(C), _DTYPES[dtype], 0.0)
     ws = ctypes.c_size_t(0)
