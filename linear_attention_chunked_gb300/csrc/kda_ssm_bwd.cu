@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_rcarry(SsmArgs a, int blo
     float* gs = a.gs + int64_t(k0) * CS + i;
     const float* sd = a.sumdt + int64_t(k0) * a.C + c;
     gs[int64_t(nc - 1) * CS] = g;
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int k = nc - 1; k > 0; k -= U) {
         float e[U], d[U];
         const int m = min(U, k);

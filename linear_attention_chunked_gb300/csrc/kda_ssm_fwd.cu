@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_carry(SsmArgs a, int bloc
     float* hs = a.hs + k0 * hstep + i;
     const float* sd = a.sumdt + int64_t(k0) * a.C + c;
     hs[0] = h;
-    constexpr int U = 8;  // chunks loaded together
+    constexpr int U = 16;  // chunks loaded together (few threads, each a serial walk: latency)
     for (int k = 0; k < k1 - k0 - 1; k += U) {
         float e[U], d[U];
         const int m = min(U, k1 - k0 - 1 - k);
