@@ -14,6 +14,11 @@
 // values.  The backward keeps its columns' dw and db terms in registers over the rows of its walk, and
 // a second kernel adds the blocks' sums in order: results are bitwise reproducible.  Rows too long
 // for the registers take kernels that read them again.
+//
+// Rows whose length is no multiple of a vector (V elements) start inside one.  They are read as the aligned
+// vectors that cover them, the neighbours' elements cleared (SHIFT); a slot's rows are V apart or a
+// multiple of it, so all of them start at the same place in a vector and its columns stay in its
+// registers.
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -50,53 +55,64 @@ template <> __device__ __forceinline__ float ln_cast<float>(float v) { return v;
 template <> __device__ __forceinline__ __nv_bfloat16 ln_cast<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half ln_cast<__half>(float v) { return __float2half_rn(v); }
 
-// Arithmetic on pairs of values (one packed instruction for two), on single values where rows are not
-// whole vectors
-using kda::add2;  // (the single-value forms below would hide the pairs')
-using kda::fma2;
-using kda::mul2;
-__device__ __forceinline__ float mul2(float a, float b) { return __fmul_rn(a, b); }
-__device__ __forceinline__ float add2(float a, float b) { return __fadd_rn(a, b); }
-__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ float total(float v) { return v; }
-__device__ __forceinline__ float total(f2 v) { return hsum2(v); }
-template <int V> struct PairOf { using T = f2; };
-template <> struct PairOf<1> { using T = float; };
-template <int V> using Pair = typename PairOf<V>::T;
-template <int V> __host__ __device__ constexpr int pairs() { return V == 1 ? 1 : V / 2; }
-template <int V> __device__ __forceinline__ Pair<V> both(float x) {
-    if constexpr (V == 1) return x;
-    else return pk2(x, x);
-}
 // pair j of a vector
 template <class E, int V>
-__device__ __forceinline__ Pair<V> ln_get(const Vec<E, V>& v, int j) {
-    if constexpr (V == 1) return ssm_f<E>(v.e[0]);
-    else return pk2(ssm_f<E>(v.e[2 * j]), ssm_f<E>(v.e[2 * j + 1]));
+__device__ __forceinline__ f2 ln_get(const Vec<E, V>& v, int j) {
+    return pk2(ssm_f<E>(v.e[2 * j]), ssm_f<E>(v.e[2 * j + 1]));
 }
 template <class E, int V>
-__device__ __forceinline__ void ln_put(Vec<E, V>& v, int j, Pair<V> x) {
-    if constexpr (V == 1) {
-        v.e[0] = ln_cast<E>(x);
+__device__ __forceinline__ void ln_put(Vec<E, V>& v, int j, f2 x) {
+    float p, q;
+    up2(x, p, q);
+    v.e[2 * j] = ln_cast<E>(p);
+    v.e[2 * j + 1] = ln_cast<E>(q);
+}
+__device__ __forceinline__ f2 both(float x) { return pk2(x, x); }
+__device__ __forceinline__ f2 ln_mul_rn(f2 a, f2 b) {
+    float p, q, r, t;
+    up2(a, p, q);
+    up2(b, r, t);
+    return pk2(__fmul_rn(p, r), __fmul_rn(q, t));
+}
+// whether the V columns from cb (negative, or reaching past C, at a row's ends) hold a neighbour's elements
+template <int V> __device__ __forceinline__ bool ln_edge(int cb, int C) { return cb < 0 || cb + V > C; }
+template <class E, int V>
+__device__ __forceinline__ void ln_clip(Vec<E, V>& v, int cb, int C) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (cb + j < 0 || cb + j >= C) v.e[j] = ln_cast<E>(0.f);
+}
+__device__ __forceinline__ f2 ln_inside(f2 v, int c, int C) {
+    float p, q;
+    up2(v, p, q);
+    return pk2(c >= 0 && c < C ? p : 0.f, c + 1 >= 0 && c + 1 < C ? q : 0.f);
+}
+template <class E, int V, bool SHIFT>
+__device__ __forceinline__ void ln_store_row(void* p, int64_t row0, int cb, int C, const Vec<E, V>& v) {
+    if (SHIFT && ln_edge<V>(cb, C)) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (cb + j >= 0 && cb + j < C) static_cast<E*>(p)[row0 + cb + j] = v.e[j];
     } else {
-        float p, q;
-        up2(x, p, q);
-        v.e[2 * j] = ln_cast<E>(p);
-        v.e[2 * j + 1] = ln_cast<E>(q);
+        ln_store<E, V>(p, row0 + cb, v);
     }
 }
-// V consecutive fp32 parameters, `none` where there are none
-template <int V>
-__device__ __forceinline__ void ln_par(const float* p, int c, Pair<V> (&o)[pairs<V>()], float none) {
+// V fp32 parameters from column cb, `none` where there are none
+template <int V, bool SHIFT>
+__device__ __forceinline__ void ln_par(const float* p, int cb, int C, f2 (&o)[V / 2], float none) {
     if (!p) {
 #pragma unroll
-        for (int j = 0; j < pairs<V>(); ++j) o[j] = both<V>(none);
-    } else if constexpr (V == 1) {
-        o[0] = p[c];
+        for (int j = 0; j < V / 2; ++j) o[j] = both(none);
+    } else if (SHIFT) {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = cb + j >= 0 && cb + j < C ? p[cb + j] : 0.f;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) o[j] = pk2(f[2 * j], f[2 * j + 1]);
     } else {
 #pragma unroll
         for (int j = 0; j < V / 2; j += 2) {
-            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + c + 2 * j);
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + cb + 2 * j);
             o[j] = t.x, o[j + 1] = t.y;
         }
     }
@@ -135,27 +151,34 @@ template <int NT> __host__ __device__ constexpr int ln_blocks() { return 512 / l
 template <int NT> __host__ __device__ constexpr int ln_budget() { return 200 * 1024 / ln_blocks<NT>(); }
 // Rows of a walk are taken R at a time (their sums cross the block together), D - 1 such steps ahead
 template <int V, int K, int NT, int M> __host__ __device__ constexpr int ln_rows() {
-    return V > 1 && K * V <= 16 && 4 * M * K * ln_block<NT>() * 16 <= ln_budget<NT>() ? 2 : 1;
+    return K * V <= 16 && 4 * M * K * ln_block<NT>() * 16 <= ln_budget<NT>() ? 2 : 1;
 }
 template <int V, int K, int NT, int M> __host__ __device__ constexpr int ln_depth() {
     const int d = ln_budget<NT>() / (M * ln_rows<V, K, NT, M>() * K * ln_block<NT>() * 16);
     return d < 2 ? 2 : d > 4 ? 4 : d;
 }
 template <int V, int K, int NT, int M> constexpr size_t ln_ring_bytes() {
-    return V > 1 ? size_t(ln_depth<V, K, NT, M>()) * M * ln_rows<V, K, NT, M>() * K * ln_block<NT>() * 16 : 0;
+    return size_t(ln_depth<V, K, NT, M>()) * M * ln_rows<V, K, NT, M>() * K * ln_block<NT>() * 16;
+}
+
+// Copies the vector at element i of a tensor of n; SHIFT: the last one may end past it (cleared there)
+template <class E, int V, bool SHIFT>
+__device__ __forceinline__ void ln_copy(uint4* smem, const E* src, int64_t i, int64_t n) {
+    const int bytes = SHIFT && n - i < V ? int(n - i) * int(sizeof(E)) : 16;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(smem)), "l"(src + i), "r"(bytes) : "memory");
 }
 
 // A thread's vectors of M tensors' rows, step by step: step i covers rows row0 + (i R + r) stride
-template <class E, int V, int K, int NT, int M>
+template <class E, int V, int K, int NT, int M, bool SHIFT>
 struct Ring {
     static constexpr int R = ln_rows<V, K, NT, M>(), D = ln_depth<V, K, NT, M>();
     uint4* mine;  // this thread's first vector
     const E* src[M];
     int64_t row, stride, T;
-    int C, tid, d = 0;
+    int C, tid, sh, d = 0;
     __device__ __forceinline__ Ring(uint4* smem, const void* const (&t)[M], int tid_, int64_t row0, int64_t stride_,
-                                    int64_t T_, int C_)
-        : mine(smem + threadIdx.x), row(row0), stride(stride_), T(T_), C(C_), tid(tid_) {
+                                    int64_t T_, int C_, int sh_)
+        : mine(smem + threadIdx.x), row(row0), stride(stride_), T(T_), C(C_), tid(tid_), sh(sh_) {
 #pragma unroll
         for (int m = 0; m < M; ++m) src[m] = static_cast<const E*>(t[m]);
 #pragma unroll
@@ -172,8 +195,8 @@ struct Ring {
                 for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
-                        const int c = (k * NT + tid) * V;
-                        if (c < C) cp16(reinterpret_cast<void*>(at(d, r, m, k)), src[m] + row * C + c);
+                        const int cb = (k * NT + tid) * V - sh;
+                        if (cb < C) ln_copy<E, V, SHIFT>(at(d, r, m, k), src[m], row * C + cb, T * C);
                     }
         cp_commit();
         d = d + 1 == D ? 0 : d + 1;
@@ -192,31 +215,32 @@ struct Ring {
 };
 
 // Forward over the rows slot, slot + parts, .. of a slot (a block, or a warp where a row takes one)
-template <class E, int V, int K, int NT, bool RES>
+template <class E, int V, int K, int NT, bool RES, bool SHIFT>
 __global__ void __launch_bounds__(ln_block<NT>(), ln_blocks<NT>()) k_ln_fwd_walk(LnArgs a) {
     extern __shared__ __align__(16) uint4 ring_smem[];
-    constexpr int M = RES ? 2 : 1, H = pairs<V>();
-    using P = Pair<V>;
-    using Rg = Ring<E, V, K, NT, M>;
+    constexpr int M = RES ? 2 : 1, H = V / 2;
+    using P = f2;
+    using Rg = Ring<E, V, K, NT, M, SHIFT>;
     constexpr int R = Rg::R;
     __shared__ __align__(16) float buf[2][2][NT / 32][R];
     const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int slot = NT == 32 ? blockIdx.x * LN_WARP_ROWS + (threadIdx.x >> 5) : blockIdx.x;
     if (NT == 32 && slot >= a.parts) return;
     const float inv = 1.f / float(a.C);
+    const int sh = SHIFT ? int(int64_t(slot) * a.C % V) : 0;
     P w[K][H], b[K][H];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * NT + tid) * V;
-        if (c < a.C) {
-            ln_par<V>(a.w, c, w[k], 1.f);
-            ln_par<V>(a.b, c, b[k], 0.f);
+        const int cb = (k * NT + tid) * V - sh;
+        if (cb < a.C) {
+            ln_par<V, SHIFT>(a.w, cb, a.C, w[k], 1.f);
+            ln_par<V, SHIFT>(a.b, cb, a.C, b[k], 0.f);
         }
     }
     const void* src[M];
     src[0] = a.x;
     if (RES) src[M - 1] = a.res;
-    Rg ring(ring_smem, src, tid, slot, a.parts, a.T, a.C);
+    Rg ring(ring_smem, src, tid, slot, a.parts, a.T, a.C, sh);
     int odd = 0;
     for (int64_t row0 = slot; row0 < a.T; row0 += int64_t(R) * a.parts, odd ^= 1) {
         ring.turn();
@@ -225,18 +249,19 @@ __global__ void __launch_bounds__(ln_block<NT>(), ln_blocks<NT>()) k_ln_fwd_walk
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = row0 + r * int64_t(a.parts);
-            P sum = both<V>(0.f);
+            P sum = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + tid) * V;
-                if (c < a.C && row < a.T) {
+                const int cb = (k * NT + tid) * V - sh;
+                if (cb < a.C && row < a.T) {
                     Vec<E, V> v = ring.get(r, 0, k);
                     if (RES) {
                         const Vec<E, V> q = ring.get(r, M - 1, k);
 #pragma unroll
                         for (int j = 0; j < H; ++j) ln_put<E, V>(v, j, add2(ln_get<E, V>(v, j), ln_get<E, V>(q, j)));
-                        if (a.sum) ln_store<E, V>(a.sum, row * a.C + c, v);
+                        if (a.sum) ln_store_row<E, V, SHIFT>(a.sum, row * a.C, cb, a.C, v);
                     }
+                    if (SHIFT && ln_edge<V>(cb, a.C)) ln_clip<E, V>(v, cb, a.C);
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         f[r][k][j] = ln_get<E, V>(v, j);
@@ -244,23 +269,26 @@ __global__ void __launch_bounds__(ln_block<NT>(), ln_blocks<NT>()) k_ln_fwd_walk
                     }
                 }
             }
-            mean[r] = total(sum);
+            mean[r] = hsum2(sum);
         }
         row_sums<NT, R>(mean, buf[odd][0]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mean[r] *= inv;
-            P sq = both<V>(0.f);
-            const P neg = both<V>(-mean[r]);
+            P sq = 0;
+            const P neg = both(-mean[r]);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if ((k * NT + tid) * V < a.C)
+            for (int k = 0; k < K; ++k) {
+                const int cb = (k * NT + tid) * V - sh;
+                if (cb < a.C)
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         f[r][k][j] = add2(f[r][k][j], neg);
+                        if (SHIFT) f[r][k][j] = ln_inside(f[r][k][j], cb + 2 * j, a.C);
                         sq = fma2(f[r][k][j], f[r][k][j], sq);
                     }
-            rstd[r] = total(sq);
+            }
+            rstd[r] = hsum2(sq);
         }
         row_sums<NT, R>(rstd, buf[odd][1]);
 #pragma unroll
@@ -272,15 +300,15 @@ __global__ void __launch_bounds__(ln_block<NT>(), ln_blocks<NT>()) k_ln_fwd_walk
                 if (a.mean) a.mean[row] = mean[r];
                 if (a.rstd) a.rstd[row] = rstd[r];
             }
-            const P rs = both<V>(rstd[r]);
+            const P rs = both(rstd[r]);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + tid) * V;
-                if (c < a.C) {
+                const int cb = (k * NT + tid) * V - sh;
+                if (cb < a.C) {
                     Vec<E, V> y;
 #pragma unroll
                     for (int j = 0; j < H; ++j) ln_put<E, V>(y, j, fma2(mul2(f[r][k][j], rs), w[k][j], b[k][j]));
-                    ln_store<E, V>(a.y, row * a.C + c, y);
+                    ln_store_row<E, V, SHIFT>(a.y, row * a.C, cb, a.C, y);
                 }
             }
         }
@@ -288,61 +316,38 @@ __global__ void __launch_bounds__(ln_block<NT>(), ln_blocks<NT>()) k_ln_fwd_walk
     cp_wait<0>();
 }
 
-// Plain loads into registers in the ring's place (rows that are not whole vectors)
-template <class E, int V, int K, int NT, int M>
-struct Direct {
-    static constexpr int R = 1;
-    const E* src[M];
-    Vec<E, V> v[M][K];
-    int64_t row, stride;
-    int C, tid;
-    __device__ __forceinline__ Direct(uint4*, const void* const (&t)[M], int tid_, int64_t row0, int64_t stride_, int64_t, int C_)
-        : row(row0 - stride_), stride(stride_), C(C_), tid(tid_) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) src[m] = static_cast<const E*>(t[m]);
-    }
-    __device__ __forceinline__ void turn() {
-        row += stride;
-#pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if ((k * NT + tid) * V < C) v[m][k] = ln_load<E, V>(src[m], row * C + (k * NT + tid) * V);
-    }
-    __device__ __forceinline__ Vec<E, V> get(int, int m, int k) { return v[m][k]; }
-};
-template <class E, int V, int K, int NT, int M> struct RowsOf { using T = Ring<E, V, K, NT, M>; };
-template <class E, int K, int NT, int M> struct RowsOf<E, 1, K, NT, M> { using T = Direct<E, 1, K, NT, M>; };
-
-// Backward over the rows of a slot.  Whole-vector rows are read from the ring twice, before and after
-// the exchange of their sums, and hold no registers across it.
-template <class E, int V, int K, int NT, bool DSUM>
-__global__ void __launch_bounds__(ln_block<NT>(), V > 1 ? ln_blocks<NT>() : 1) k_ln_bwd(LnArgs a) {
+// Backward over the rows of a slot.  The rows are read from the ring twice, before and after the exchange
+// of their sums, and hold no registers across it.
+template <class E, int V, int K, int NT, bool DSUM, bool SHIFT>
+__global__ void __launch_bounds__(ln_block<NT>(), ln_blocks<NT>()) k_ln_bwd(LnArgs a) {
     extern __shared__ __align__(16) uint4 ring_smem[];
-    constexpr int M = DSUM ? 3 : 2, H = pairs<V>();
-    using P = Pair<V>;
-    using Rg = typename RowsOf<E, V, K, NT, M>::T;
+    constexpr int M = DSUM ? 3 : 2, H = V / 2;
+    using P = f2;
+    using Rg = Ring<E, V, K, NT, M, SHIFT>;
     constexpr int R = Rg::R;
     constexpr bool HOLD = K * V <= 16;  // w in registers over the walk
     __shared__ __align__(16) float buf[2][NT / 32][2 * R];
     const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int slot = NT == 32 ? blockIdx.x * LN_WARP_ROWS + (threadIdx.x >> 5) : blockIdx.x;
     if (NT == 32 && slot >= a.parts) return;
+    const int sh = SHIFT ? int(int64_t(slot) * a.C % V) : 0;
     const float inv = 1.f / float(a.C);
     P dw[K][H], db[K][H], wh[HOLD ? K : 1][H];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < H; ++j) dw[k][j] = db[k][j] = both<V>(0.f);
+        for (int j = 0; j < H; ++j) dw[k][j] = db[k][j] = 0;
     if constexpr (HOLD)
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if ((k * NT + tid) * V < a.C) ln_par<V>(a.w, (k * NT + tid) * V, wh[k], 1.f);
+        for (int k = 0; k < K; ++k) {
+            const int cb = (k * NT + tid) * V - sh;
+            if (cb < a.C) ln_par<V, SHIFT>(a.w, cb, a.C, wh[k], 1.f);
+        }
     const void* src[M];
     src[0] = a.x;
     src[1] = a.dy;
     if (DSUM) src[M - 1] = a.dsum;
-    Rg rows(ring_smem, src, tid, slot, a.parts, a.T, a.C);
+    Rg rows(ring_smem, src, tid, slot, a.parts, a.T, a.C, sh);
     float nm[R], nr[R];  // the next step's statistics
     auto stats = [&](int64_t row0) {
 #pragma unroll
@@ -360,19 +365,28 @@ __global__ void __launch_bounds__(ln_block<NT>(), V > 1 ? ln_blocks<NT>() : 1) k
 #pragma unroll
         for (int r = 0; r < R; ++r) m[r] = nm[r], rs[r] = nr[r];
         stats(row0 + int64_t(R) * a.parts);
+        // x and dy of row r, vector k (the neighbours' elements zero: they add nothing to any sum)
+        auto get2 = [&](int r, int k, int cb, Vec<E, V>& x, Vec<E, V>& g) {
+            x = rows.get(r, 0, k), g = rows.get(r, 1, k);
+            if (SHIFT && ln_edge<V>(cb, a.C)) {
+                ln_clip<E, V>(x, cb, a.C);
+                ln_clip<E, V>(g, cb, a.C);
+            }
+        };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             s[2 * r] = s[2 * r + 1] = 0.f;
             if (row0 + r * int64_t(a.parts) >= a.T) continue;
-            const P rr = both<V>(rs[r]), mr = both<V>(-m[r]);
-            P s0 = both<V>(0.f), s1 = s0;
+            const P rr = both(rs[r]), mr = both(-m[r]);
+            P s0 = 0, s1 = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + tid) * V;
-                if (c < a.C) {
-                    const Vec<E, V> x = rows.get(r, 0, k), g = rows.get(r, 1, k);
+                const int cb = (k * NT + tid) * V - sh;
+                if (cb < a.C) {
+                    Vec<E, V> x, g;
+                    get2(r, k, cb, x, g);
                     P wl[H];
-                    if constexpr (!HOLD) ln_par<V>(a.w, c, wl, 1.f);
+                    if constexpr (!HOLD) ln_par<V, SHIFT>(a.w, cb, a.C, wl, 1.f);
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         const P xh = mul2(add2(ln_get<E, V>(x, j), mr), rr), q = ln_get<E, V>(g, j);
@@ -384,52 +398,61 @@ __global__ void __launch_bounds__(ln_block<NT>(), V > 1 ? ln_blocks<NT>() : 1) k
                     }
                 }
             }
-            s[2 * r] = total(s0);
-            s[2 * r + 1] = total(s1);
+            s[2 * r] = hsum2(s0);
+            s[2 * r + 1] = hsum2(s1);
         }
         row_sums<NT, 2 * R>(s, buf[odd]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = row0 + r * int64_t(a.parts);
             if (row >= a.T) break;
-            const P rr = both<V>(rs[r]), mr = both<V>(-m[r]);
-            const P n0 = both<V>(-(s[2 * r] * inv)), n1 = both<V>(-(s[2 * r + 1] * inv) * rs[r]);
+            const P rr = both(rs[r]), mr = both(-m[r]);
+            const P n0 = both(-(s[2 * r] * inv)), n1 = both(-(s[2 * r + 1] * inv) * rs[r]);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + tid) * V;
-                if (c < a.C) {
+                const int cb = (k * NT + tid) * V - sh;
+                if (cb < a.C) {
                     const Vec<E, V> x = rows.get(r, 0, k), g = rows.get(r, 1, k);
                     Vec<E, V> e, o;
                     if (DSUM) e = rows.get(r, M - 1, k);
                     P wl[H];
-                    if constexpr (!HOLD) ln_par<V>(a.w, c, wl, 1.f);
+                    if constexpr (!HOLD) ln_par<V, SHIFT>(a.w, cb, a.C, wl, 1.f);
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         const P xh = mul2(add2(ln_get<E, V>(x, j), mr), rr);
-                        const P d = mul2(ln_get<E, V>(g, j), HOLD ? wh[HOLD ? k : 0][j] : wl[j]);
+                        // SHIFT: the product as it was summed, unfused with the difference below (a row of one
+                        // element has exactly no gradient)
+                        const P q = ln_get<E, V>(g, j), wj = HOLD ? wh[HOLD ? k : 0][j] : wl[j];
+                        const P d = SHIFT ? ln_mul_rn(q, wj) : mul2(q, wj);
                         P t = fma2(xh, n1, mul2(add2(d, n0), rr));  // rstd (d - mean d - xh mean(d xh))
                         if (DSUM) t = add2(t, ln_get<E, V>(e, j));
                         ln_put<E, V>(o, j, t);
                     }
-                    ln_store<E, V>(a.dx, row * a.C + c, o);
+                    ln_store_row<E, V, SHIFT>(a.dx, row * a.C, cb, a.C, o);
                 }
             }
         }
     }
-    if constexpr (V > 1) cp_wait<0>();
+    cp_wait<0>();
     float* p = a.part + int64_t(slot) * 2 * a.C;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * NT + tid) * V;
-        if (c < a.C)
+        const int cb = (k * NT + tid) * V - sh;
+        if (cb < a.C)
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                if constexpr (V > 1) {
-                    *reinterpret_cast<P*>(p + c + 2 * j) = dw[k][j];
-                    *reinterpret_cast<P*>(p + a.C + c + 2 * j) = db[k][j];
+                if (SHIFT) {
+                    float u[2], v[2];
+                    up2(dw[k][j], u[0], u[1]);
+                    up2(db[k][j], v[0], v[1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = cb + 2 * j + i;
+                        if (c >= 0 && c < a.C) p[c] = u[i], p[a.C + c] = v[i];
+                    }
                 } else {
-                    p[c] = dw[k][0];
-                    p[a.C + c] = db[k][0];
+                    *reinterpret_cast<f2*>(p + cb + 2 * j) = dw[k][j];
+                    *reinterpret_cast<f2*>(p + a.C + cb + 2 * j) = db[k][j];
                 }
             }
     }
@@ -459,28 +482,39 @@ __global__ void __launch_bounds__(1024) k_ln_reduce(LnArgs a, float* dw, float* 
 
 // ---- few rows: one per block (or warp) ----
 
-template <class E, int V, int K, int NT>
+template <class E, int V, int K, int NT, bool SHIFT>
 __global__ void __launch_bounds__(ln_block<NT>()) k_ln_fwd(LnArgs a) {
-    constexpr int H = pairs<V>();
-    using P = Pair<V>;
+    constexpr int H = V / 2;
+    using P = f2;
     __shared__ float buf[2][NT / 32][1];
     const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int64_t row = NT == 32 ? int64_t(blockIdx.x) * LN_WARP_ROWS + (threadIdx.x >> 5) : blockIdx.x;
     if (NT == 32 && row >= a.T) return;
-    const int64_t base = row * a.C;
+    const int64_t base = row * a.C, all = a.T * a.C;
+    const int sh = SHIFT ? int(base % V) : 0;
     const float inv = 1.f / float(a.C);
-    P f[K][H], s = both<V>(0.f);
+    auto load = [&](const void* p, int cb) {
+        if (SHIFT && base + cb + V > all) {  // the tensor's last vector
+            Vec<E, V> v;
+#pragma unroll
+            for (int j = 0; j < V; ++j) v.e[j] = base + cb + j < all ? static_cast<const E*>(p)[base + cb + j] : ln_cast<E>(0.f);
+            return v;
+        }
+        return ln_load<E, V>(p, base + cb);
+    };
+    P f[K][H], s = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * NT + tid) * V;
-        if (c < a.C) {
-            Vec<E, V> x = ln_load<E, V>(a.x, base + c);
+        const int cb = (k * NT + tid) * V - sh;
+        if (cb < a.C) {
+            Vec<E, V> x = load(a.x, cb);
             if (a.res) {
-                const Vec<E, V> r = ln_load<E, V>(a.res, base + c);
+                const Vec<E, V> r = load(a.res, cb);
 #pragma unroll
                 for (int j = 0; j < H; ++j) ln_put<E, V>(x, j, add2(ln_get<E, V>(x, j), ln_get<E, V>(r, j)));
-                if (a.sum) ln_store<E, V>(a.sum, base + c, x);
+                if (a.sum) ln_store_row<E, V, SHIFT>(a.sum, base, cb, a.C, x);
             }
+            if (SHIFT && ln_edge<V>(cb, a.C)) ln_clip<E, V>(x, cb, a.C);
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 f[k][j] = ln_get<E, V>(x, j);
@@ -488,19 +522,22 @@ __global__ void __launch_bounds__(ln_block<NT>()) k_ln_fwd(LnArgs a) {
             }
         }
     }
-    float mean[1] = {total(s)}, rstd[1];
+    float mean[1] = {hsum2(s)}, rstd[1];
     row_sums<NT, 1>(mean, buf[0]);
     mean[0] *= inv;
-    s = both<V>(0.f);
+    s = 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if ((k * NT + tid) * V < a.C)
+    for (int k = 0; k < K; ++k) {
+        const int cb = (k * NT + tid) * V - sh;
+        if (cb < a.C)
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                f[k][j] = add2(f[k][j], both<V>(-mean[0]));
+                f[k][j] = add2(f[k][j], both(-mean[0]));
+                if (SHIFT) f[k][j] = ln_inside(f[k][j], cb + 2 * j, a.C);
                 s = fma2(f[k][j], f[k][j], s);
             }
-    rstd[0] = total(s);
+    }
+    rstd[0] = hsum2(s);
     row_sums<NT, 1>(rstd, buf[1]);
     rstd[0] = rsqrtf(rstd[0] * inv + a.eps);
     if (tid == 0) {
@@ -509,15 +546,15 @@ __global__ void __launch_bounds__(ln_block<NT>()) k_ln_fwd(LnArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * NT + tid) * V;
-        if (c < a.C) {
+        const int cb = (k * NT + tid) * V - sh;
+        if (cb < a.C) {
             P w[H], b[H];
-            ln_par<V>(a.w, c, w, 1.f);
-            ln_par<V>(a.b, c, b, 0.f);
+            ln_par<V, SHIFT>(a.w, cb, a.C, w, 1.f);
+            ln_par<V, SHIFT>(a.b, cb, a.C, b, 0.f);
             Vec<E, V> y;
 #pragma unroll
-            for (int j = 0; j < H; ++j) ln_put<E, V>(y, j, fma2(mul2(f[k][j], both<V>(rstd[0])), w[j], b[j]));
-            ln_store<E, V>(a.y, base + c, y);
+            for (int j = 0; j < H; ++j) ln_put<E, V>(y, j, fma2(mul2(f[k][j], both(rstd[0])), w[j], b[j]));
+            ln_store_row<E, V, SHIFT>(a.y, base, cb, a.C, y);
         }
     }
 }
@@ -604,30 +641,29 @@ __global__ void __launch_bounds__(256) k_ln_cols_long(LnArgs a) {
 // ---- dispatch ----
 
 // Threads per row and vectors per thread by the row's length in vectors: the fewest threads whose
-// registers hold the row.  wide: rows are whole 16-byte vectors.  nt = 0: the re-reading kernels.  Of
-// the 1024-vector rows (16384 x 8192 bf16), the forward takes 91 us with 256 threads of four vectors
-// and 99 with 512 of two; the backward, whose accumulators are twice as many, 186 and 145.
-struct Shape { int nt, k; bool wide; };
+// registers hold the row.  shift: rows start inside vectors (up to V - 1 elements in, so that one
+// more may be needed).  nt = 0: the re-reading kernels.  Of the 1024-vector rows (16384 x 8192 bf16), the
+// forward takes 91 us with 256 threads of four vectors and 99 with 512 of two; the backward, whose
+// accumulators are twice as many, 186 and 145.
+struct Shape { int nt, k; bool shift; };
 Shape shape_of(int C, int esize, bool back) {
     const int V = 16 / esize;
-    if (C % V == 0) {
-        const Shape wide[] = {{32, 1, true}, {32, 2, true}, {128, 1, true}, {128, 2, true}, {256, 2, true},
-                              back ? Shape{512, 2, true} : Shape{256, 4, true}, {512, 4, true}};
-        for (const Shape& s : wide)
-            if (C / V <= s.nt * s.k) return s;
-        return {0, 0, true};
-    }
-    for (int nt : {32, 128, 512})
-        if (C <= nt * 16) return {nt, 16, false};
-    return {0, 0, false};
+    const bool shift = C % V != 0;
+    const int n = shift ? (C + V - 1 + V - 1) / V : C / V;
+    const int shapes[][2] = {{32, 1}, {32, 2}, {128, 1}, {128, 2}, {256, 2}, {back ? 512 : 256, back ? 2 : 4}, {512, 4}};
+    for (const auto& s : shapes)
+        if (n <= s[0] * s[1]) return {s[0], s[1], shift};
+    return {0, 0, shift};
 }
 
 // Slots of a walk: as many blocks as the machine's 152 multiprocessors hold at once (rows of a warp go
-// four to a block), with at least two rows each
+// four to a block), with at least two rows each; a multiple of 8, the largest V, so that a slot's rows
+// start alike
 int parts_of(int64_t T, const Shape& s) {
     const int slots = s.nt ? 152 * (512 / s.nt) : 32;
     const int64_t want = s.nt ? (T + 1) / 2 : T;
-    return int(want < 1 ? 1 : want < slots ? want : slots);
+    const int parts = int(want < 1 ? 1 : want < slots ? want : slots);
+    return s.nt && s.shift ? (parts + 7) / 8 * 8 : parts;
 }
 
 template <auto* F>
@@ -637,34 +673,32 @@ void ring_launch(unsigned blocks, int threads, size_t smem, const LnArgs& a, cud
     F<<<blocks, threads, smem, st>>>(a);
 }
 
-template <class E, int V, int K, int NT>
+template <class E, int V, int K, int NT, bool SHIFT>
 void fwd(LnArgs a, const Shape& s, cudaStream_t st) {
     // a walk pays off from four rows per slot on; fewer rows spread one per block (or warp)
     const int parts = parts_of(a.T, s);
-    if constexpr (V > 1) {
-        if (a.T >= 4 * int64_t(parts)) {
-            a.parts = parts;
-            const unsigned blocks = unsigned(NT == 32 ? (parts + LN_WARP_ROWS - 1) / LN_WARP_ROWS : parts);
-            if (a.res) ring_launch<k_ln_fwd_walk<E, V, K, NT, true>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
-            else ring_launch<k_ln_fwd_walk<E, V, K, NT, false>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 1>(), a, st);
-            return;
-        }
+    if (a.T >= 4 * int64_t(parts)) {
+        a.parts = parts;
+        const unsigned blocks = unsigned(NT == 32 ? (parts + LN_WARP_ROWS - 1) / LN_WARP_ROWS : parts);
+        if (a.res) ring_launch<k_ln_fwd_walk<E, V, K, NT, true, SHIFT>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
+        else ring_launch<k_ln_fwd_walk<E, V, K, NT, false, SHIFT>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 1>(), a, st);
+        return;
     }
     const int64_t blocks = NT == 32 ? (a.T + LN_WARP_ROWS - 1) / LN_WARP_ROWS : a.T;
-    k_ln_fwd<E, V, K, NT><<<unsigned(blocks), ln_block<NT>(), 0, st>>>(a);
+    k_ln_fwd<E, V, K, NT, SHIFT><<<unsigned(blocks), ln_block<NT>(), 0, st>>>(a);
 }
-template <class E, int V, int K, int NT>
+template <class E, int V, int K, int NT, bool SHIFT>
 void bwd(const LnArgs& a, cudaStream_t st) {
     const unsigned blocks = unsigned(NT == 32 ? (a.parts + LN_WARP_ROWS - 1) / LN_WARP_ROWS : a.parts);
-    if (a.dsum) ring_launch<k_ln_bwd<E, V, K, NT, true>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 3>(), a, st);
-    else ring_launch<k_ln_bwd<E, V, K, NT, false>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
+    if (a.dsum) ring_launch<k_ln_bwd<E, V, K, NT, true, SHIFT>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 3>(), a, st);
+    else ring_launch<k_ln_bwd<E, V, K, NT, false, SHIFT>>(blocks, ln_block<NT>(), ln_ring_bytes<V, K, NT, 2>(), a, st);
 }
 template <class E, int V, int K, int NT>
 void run(const LnArgs& a, const Shape& s, bool back, cudaStream_t st) {
     if (back) {
-        if constexpr (NT != 256 || K != 4) bwd<E, V, K, NT>(a, st);
+        if constexpr (NT != 256 || K != 4) s.shift ? bwd<E, V, K, NT, true>(a, st) : bwd<E, V, K, NT, false>(a, st);
     } else {
-        if constexpr (NT != 512 || K != 2) fwd<E, V, K, NT>(a, s, st);
+        if constexpr (NT != 512 || K != 2) s.shift ? fwd<E, V, K, NT, true>(a, s, st) : fwd<E, V, K, NT, false>(a, s, st);
     }
 }
 template <class E>
@@ -677,10 +711,6 @@ void by_shape(const LnArgs& a, const Shape& s, bool back, cudaStream_t st) {
             k_ln_bwd_long<E><<<unsigned(a.T), LONG_NT, 0, st>>>(a);
             k_ln_cols_long<E><<<dim3(unsigned((a.C + 255) / 256), unsigned(a.parts)), 256, 0, st>>>(a);
         }
-    } else if (!s.wide) {
-        if (s.nt == 32) run<E, 1, 16, 32>(a, s, back, st);
-        else if (s.nt == 128) run<E, 1, 16, 128>(a, s, back, st);
-        else run<E, 1, 16, 512>(a, s, back, st);
     } else if (s.nt == 32) {
         s.k == 1 ? run<E, V, 1, 32>(a, s, back, st) : run<E, V, 2, 32>(a, s, back, st);
     } else if (s.nt == 128) {

@@ -61,7 +61,11 @@ def test_layernorm(shape, dtype):
 # step short), for a warp, 128, 256 and 512 threads a row, one, two and four vectors a thread
 @pytest.mark.parametrize("dtype,T,C", [("bf16", 9999, 136), ("fp32", 9731, 200), ("fp16", 7500, 1000), ("bf16", 2501, 1032),
                                        ("fp32", 2437, 1024), ("bf16", 2000, 4096), ("bf16", 701, 8192), ("fp32", 1300, 2048),
-                                       ("fp32", 613, 4096), ("bf16", 611, 16384), ("fp32", 620, 8192), ("bf16", 1500, 3001)])
+                                       ("fp32", 613, 4096), ("bf16", 611, 16384), ("fp32", 620, 8192), ("bf16", 1500, 3001),
+                                       # rows that start inside a vector, in every such form
+                                       ("fp16", 9999, 61), ("bf16", 9999, 399), ("fp32", 10001, 131), ("bf16", 5000, 777), ("fp32", 2500, 555),
+                                       ("fp32", 1300, 1111), ("fp16", 2600, 2047), ("fp32", 700, 3333), ("bf16", 1300, 7001), ("fp32", 640, 8001),
+                                       ("bf16", 700, 15001), ("fp16", 3000, 10), ("fp32", 40000, 3)])
 def test_layernorm_many_rows(dtype, T, C):
     gen, dt = torch.Generator("cuda").manual_seed(T), DT[dtype]
     rn = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
@@ -72,13 +76,16 @@ def test_layernorm_many_rows(dtype, T, C):
         if res is not None:
             assert torch.equal(total, (x.float() + r.float()).to(dt))
         yr, mr, rr = layernorm.layernorm_fwd(_np(total), _np(w), _np(b))
-        _close("y", y, yr, TOL)
+        # fp32 statistics: the mean's rounding, 2^-24 |x|, reaches a normalised value times rstd and a gradient
+        # times rstd^2 (rows of three elements can lie close together; from tens of elements on rstd is below 1)
+        cond = [2.0 ** -22 * float(total.abs().max()) * float(rr.max()) ** n for n in (1, 2)]
+        _close("y", y, yr, TOL + cond[0])
         _close("mean", mean, mr, TOL)
-        _close("rstd", rstd, rr, TOL)
+        _close("rstd", rstd, rr, TOL + cond[0])
         g = kda.kda_layernorm_bwd(total, w, mean, rstd, dy, dsum=dsum)
         ref = layernorm.layernorm_bwd(_np(total), _np(dy), _np(w), _np(dsum))
         for k in g:
-            _close(k, g[k], ref[k], TOL)
+            _close(k, g[k], ref[k], TOL + (cond[1] if k == "dx" else cond[0]))
 
 
 def test_large_offset_keeps_the_variance():
