@@ -1,4 +1,5 @@
-// Shared parts of the selective state-space scan (prompt, backward and single-token kernels).
+// Shared parts of the selective state-space scan (prompt, backward and single-token kernels); the layer norm
+// uses its element types and packed arithmetic.
 //
 // Per document, channel c, state s and the channel's group g of B and C:
 //   delta = softplus(dt + bias)   (or dt + bias),   a = exp(delta A[c, s])
@@ -34,16 +35,14 @@ struct SsmArgs {
     // workspace
     int *status, *nchunks, *doc_off;  // the chunk plan's (a saved set holds its forward's plan)
     int* call_status;                 // the first word of this call's workspace
-    int4* chunk_tab;  // {doc, first token, length, chunk index within the doc}
+    int4* chunk_tab;                  // {doc, first token, length, chunk index within the doc}
+    int direct;                       // every document fits one chunk: no plan, no carry
+    int sub;          // states kept per chunk: 1 (its start) or SSM_SUB (every SSM_UT-th token: the backward's set)
     float* sumdt;     // [maxC][C] sum of delta over the chunk
-    float* hs;        // [maxC][sub][C][S] states at the chunks' starts (a document's first chunk: h0)
-                      // and, with sub = SSM_SUB, at every SSM_UT-th token (the backward's set)
-    int sub;
-    int direct;  // every document fits one chunk: no plan, no carry
+    float* hs;        // [maxC][sub][C][S] those states (a document's first: h0)
     float* gs;        // [maxC][C][S] gradient of the state at each chunk's end (last chunk: dht)
     float* pBC;       // [channel blocks][T][2 S] partial sums of dB and dC
     float* pA;        // [maxC][C][S + 2] partial sums of dA, dD, dbias
-    int nsplit;       // channel blocks per group of the backward
 };
 
 // ---- element types ----
@@ -121,7 +120,6 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float ssm_sigmoid(float z) { return rcp(1.f + ex2(-LOG2E * z)); }
 // z sigmoid(z).  Past z = -87 the divisor leaves the range of its reciprocal: the limit there is 0
 __device__ __forceinline__ float ssm_silu(float z) {
     return __fmul_rn(z, z < -87.f ? 0.f : rcp(__fadd_rn(1.f, ex2(-LOG2E * z))));

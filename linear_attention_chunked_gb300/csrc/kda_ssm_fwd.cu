@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(SSM_THREADS, MODE == STATE ? 6 : MODE == OUT ?
     d.load(len);
     if (gated) z.load(len);
     __syncthreads();
-    E cu[GR], cd[GR], cz[GR];
+    E cu[GR] = {}, cd[GR] = {}, cz[GR] = {};
     float sum = 0.f;
     auto token = [&](int q, int i) {
         const float dl = ssm_delta(__fadd_rn(ssm_f<E>(cd[i]), bias), a.softplus);
