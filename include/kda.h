@@ -298,7 +298,9 @@ typedef enum kda_dtype { KDA_DT_BF16 = 0, KDA_DT_FP16 = 1, KDA_DT_FP32 = 2 } kda
  * on the rest of the pack.
  *
  * kda_ssm_fwd with a non-NULL saved buffer writes the states at every 64-token chunk's start for
- * kda_ssm_bwd (saved = NULL there recomputes them).  The backward is that of L = sum(y * dy) +
+ * kda_ssm_bwd (saved = NULL there recomputes them).  A saved set serves the inputs of the forward
+ * that wrote it: one written for other sizes, or by no forward, sets the device status
+ * KDA_ERR_DEVICE_CHECK and the backward writes nothing.  The backward is that of L = sum(y * dy) +
  * sum(ht * dht) (dht nullable); dD, ddt_bias and dh0 are nullable, dz is written when z is given.
  * Workspace sizes (op: KDA_OP_FWD, KDA_OP_BWD_SAVED, KDA_OP_BWD_REPLAY) depend on T, N, C, S, G
  * only.  The first call on a device sets it up: make it before any stream capture. */

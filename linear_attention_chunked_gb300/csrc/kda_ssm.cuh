@@ -36,6 +36,9 @@ struct SsmArgs {
     int *status, *nchunks, *doc_off;  // the chunk plan's (a saved set holds its forward's plan)
     int* call_status;                 // the first word of this call's workspace
     int4* chunk_tab;                  // {doc, first token, length, chunk index within the doc}
+    int4* made_for;                   // beside a saved set's plan: the sizes of the forward that wrote it
+    int4 sizes;                       // this call's
+    int from_saved;                   // the plan is a saved set's (backward)
     int direct;                       // every document fits one chunk: no plan, no carry
     int sub;          // states kept per chunk: 1 (its start) or SSM_SUB (every SSM_UT-th token: the backward's set)
     float* sumdt;     // [maxC][C] sum of delta over the chunk
@@ -44,6 +47,16 @@ struct SsmArgs {
     float* pBC;       // [channel blocks][T][2 S] partial sums of dB and dC
     float* pA;        // [maxC][C][S + 2] partial sums of dA, dD, dbias
 };
+
+// Whether the call's plan may be followed: well-formed offsets, and a saved set that was written for these
+// sizes (the plan of another problem, or what a buffer held that no forward wrote, would lead outside the
+// tensors).
+__device__ __forceinline__ bool ssm_plan_ok(const SsmArgs& a) {
+    if (*a.status != KDA_OK) return false;
+    if (!a.from_saved) return true;
+    const int4 m = *a.made_for;
+    return m.x == a.sizes.x && m.y == a.sizes.y && m.z == a.sizes.z && m.w == a.sizes.w;
+}
 
 // ---- element types ----
 template <class E> __device__ __forceinline__ float ssm_ld(const void* p, int64_t i);

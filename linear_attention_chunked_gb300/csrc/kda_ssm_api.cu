@@ -61,7 +61,7 @@ kda_status check_problem(const kda_ssm_problem* p) {
 
 // The chunk plan (its bytes first in a saved set, or in the workspace), and what follows.
 struct Regions {
-    size_t status, nchunks, doc_off, doc_order, chunk_tab, plan;  // inside the plan; its size
+    size_t status, made_for, nchunks, doc_off, doc_order, chunk_tab, plan;  // inside the plan; its size
     size_t sumdt, hs, gs, pBC, pA;                                // inside the workspace
     size_t head, fwd, bwd_saved, bwd_replay, states, saved;
 };
@@ -73,6 +73,7 @@ Regions regions(const kda_ssm_problem* p) {
     const size_t nc = size_t(max_chunks(p)), CS = size_t(p->C) * p->S;
     const SsmBwdPlan pl = ssm_bwd_plan(int64_t(nc), p->C, p->S, p->G);
     r.status = take(256);
+    r.made_for = r.status + sizeof(int4);  // in the status word's 256 bytes
     r.nchunks = take(sizeof(int));
     r.doc_off = take(sizeof(int) * size_t(p->N + 1));
     r.doc_order = take(sizeof(int) * size_t(p->N));
@@ -115,6 +116,7 @@ SsmArgs make_args(const kda_ssm_problem* p, const Regions& r, void* ws) {
     a.ldz = ld_or(p->ld_z, p->C);
     a.ldb = ld_or(p->ld_b, GS);
     a.ldc = ld_or(p->ld_c, GS);
+    a.sizes = make_int4(int(p->T), p->N | p->S << 16, p->C, p->G);
     a.cu = p->cu_seqlens;
     char* w = static_cast<char*>(ws);
     a.call_status = static_cast<int*>(ws);
@@ -185,7 +187,10 @@ kda_status kda_ssm_fwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     a.ht = ht;
     // a saved set holds the plan and the states of every 16th token
     a.hs = reinterpret_cast<float*>(saved ? static_cast<char*>(saved) + r.plan : static_cast<char*>(ws) + r.head);
-    if (saved) use_plan(a, r, static_cast<char*>(saved));
+    if (saved) {
+        use_plan(a, r, static_cast<char*>(saved));
+        a.made_for = reinterpret_cast<int4*>(static_cast<char*>(saved) + r.made_for);
+    }
     a.sub = saved ? SSM_SUB : 1;
     // a short prompt (every document within one chunk, few of them): one launch, no plan, no carry
     a.direct = !saved && a.T <= CH && a.N <= 64;
@@ -215,6 +220,8 @@ kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* u, const void* dt, 
     if (saved) {
         char* set = static_cast<char*>(const_cast<void*>(saved));
         use_plan(a, r, set);
+        a.made_for = reinterpret_cast<int4*>(set + r.made_for);
+        a.from_saved = 1;
         a.hs = reinterpret_cast<float*>(set + r.plan);
     } else {  // recompute the states (no y, no final state)
         launch_plan(a, r, st);

@@ -55,8 +55,9 @@ __device__ __forceinline__ void st4(float* p, int s, int S, float4 v) {
 
 constexpr int CARRY_THREADS = 128;
 __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_rcarry(SsmArgs a, int blocks_per_doc) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.call_status = *a.status;  // (the plan may be a saved one)
-    if (*a.status != KDA_OK) return;
+    const bool ok = ssm_plan_ok(a);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.call_status = ok ? KDA_OK : KDA_ERR_DEVICE_CHECK;  // (the plan may be a saved one)
+    if (!ok) return;
     const int n = blockIdx.x / blocks_per_doc;
     const int64_t CS = int64_t(a.C) * a.S;
     const int64_t i = int64_t(blockIdx.x % blocks_per_doc) * CARRY_THREADS + threadIdx.x;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(SSM_THREADS, P == 1 ? 2 : P <= 4 ? 3 : 1) k_ss
     extern __shared__ __align__(16) float sm[];
     const int per_chunk = a.G * pl.splits;
     const int k = blockIdx.x / per_chunk;
-    if (k >= *a.nchunks) return;
+    if (!ssm_plan_ok(a) || k >= *a.nchunks) return;
     const int4 tab = a.chunk_tab[k];
     const int t0 = tab.y, len = tab.z;
     const int gsp = blockIdx.x % per_chunk, g_ = gsp / pl.splits, split = gsp % pl.splits;
@@ -500,7 +501,7 @@ __device__ __forceinline__ void reduce_par(const SsmArgs& a, int block) {
 // the first par_blocks blocks take the parameters, the others dB and dC
 template <class E>
 __global__ void __launch_bounds__(32 * PAR_STRANDS) k_ssm_reduce(SsmArgs a, SsmBwdPlan pl, int par_blocks) {
-    if (*a.status != KDA_OK) return;
+    if (!ssm_plan_ok(a)) return;
     if (int(blockIdx.x) < par_blocks) reduce_par(a, blockIdx.x);
     else reduce_bc<E>(a, pl, blockIdx.x - par_blocks, gridDim.x - par_blocks);
 }

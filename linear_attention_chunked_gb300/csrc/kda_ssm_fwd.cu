@@ -73,7 +73,10 @@ __device__ __forceinline__ void load_A(const SsmArgs& a, int c, int s0, f2 (&A2)
 // start and receives chunk k + 1's start state.
 constexpr int CARRY_THREADS = 128;
 __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_carry(SsmArgs a, int blocks_per_doc) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.call_status = *a.status;  // (the plan may lie in the saved set)
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.call_status = *a.status;  // (the plan may lie in the saved set)
+        if (a.made_for) *a.made_for = a.sizes;
+    }
     if (*a.status != KDA_OK) return;
     const int n = blockIdx.x / blocks_per_doc;
     const int64_t CS = int64_t(a.C) * a.S;
@@ -157,6 +160,7 @@ __global__ void __launch_bounds__(SSM_THREADS, MODE == STATE ? 6 : MODE == OUT ?
     constexpr int CW = L::CW, SP = L::SP, H2 = SPT / 2, GR = MODE == RSTATE ? 8 : 4;
     __shared__ __align__(16) float sB[MODE == RSTATE ? 4 : CH * SP], sC[MODE == STATE ? 4 : CH * SP];
     const int k = blockIdx.x / tiles, tile = blockIdx.x % tiles, S = a.S;
+    if (MODE == RSTATE && !ssm_plan_ok(a)) return;
     if (k >= *a.nchunks) return;
     const int4 t = a.chunk_tab[k];
     const int t0 = t.y, len = t.z;
@@ -296,6 +300,7 @@ __global__ void __launch_bounds__(SSM_THREADS) k_ssm_small(SsmArgs a, int tiles,
         doc = k, t0 = a.cu[k], len = a.cu[k + 1] - t0;
         last = first = true;
     } else {
+        if (MODE == RSTATE && !ssm_plan_ok(a)) return;
         if (k >= *a.nchunks) return;
         const int4 t = a.chunk_tab[k];
         doc = t.x, t0 = t.y, len = t.z;
