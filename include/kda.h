@@ -292,7 +292,8 @@ typedef enum kda_dtype { KDA_DT_BF16 = 0, KDA_DT_FP16 = 1, KDA_DT_FP32 = 2 } kda
  * tensor (row strides ld_*, in elements; 0 = dense) and needs the alignment of its element only.
  * Everything else is dense and 16-byte aligned: A fp32 [C, S], D and dt_bias fp32 [C] (nullable:
  * zero), y, dy and the gradients of u, dt, z, B, Cm in p->dtype, states fp32 [N, C, S].  z is nullable
- * (no gate); h0 is nullable (zero); ht is nullable.  The states, decays and every sum are fp32.  An
+ * (no gate); h0 is nullable (zero); ht is nullable.  An A of -inf is a decay of 0 (its term of dt's
+ * gradient counts as 0).  The states, decays and every sum are fp32.  An
  * empty document's ht is its h0 and its dh0 is its dht.  Results are bitwise reproducible, and a
  * document's outputs (dA, dD, ddt_bias excepted, which are sums over documents) do not depend
  * on the rest of the pack.

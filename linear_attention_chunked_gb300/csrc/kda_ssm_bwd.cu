@@ -53,6 +53,16 @@ __device__ __forceinline__ void st4(float* p, int s, int S, float4 v) {
     if (s + 3 < S) p[s + 3] = v.w;
 }
 
+// A decay rate of -inf as the lowest finite one: the decay is 0 either way (from steps of 4e-37 on), and the
+// steps of 0 that stand for tokens past the chunk and for lanes past the group's channels keep their decay
+// of 1, where 0 times infinity would reach dB and dC of every channel.  (NaN stays.)
+__device__ __forceinline__ f2 above_inf2(f2 v) {
+    constexpr float low = -3.402823466e38f;
+    float x, y;
+    up2(v, x, y);
+    return pk2(x < low ? low : x, y < low ? low : y);
+}
+
 constexpr int CARRY_THREADS = 128;
 __global__ void __launch_bounds__(CARRY_THREADS) k_ssm_rcarry(SsmArgs a, int blocks_per_doc) {
     const bool ok = ssm_plan_ok(a);
@@ -231,7 +241,7 @@ __global__ void __launch_bounds__(SSM_THREADS, P == 1 ? 2 : P <= 4 ? 3 : 1) k_ss
             paired(vg, g);
         }
 #pragma unroll
-        for (int j = 0; j < SPT; ++j) A2[j] = mul2(A2[j], pk2(LOG2E, LOG2E)), dA[j] = 0;
+        for (int j = 0; j < SPT; ++j) A2[j] = above_inf2(mul2(A2[j], pk2(LOG2E, LOG2E))), dA[j] = 0;
         const f2 skip = a.D ? pk2(a.D[c0], a.D[c1]) : 0;
         f2 accD = 0, accb = 0;
         // lanes as items: item x of a run is token (lane + 32 x) / CL, channels lane % CL and lane % CL + CL
