@@ -271,8 +271,9 @@ kda_status kda_conv_bwd(const kda_conv_problem* p, const void* x, const float* w
  *     (win[n] when slots is NULL) in a pool bf16 [n_slots, 3, C], and win_out (may be win itself)
  *     receives it shifted by x.  A negative slot marks an unused row: its y is zero and no window
  *     is touched; a slot >= n_slots is treated the same way and sets the device status
- *     KDA_ERR_DEVICE_CHECK in ws (nullable, >= 256 bytes).  The used slots must differ from each
- *     other. */
+ *     KDA_ERR_DEVICE_CHECK in ws (nullable, >= 256 bytes; its first word becomes the status of this
+ *     call, KDA_OK included, so read it before the next call on the same ws).  The used slots must
+ *     differ from each other. */
 kda_status kda_conv_tail(const kda_conv_problem* p, const void* x, const void* halo, void* tail,
                          kda_stream_t stream);
 kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* w,

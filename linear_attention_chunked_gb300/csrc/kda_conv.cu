@@ -672,6 +672,7 @@ kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* 
     a.rpt = int(rpt > 1 ? rpt : 1);
     while ((q.N + a.rpt - 1) / a.rpt > 65535) a.rpt *= 2;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!clear_status(ws, st)) return KDA_ERR_CUDA;
     {
         ProfScope ps(KK_CONV_STEP, st);
         const dim3 grid(gx, unsigned((q.N + a.rpt - 1) / a.rpt));

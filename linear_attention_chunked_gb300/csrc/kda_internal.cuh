@@ -408,6 +408,10 @@ inline void allow_smem(const void* kernel, size_t bytes, unsigned long long* don
         __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
 }
 
+// Clears the status word of a call whose kernels only raise it (ws nullable): the word tells of that call alone,
+// whatever it held.
+inline bool clear_status(void* ws, cudaStream_t st) { return !ws || cudaMemsetAsync(ws, 0, sizeof(int), st) == cudaSuccess; }
+
 // Launch accounting: every kernel launch of the library sits inside a ProfScope, which counts it
 // and, while profiling is enabled (kda_profile_enable), brackets it with CUDA events on its stream.
 enum KernelKind {

@@ -250,7 +250,9 @@ kda_status kda_ssm_step(const kda_ssm_problem* p, const void* u, const void* dt,
     const SsmArgs t = make_args(&q, none, ws);
     SsmStepArgs a{q.N, q.C, q.S, q.G, q.dt_softplus, t.ldu, t.lddt, t.ldb, t.ldc, t.ldz, n_slots,
                   u, dt, B, Cm, z, A, D_, dt_bias, h_in, slots, h_out, y, static_cast<int*>(ws)};
-    launch_ssm_step(a, q.dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!clear_status(ws, st)) return KDA_ERR_CUDA;
+    launch_ssm_step(a, q.dtype, st);
     return launched();
 }
 

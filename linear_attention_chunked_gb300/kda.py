@@ -470,7 +470,7 @@ def kda_conv_step(x, w, win, *, bias=None, activation=True, slots=None, out_dtyp
     """The conv of one token per sequence: x [N, C] bf16, taps w [C, 4] fp32, windows win
     [n_slots, 3, C] bf16 (row n's is win[slots[n]], win[n] without slots).  Returns (y [N, C] in
     out_dtype, win_out); win_out defaults to win, updated in place.  A negative slot marks an
-    unused row; ws (optional, >= 256 bytes) receives the device status."""
+    unused row; ws (optional, >= 256 bytes) receives the device status of this call."""
     fn = "kda_conv_step"
     N, C = x.shape
     dev = x.device
@@ -607,7 +607,7 @@ def kda_ssm_step(u, dt, A, B, C, h, *, D=None, dt_bias=None, z=None, softplus=Tr
     """The scan of one token per sequence: rows are sequences, h [n_slots, ch, S] fp32 the states
     (row n's is h[slots[n]], h[n] without slots).  Returns (y, h_out); h_out defaults to h, updated
     in place.  A negative slot marks an unused row; ws (optional, >= 256 bytes) receives the
-    device status."""
+    device status of this call."""
     fn = "kda_ssm_step"
     N, dev = u.shape[0], u.device
     pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, None)
