@@ -451,13 +451,15 @@ def _call(fn, dev, *args):
 
 def kda_conv_tail(x, cu_seqlens, *, halo=None, tail=None):
     """The conv window that a prompt leaves: tail [N, 3, C] bf16, the three rows before each
-    document's end (from halo [N, 3, C], or zero, where the document is shorter)."""
+    document's end (from halo [N, 3, C], or zero, where the document is shorter).  As for
+    kda_conv_fwd, malformed offsets give unspecified rows."""
     fn = "kda_conv_tail"
     T, N, C = _conv_shape(x, cu_seqlens)
     dev = x.device
     if tail is None:
         tail = torch.empty((N, 3, C), dtype=torch.bfloat16, device=dev)
     _check_tensor(fn, "x", x, x.shape, torch.bfloat16, dev)
+    _check_tensor(fn, "cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     _check_tensor(fn, "halo", halo, (N, 3, C), torch.bfloat16, dev)
     _check_tensor(fn, "tail", tail, (N, 3, C), torch.bfloat16, dev)
     pr = make_conv_problem(T, N, C, cu_seqlens)
