@@ -416,6 +416,27 @@ def _check_tensor(fn, name, t, shape, dtype, device, strided=False):
                              f"{'rows' if strided else 'storage'}")
 
 
+def _check_bytes(fn, name, t, need, device):
+    """A workspace or saved set (of any type) is dense, lies on the call's device and holds `need`
+    bytes.  Returns the bytes it holds."""
+    if t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} has strides {t.stride()}, expected dense storage")
+    n = t.numel() * t.element_size()
+    if n < need:
+        raise ValueError(f"{fn}: {name} holds {n} bytes, needs {need}")
+    return n
+
+
+def _workspace(fn, ws, need, device):
+    """The caller's workspace or a new one, and its bytes (the library refuses too few)."""
+    if ws is None:
+        ws = _empty_bytes(need, device)
+        return ws, ws.numel()
+    return ws, _check_bytes(fn, "ws", ws, 0, device)
+
+
 def _row_stride(t):
     """The row stride of a tensor whose rows are dense (0, the library's dense, where it has at
     most one row)."""
@@ -489,6 +510,8 @@ def kda_conv_step(x, w, win, *, bias=None, activation=True, slots=None, out_dtyp
     if win_out is not win:
         _check_tensor(fn, "win_out", win_out, win.shape, torch.bfloat16, dev)
     _slots(fn, slots, N, win.shape[0], dev)
+    if ws is not None:
+        _check_bytes(fn, "ws", ws, 256, dev)
     pr = make_conv_problem(N, N, C, activation=activation, out_dtype=out_dtype)
     _call(fn, dev, ctypes.byref(pr), x.data_ptr(), w.data_ptr(), _at(bias), _at(slots), win.shape[0],
           win.data_ptr(), win_out.data_ptr(), y.data_ptr(), _at(ws))
@@ -545,14 +568,13 @@ def kda_ssm_fwd(u, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, z=None, h0=
     pr = _ssm_problem(fn, u, dt, A, B, C, z, D, dt_bias, softplus, N, cu_seqlens)
     ws_b, sv_b = _ssm_sizes(pr.T, N, pr.C, pr.S, pr.G, KDA_OP_FWD)
     state = (N, pr.C, pr.S)
-    if ws is None:
-        ws = _empty_bytes(ws_b, dev)
+    ws, ws_n = _workspace(fn, ws, ws_b, dev)
     if not save:
         saved = None
     elif saved is None:
         saved = _empty_bytes(sv_b, dev)
-    elif saved.numel() * saved.element_size() < sv_b:
-        raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
+    else:
+        _check_bytes(fn, "saved", saved, sv_b, dev)
     if y is None:  # dense rows, whatever u's strides are
         y = torch.empty_like(u, memory_format=torch.contiguous_format)
     else:
@@ -563,8 +585,7 @@ def kda_ssm_fwd(u, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, z=None, h0=
         _check_tensor(fn, "ht", ht, state, torch.float32, dev)
     _check_tensor(fn, "h0", h0, state, torch.float32, dev)
     _call(fn, dev, ctypes.byref(pr), u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
-          _at(D), _at(dt_bias), _at(z), _at(h0), y.data_ptr(), ht.data_ptr(), _at(saved), ws.data_ptr(),
-          ws.numel())
+          _at(D), _at(dt_bias), _at(z), _at(h0), y.data_ptr(), ht.data_ptr(), _at(saved), ws.data_ptr(), ws_n)
     return y, ht, saved
 
 
@@ -581,10 +602,9 @@ def kda_ssm_bwd(u, dt, A, B, C, cu_seqlens, dy, *, saved=None, D=None, dt_bias=N
     _check_tensor(fn, "h0", h0, state, torch.float32, dev)
     _check_tensor(fn, "dht", dht, state, torch.float32, dev)
     ws_b, sv_b = _ssm_sizes(pr.T, N, pr.C, pr.S, pr.G, KDA_OP_BWD_REPLAY if saved is None else KDA_OP_BWD_SAVED)
-    if saved is not None and saved.numel() * saved.element_size() < sv_b:
-        raise ValueError(f"{fn}: saved holds {saved.numel() * saved.element_size()} bytes, needs {sv_b}")
-    if ws is None:
-        ws = _empty_bytes(ws_b, dev)
+    if saved is not None:
+        _check_bytes(fn, "saved", saved, sv_b, dev)
+    ws, ws_n = _workspace(fn, ws, ws_b, dev)
     # (like dy: dense rows whatever the inputs' strides are)
     out = dict(du=torch.empty_like(dy), ddt=torch.empty_like(dy), dA=torch.empty_like(A),
                dB=torch.empty(B.shape, dtype=dtype, device=dev),
@@ -600,7 +620,7 @@ def kda_ssm_bwd(u, dt, A, B, C, cu_seqlens, dy, *, saved=None, D=None, dt_bias=N
     _call(fn, dev, ctypes.byref(pr), u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
           _at(D), _at(dt_bias), _at(z), _at(h0), dy.data_ptr(), _at(dht), _at(saved),
           *(_at(out.get(k)) for k in ("du", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dz", "dh0")),
-          ws.data_ptr(), ws.numel())
+          ws.data_ptr(), ws_n)
     return out
 
 
@@ -623,6 +643,8 @@ def kda_ssm_step(u, dt, A, B, C, h, *, D=None, dt_bias=None, z=None, softplus=Tr
         _check_tensor(fn, "y", y, u.shape, u.dtype, dev)
     _check_tensor(fn, "h", h, (h.shape[0], pr.C, pr.S), torch.float32, dev)
     _slots(fn, slots, N, h.shape[0], dev)
+    if ws is not None:
+        _check_bytes(fn, "ws", ws, 256, dev)
     _call(fn, dev, ctypes.byref(pr), u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
           _at(D), _at(dt_bias), _at(z), _at(slots), h.shape[0], h.data_ptr(), h_out.data_ptr(),
           y.data_ptr(), _at(ws))
@@ -686,14 +708,13 @@ def kda_layernorm_bwd(x, w, mean, rstd, dy, *, dsum=None, ws=None):
     _check_tensor(fn, "w", w, (pr.C,), torch.float32, dev)
     _check_tensor(fn, "mean", mean, x.shape[:-1], torch.float32, dev)
     _check_tensor(fn, "rstd", rstd, x.shape[:-1], torch.float32, dev)
-    if ws is None:
-        ws = _empty_bytes(kda_layernorm_workspace_size(pr.T, pr.C, dtype=x.dtype), dev)
+    ws, ws_n = _workspace(fn, ws, kda_layernorm_workspace_size(pr.T, pr.C, dtype=x.dtype), dev)
     out = dict(dx=torch.empty_like(x),
                dw=torch.empty((pr.C,), dtype=torch.float32, device=dev),
                db=torch.empty((pr.C,), dtype=torch.float32, device=dev))
     _call(fn, dev, ctypes.byref(pr), x.data_ptr(), _at(w), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
           _at(dsum), out["dx"].data_ptr(), out["dw"].data_ptr(), out["db"].data_ptr(), ws.data_ptr(),
-          ws.numel())
+          ws_n)
     return out
 
 
