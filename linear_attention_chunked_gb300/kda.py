@@ -661,6 +661,8 @@ def _layernorm_problem(fn, x, eps):
 
 @functools.lru_cache(maxsize=256)  # a function of these numbers alone
 def kda_layernorm_workspace_size(T, C, *, dtype=torch.bfloat16):
+    if dtype not in _DTYPES:
+        raise ValueError(f"kda_layernorm_workspace_size: dtype is {dtype}, expected one of bfloat16, float16, float32")
     pr = kda_layernorm_problem(int(T), int(C), _DTYPES[dtype], 0.0)
     ws = ctypes.c_size_t(0)
     _check("kda_layernorm_workspace_size",

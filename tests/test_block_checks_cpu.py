@@ -81,3 +81,9 @@ def test_saved_sets():
             kda.kda_ssm_fwd(*a, saved=saved)
         with pytest.raises(ValueError, match=word):
             kda.kda_ssm_bwd(*a, x, saved=saved)
+
+
+def test_size_queries_refuse_other_types():
+    for size in (lambda **kw: kda.kda_ssm_workspace_size(6, 1, 16, 4, 1, kda.KDA_OP_FWD, **kw), lambda **kw: kda.kda_layernorm_workspace_size(6, 16, **kw)):
+        with pytest.raises(ValueError, match="dtype is torch.float64"):
+            size(dtype=torch.float64)
