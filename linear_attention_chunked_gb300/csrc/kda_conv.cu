@@ -670,7 +670,6 @@ kda_status kda_conv_step(const kda_conv_problem* p, const void* x, const float* 
     // make one wave (512 x 8192: 19.3 us with four sequences a thread in 1.7 waves, 16.9 us so)
     const int64_t rpt = (int64_t(gx) * q.N + 607) / 608;
     a.rpt = int(rpt > 1 ? rpt : 1);
-    while ((q.N + a.rpt - 1) / a.rpt > 65535) a.rpt *= 2;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!clear_status(ws, st)) return KDA_ERR_CUDA;
     {

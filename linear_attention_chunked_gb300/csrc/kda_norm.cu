@@ -37,9 +37,9 @@ struct LnArgs {
     int parts;    // slots that the rows of a walk are dealt to
 };
 
-// V consecutive elements (one 16-byte access when V > 1)
+// V consecutive elements, one 16-byte access
 template <class E, int V>
-struct alignas(V > 1 ? 16 : sizeof(E)) Vec {
+struct alignas(16) Vec {
     E e[V];
 };
 template <class E, int V>

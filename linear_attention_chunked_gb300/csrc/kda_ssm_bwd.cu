@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(32 * PAR_STRANDS) k_ssm_reduce(SsmArgs a, SsmB
 template <class E, int P>
 void launch_main(const SsmArgs& a, const SsmBwdPlan& pl, cudaStream_t st) {
     const unsigned grid = unsigned(a.maxC * a.G * pl.splits);
-    if (grid) {
+    {
         ProfScope ps(KK_SSM_BWD, st);
         k_ssm_bwd<E, P><<<grid, SSM_THREADS, BwdShape<P>::floats * 4, st>>>(a, pl);
     }
