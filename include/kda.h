@@ -294,18 +294,21 @@ typedef enum kda_dtype { KDA_DT_BF16 = 0, KDA_DT_FP16 = 1, KDA_DT_FP32 = 2 } kda
  * Everything else is dense and 16-byte aligned: A fp32 [C, S], D and dt_bias fp32 [C] (nullable:
  * zero), y, dy and the gradients of u, dt, z, B, Cm in p->dtype, states fp32 [N, C, S].  z is nullable
  * (no gate); h0 is nullable (zero); ht is nullable.  An A of -inf is a decay of 0 (its term of dt's
- * gradient counts as 0).  The states, decays and every sum are fp32.  An
- * empty document's ht is its h0 and its dh0 is its dht.  Results are bitwise reproducible, and a
- * document's outputs (dA, dD, ddt_bias excepted, which are sums over documents) do not depend
- * on the rest of the pack.
+ * gradient counts as 0).  The states, decays and every sum are fp32, for fp32 rows too with the
+ * approximate base-2 exponential and reciprocal.  An empty document's ht is its h0 and its dh0 is
+ * its dht.  Results are bitwise reproducible, and a document's outputs (dA, dD, ddt_bias excepted,
+ * which are sums over documents) do not depend on the rest of the pack.
  *
- * kda_ssm_fwd with a non-NULL saved buffer writes the states at every 64-token chunk's start for
- * kda_ssm_bwd (saved = NULL there recomputes them).  A saved set serves the inputs of the forward
+ * kda_ssm_fwd with a non-NULL saved buffer writes its chunk plan and the state of every 16th token
+ * of a document's 64-token chunks there, for kda_ssm_bwd (saved = NULL there recomputes them): 16 C S
+ * bytes for each of the ceil(T / 64) + N chunks that the pack may have, i.e. 136 MB for 16384 tokens x
+ * 2048 channels x 16 states and in proportion to each.  A saved set serves the inputs of the forward
  * that wrote it: one written for other sizes, or by no forward, sets the device status
  * KDA_ERR_DEVICE_CHECK and the backward writes nothing.  The backward is that of L = sum(y * dy) +
  * sum(ht * dht) (dht nullable); dD, ddt_bias and dh0 are nullable, dz is written when z is given.
  * Workspace sizes (op: KDA_OP_FWD, KDA_OP_BWD_SAVED, KDA_OP_BWD_REPLAY) depend on T, N, C, S, G
- * only.  The first call on a device sets it up: make it before any stream capture. */
+ * only; KDA_OP_FWD's is that of a forward without a saved set.  The first call on a device sets it up:
+ * make it before any stream capture (other sizes and types may be met first inside one). */
 typedef struct kda_ssm_problem {
     int64_t T;            /* packed tokens, >= 0 */
     int32_t N;            /* documents, 1 .. 65535 */

@@ -22,7 +22,7 @@
 // one token, whose du, ddt and dz that lane finishes; the eight dB / dC terms per token, summed over the
 // two channels first, take 7 shuffles over 8 lanes.
 //
-// Bound by instruction issue and shared-memory operands together (16384 x 2048 x 16: 760 us, about 29
+// Bound by instruction issue and shared-memory operands together (16384 x 2048 x 16: 768 us, about 29
 // instructions per channel, state and token, half of the issue slots, 12 warps per multiprocessor by
 // registers).  Measured and worse: B and C doubled in shared memory, which saves the copies into
 // pairs (+51 us: the operand reads double); their products as two scalar instructions (+24 us); four

@@ -13,9 +13,10 @@
 // sum over up to 16 states stays in the lane, and a lane's B and C values are shared-memory broadcasts.
 // The walk loads several pipes at once (per token and 16 states: 16 of 32 ex2 a clock, 16 packed fp32
 // instructions, and 4 clocks of register write-back for each shared 16-byte operand) and runs at 0.7
-// instructions a clock per scheduler.  Measured and worse on 16384 x 8192 (state + out 1067 us): two channels
-// a lane, which halves the operand reads but leaves 12 warps (1270); two lanes a channel with the
-// scalars handed over through shared memory, 32 warps (1295); scalars computed a group ahead (1121).
+// instructions a clock per scheduler.  Measured and worse on 16384 x 8192 x 16 (the call's kernels 1067 us:
+// states 390, output 614, carry 57, plan 6): two channels a lane, which halves the operand reads but leaves
+// 12 warps (1270); two lanes a channel with the scalars handed over through shared memory, 32 warps (1295);
+// scalars computed a group ahead (1121).
 //
 // Small problems (k_ssm_small) are bound by the latency of the serial walk instead: there a channel's
 // states are spread four to a lane, and the scalars of the whole chunk are computed before the walk by

@@ -6,7 +6,7 @@
 // is instructions, so a thread takes four sequences: the weights are read once for them, each of a
 // channel's lanes computes the scalars (delta, the gate) of one sequence and hands them to the others, and
 // the sums over states go back by halving, so that a lane finishes the sequence it began.  256 sequences x
-// 8192 channels x 16 states: 66 us, 4.3 TB/s (three blocks per multiprocessor; 68 us with four, 97 with
+// 8192 channels x 16 states: 63 us, 4.6 TB/s (three blocks per multiprocessor; 68 us with four, 97 with
 // five, whose registers no longer hold the loads in flight).
 #include "kda_ssm.cuh"
 #include "kda_ssm_launch.cuh"
