@@ -362,6 +362,103 @@ kda_status kda_layernorm_bwd(const kda_layernorm_problem* p, const void* x, cons
                              const void* dsum, void* dx, float* dw, float* db, void* ws,
                              size_t ws_bytes, kda_stream_t stream);
 
+/* Linear attention with a decay for each head, over packed documents: the state recurrence without an erase
+ * step and with one constant decay per head.  Per document and head h, with lambda = exp(slope[h]) and the
+ * query / key head hk = h / (H / Hk):
+ *     S_t = lambda S_{t-1} + k_t[hk] v_t[h]^T,   o_t[h] = scale * S_t^T q_t[hk]
+ * q, k [T, Hk, 128], v, o, dO [T, H, 128] are bf16 (p->dtype; the products' operands -- scores and states --
+ * are rounded to the row type, which must hold their range, so fp16 is KDA_ERR_UNSUPPORTED, and so is a head
+ * dim d other than 128).  q, k and v may be column ranges of a wider row-major tensor: token strides ld_* in
+ * elements, a multiple of 8 (0 = dense); everything is 16-byte aligned, the rest dense.  Hk divides H.
+ * slope fp32 [H] is a constant of the model, usually <= 0 (-inf: no memory; above 0 the state grows as the
+ * formula says).  States h0, ht, dht, dh0 are fp32 [N, H, 128, 128] indexed [key][value]; h0 nullable
+ * (zero), ht nullable.  The states and every sum are fp32; an empty document's ht is its h0 and its dh0 its dht.
+ * A document's results do not depend on the rest of the pack and are bitwise reproducible.  What is not finite in a
+ * document's rows reaches that document alone (earlier tokens of the same 128 among them).
+ *
+ * kda_linattn_fwd with a non-NULL saved buffer leaves there what kda_linattn_bwd needs besides the inputs
+ * (saved = NULL there recomputes it).  The backward is that of L = sum(o * dO) + sum(ht * dht): dq, dk
+ * [T, Hk, 128] (the sums over the heads that share them), dv [T, H, 128] bf16, dh0 (nullable); dht nullable.
+ * A saved set that was written for other sizes sets the device status KDA_ERR_DEVICE_CHECK and the backward
+ * writes nothing; so do malformed cu_seqlens in both.  Workspace sizes (op: KDA_OP_FWD, KDA_OP_BWD_SAVED,
+ * KDA_OP_BWD_REPLAY) depend on T, N, H, Hk only; KDA_OP_FWD's serves with and without a saved set.  The
+ * first call on a device sets it up: make it before any stream capture. */
+typedef struct kda_linattn_problem {
+    int64_t T;            /* packed tokens, >= 0 */
+    int32_t N;            /* documents, 1 .. 65535 */
+    int32_t H;            /* value heads, 1 .. 65535 */
+    int32_t Hk;           /* query / key heads; divides H */
+    int32_t d;            /* head dim; must be 128 */
+    int32_t dtype;        /* kda_dtype; must be KDA_DT_BF16 */
+    float scale;          /* output scale */
+    int64_t ld_q, ld_k, ld_v;  /* token strides; 0 = Hk 128, Hk 128, H 128 */
+    const int32_t* cu_seqlens; /* device int32 [N + 1] */
+} kda_linattn_problem;
+kda_status kda_linattn_workspace_size(const kda_linattn_problem* p, int op, size_t* ws_bytes,
+                                      size_t* saved_bytes);
+kda_status kda_linattn_fwd(const kda_linattn_problem* p, const void* q, const void* k, const void* v,
+                           const float* slope, const float* h0, void* o, float* ht, void* saved,
+                           void* ws, size_t ws_bytes, kda_stream_t stream);
+kda_status kda_linattn_bwd(const kda_linattn_problem* p, const void* q, const void* k, const void* v,
+                           const float* slope, const float* h0, const void* dO, const float* dht,
+                           const void* saved, void* dq, void* dk, void* dv, float* dh0, void* ws,
+                           size_t ws_bytes, kda_stream_t stream);
+/* One token of each of p->N sequences (p->T and p->cu_seqlens are not read; rows are sequences).
+ * Row n's state is h_in[slots[n]] (h_in[n] when slots is NULL) in a pool fp32 [n_slots, H, 128, 128];
+ * h_out (may be h_in itself) receives the new one.  slots and ws as for kda_conv_step. */
+kda_status kda_linattn_step(const kda_linattn_problem* p, const void* q, const void* k, const void* v,
+                            const float* slope, const int32_t* slots, int64_t n_slots,
+                            const float* h_in, float* h_out, void* o, void* ws, kda_stream_t stream);
+
+/* Norm of the queries and keys of every head and their rotation to positions, in one pass (either alone as
+ * well).  Per token t, head and head vector x of D channels, w = wq or wk:
+ *     norm = 1:  x <- x w / sqrt(sum_c x_c^2 / D + eps)      (w fp32 [D], nullable: ones)
+ *     the first R channels turn in pairs by the angle a_i = pos[t] freq[i], i < R / 2:
+ *         (x, y) <- scale (x cos a_i - y sin a_i, x sin a_i + y cos a_i)
+ *     layout KDA_ROPE_HALF pairs channels (i, R / 2 + i), KDA_ROPE_PAIRS channels (2 i, 2 i + 1);
+ *     channels from R on are not turned (nor scaled).
+ * q [T, Hq, D] and k [T, Hk, D] are of p->dtype, inputs with token strides ld_q, ld_k and outputs with
+ * ld_qo, ld_ko (elements; 0 = dense; element alignment); an output may be its input.  pos int32 [T] are any
+ * positions; freq fp64 [R / 2] is in radians per token (kda_rope_frequencies).  An angle is reduced in
+ * 64-bit integers, so far positions keep their accuracy.  Arithmetic is fp32, rounded once.  Hq or Hk may
+ * be 0 (that tensor is not read).
+ * The backward takes the forward's inputs q, k (read when norm = 1, nullable otherwise) and the gradients of
+ * its outputs, dense or with strides ld_qo, ld_ko, and gives dq, dk (dense; may be dq_out, dk_out when those
+ * are dense) and, for norm = 1, dwq, dwk fp32 [D] (nullable), summed in a fixed order in the workspace. */
+typedef enum kda_rope_layout { KDA_ROPE_HALF = 0, KDA_ROPE_PAIRS = 1 } kda_rope_layout;
+typedef struct kda_rope_problem {
+    int64_t T;       /* tokens, >= 0 */
+    int32_t Hq, Hk;  /* heads of q and of k, 0 .. 65535, not both 0 */
+    int32_t D;       /* channels of a head, even, 2 .. 256 (above: KDA_ERR_UNSUPPORTED) */
+    int32_t R;       /* channels that turn, even, 0 .. D */
+    int32_t layout;  /* kda_rope_layout */
+    int32_t norm;    /* 1 or 0 */
+    int32_t dtype;   /* kda_dtype */
+    float eps;       /* of the norm */
+    float scale;     /* factor on the turned channels (kda_rope_frequencies; else 1) */
+    int64_t ld_q, ld_k, ld_qo, ld_ko; /* token strides; 0 = Hq D, Hk D */
+} kda_rope_problem;
+kda_status kda_rope_workspace_size(const kda_rope_problem* p, size_t* ws_bytes);
+kda_status kda_rope_fwd(const kda_rope_problem* p, const void* q, const void* k, const int32_t* pos,
+                        const double* freq, const float* wq, const float* wk, void* q_out,
+                        void* k_out, kda_stream_t stream);
+kda_status kda_rope_bwd(const kda_rope_problem* p, const void* q, const void* k, const int32_t* pos,
+                        const double* freq, const float* wq, const float* wk, const void* dq_out,
+                        const void* dk_out, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                        size_t ws_bytes, kda_stream_t stream);
+/* Host side: the R / 2 frequencies of a rotation into freq (a HOST array) and its factor into *scale
+ * (nullable).  Plain: f_i = base^(-2 i / R).  For contexts `factor` times longer than the `trained` one:
+ *   KDA_ROPE_LINEAR  f_i / factor (positions are compressed);
+ *   KDA_ROPE_BASE    base * factor^(R / (R - 2)) in place of base (the slowest pair is compressed by factor);
+ *   KDA_ROPE_RAMP    pairs that turn at least `fast` times within `trained` tokens are kept, those
+ *                    that turn at most `slow` times are compressed by factor, the others in between in
+ *                    proportion to their turns; *scale = 0.1 ln(factor) + 1 (1 for the other kinds). */
+typedef enum kda_rope_scaling {
+    KDA_ROPE_PLAIN = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_BASE = 2, KDA_ROPE_RAMP = 3
+} kda_rope_scaling;
+kda_status kda_rope_frequencies(int32_t R, double base, int scaling, double factor, double trained,
+                                double slow, double fast, double* freq, float* scale);
+
 /* Copies the device status word of `ws` to the host (synchronises `stream`) and clears it.
  * *device_status receives a kda_status value (KDA_OK when no device-side error happened). */
 kda_status kda_read_device_status(void* ws, int* device_status, kda_stream_t stream);

@@ -418,7 +418,9 @@ enum KernelKind {
     KK_PLAN, KK_INTRA_FWD, KK_CHAIN_FWD, KK_CHAIN_BWD, KK_BWD_GEMMS, KK_BWD_INTRA,
     KK_PARAM_REDUCE, KK_WALK, KK_CONV_FWD, KK_CONV_BWD, KK_CONV_REDUCE,
     KK_CONV_TAIL, KK_CONV_STEP, KK_SSM_STATE, KK_SSM_CARRY, KK_SSM_OUT, KK_SSM_RSTATE, KK_SSM_RCARRY,
-    KK_SSM_BWD, KK_SSM_REDUCE, KK_SSM_STEP, KK_LN_FWD, KK_LN_BWD, KK_LN_REDUCE, KK_COUNT
+    KK_SSM_BWD, KK_SSM_REDUCE, KK_SSM_STEP, KK_LN_FWD, KK_LN_BWD, KK_LN_REDUCE,
+    KK_LIN_PLAN, KK_LIN_STATE, KK_LIN_CARRY, KK_LIN_WALK, KK_LIN_SHARE, KK_LIN_STEP,
+    KK_ROPE_FWD, KK_ROPE_BWD, KK_ROPE_REDUCE, KK_COUNT
 };
 const char* kernel_name(int kind);
 class ProfScope {

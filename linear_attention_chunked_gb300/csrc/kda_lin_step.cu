@@ -1,0 +1,76 @@
+// Linear attention with a decay for each head, single tokens: one step of every sequence's states.
+//
+//   h <- lambda h + k v^T,  o = scale h^T q      per sequence and head, h [128 keys][128 values] fp32
+//
+// Bound by HBM: a head's state is 64 KB read and written once against 1 KB of rows.  A block takes one
+// (sequence, head): a warp reads whole key rows of 512 bytes, all of a thread's 16 loads in flight before the
+// first use, and the key rows' terms of o are added across lanes' registers and warps at the end.
+#include "kda_lin.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int LS_THREADS = 256;
+constexpr int LS_WARPS = LS_THREADS / 32, LS_ROWS = D / LS_WARPS;  // key rows of a warp
+
+__global__ void __launch_bounds__(LS_THREADS) k_lin_step(LinStepArgs a) {
+    __shared__ float qs[D], ks[D];
+    __shared__ float4 part[LS_WARPS][32];
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int h = int(blockIdx.x % unsigned(a.H)), n = int(blockIdx.x / unsigned(a.H));
+    __nv_bfloat16* o = a.o + (size_t(n) * a.H + h) * D;
+    int64_t slot = n;
+    if (a.slots) {
+        slot = a.slots[n];
+        if (slot >= a.nslots && tid == 0 && a.status) *a.status = KDA_ERR_DEVICE_CHECK;
+        if (slot < 0 || slot >= a.nslots) {  // an unused row: o is zero and no state is touched
+            if (tid < D / 2) reinterpret_cast<uint32_t*>(o)[tid] = 0u;
+            return;
+        }
+    }
+    const size_t at = (size_t(slot) * a.H + h) * D * D + size_t(w) * LS_ROWS * D + 4 * lane;
+    float4 s[LS_ROWS];
+#pragma unroll
+    for (int i = 0; i < LS_ROWS; ++i) s[i] = *reinterpret_cast<const float4*>(a.hin + at + size_t(i) * D);
+    if (tid < D) qs[tid] = a.scale * bf2f(a.q[n * a.ldq + (h / a.share) * D + tid]);
+    else ks[tid - D] = bf2f(a.k[n * a.ldk + (h / a.share) * D + tid - D]);
+    const uint2 vb = *reinterpret_cast<const uint2*>(a.v + n * a.ldv + h * D + 4 * lane);
+    const float v0 = __uint_as_float(vb.x << 16), v1 = __uint_as_float(vb.x & 0xffff0000u);
+    const float v2 = __uint_as_float(vb.y << 16), v3 = __uint_as_float(vb.y & 0xffff0000u);
+    const float lam = expf(a.slope[h]);
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < LS_ROWS; ++i) {
+        const float k = ks[w * LS_ROWS + i], q = qs[w * LS_ROWS + i];
+        s[i].x = fmaf(lam, s[i].x, k * v0);
+        s[i].y = fmaf(lam, s[i].y, k * v1);
+        s[i].z = fmaf(lam, s[i].z, k * v2);
+        s[i].w = fmaf(lam, s[i].w, k * v3);
+        *reinterpret_cast<float4*>(a.hout + at + size_t(i) * D) = s[i];
+        acc.x = fmaf(q, s[i].x, acc.x);
+        acc.y = fmaf(q, s[i].y, acc.y);
+        acc.z = fmaf(q, s[i].z, acc.z);
+        acc.w = fmaf(q, s[i].w, acc.w);
+    }
+    part[w][lane] = acc;
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < LS_WARPS; ++i) {
+            const float4 p = part[i][lane];
+            acc.x += p.x, acc.y += p.y, acc.z += p.z, acc.w += p.w;
+        }
+        *reinterpret_cast<uint2*>(o + 4 * lane) = make_uint2(pack2(acc.x, acc.y), pack2(acc.z, acc.w));
+    }
+}
+
+}  // namespace
+
+void launch_lin_step(const LinStepArgs& a, cudaStream_t st) {
+    ProfScope ps(KK_LIN_STEP, st);
+    k_lin_step<<<unsigned(a.N) * unsigned(a.H), LS_THREADS, 0, st>>>(a);
+}
+
+}  // namespace kda

@@ -23,7 +23,10 @@ const char* const kNames[KK_COUNT] = {"k_plan",      "k_intra_fwd",    "k_chain_
                                       "k_conv_step",    "k_ssm_state",    "k_ssm_carry",
                                       "k_ssm_out",      "k_ssm_rstate",   "k_ssm_rcarry",
                                       "k_ssm_bwd",      "k_ssm_reduce",   "k_ssm_step",
-                                      "k_ln_fwd",       "k_ln_bwd",       "k_ln_reduce"};
+                                      "k_ln_fwd",       "k_ln_bwd",       "k_ln_reduce",
+                                      "k_lin_plan",     "k_lin_state",    "k_lin_carry",
+                                      "k_lin_walk",     "k_lin_share",    "k_lin_step",
+                                      "k_rope_fwd",     "k_rope_bwd",     "k_rope_reduce"};
 }  // namespace
 
 const char* kernel_name(int kind) { return (kind >= 0 && kind < KK_COUNT) ? kNames[kind] : "?"; }

@@ -25,6 +25,9 @@ KDA_GATE_G, KDA_GATE_RAW = 0, 1
 KDA_OP_FWD, KDA_OP_BWD_SAVED, KDA_OP_BWD_REPLAY, KDA_OP_FRAGMENT, KDA_OP_WALK = 0, 1, 2, 3, 4
 KDA_FRAG_FWD, KDA_FRAG_BWD = 0, 1
 KDA_DT_BF16, KDA_DT_FP16, KDA_DT_FP32 = 0, 1, 2
+KDA_ROPE_HALF, KDA_ROPE_PAIRS = 0, 1
+KDA_ROPE_PLAIN, KDA_ROPE_LINEAR, KDA_ROPE_BASE, KDA_ROPE_RAMP = 0, 1, 2, 3
+ROPE_SCALINGS = {"plain": KDA_ROPE_PLAIN, "linear": KDA_ROPE_LINEAR, "base": KDA_ROPE_BASE, "ramp": KDA_ROPE_RAMP}
 _DTYPES = {torch.bfloat16: KDA_DT_BF16, torch.float16: KDA_DT_FP16, torch.float32: KDA_DT_FP32}
 KDA_WALK_FP32, KDA_WALK_TF32, KDA_WALK_TF32_HILO, KDA_WALK_BF16X3, KDA_WALK_BF16X3_HW = 0, 1, 2, 3, 4
 WALK_PRECISIONS = {"fp32": KDA_WALK_FP32, "tf32": KDA_WALK_TF32, "tf32_hilo": KDA_WALK_TF32_HILO,
@@ -35,7 +38,9 @@ EXPORTS = ("kda_workspace_size", "kda_fwd", "kda_fwd_static_ws", "kda_bwd", "kda
            "kda_transfer_walk", "kda_conv_workspace_size", "kda_conv_fwd", "kda_conv_bwd",
            "kda_conv_tail", "kda_conv_step", "kda_ssm_workspace_size", "kda_ssm_fwd", "kda_ssm_bwd",
            "kda_ssm_step", "kda_layernorm_workspace_size", "kda_layernorm_fwd",
-           "kda_layernorm_bwd", "kda_read_device_status", "kda_profile_enable",
+           "kda_layernorm_bwd", "kda_linattn_workspace_size", "kda_linattn_fwd", "kda_linattn_bwd",
+           "kda_linattn_step", "kda_rope_workspace_size", "kda_rope_fwd", "kda_rope_bwd",
+           "kda_rope_frequencies", "kda_read_device_status", "kda_profile_enable",
            "kda_profile_collect", "kda_kernel_count", "kda_kernel_name", "kda_launch_counter",
            "kda_status_string")
 
@@ -71,6 +76,21 @@ class kda_ssm_problem(ctypes.Structure):
 class kda_layernorm_problem(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("eps", ctypes.c_float)]
+
+
+class kda_linattn_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64),
+                ("ld_v", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p)]
+
+
+class kda_rope_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("R", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64),
+                ("ld_qo", ctypes.c_int64), ("ld_ko", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -114,6 +134,16 @@ def lib():
             L.kda_layernorm_workspace_size.argtypes = [NP, ctypes.POINTER(S)]
             L.kda_layernorm_fwd.argtypes = [NP] + [V] * 9
             L.kda_layernorm_bwd.argtypes = [NP] + [V] * 10 + [S, V]
+            AP = ctypes.POINTER(kda_linattn_problem)
+            L.kda_linattn_workspace_size.argtypes = [AP, I, ctypes.POINTER(S), ctypes.POINTER(S)]
+            L.kda_linattn_fwd.argtypes = [AP] + [V] * 9 + [S, V]
+            L.kda_linattn_bwd.argtypes = [AP] + [V] * 13 + [S, V]
+            L.kda_linattn_step.argtypes = [AP] + [V] * 5 + [ctypes.c_int64] + [V] * 5
+            RP, F64 = ctypes.POINTER(kda_rope_problem), ctypes.c_double
+            L.kda_rope_workspace_size.argtypes = [RP, ctypes.POINTER(S)]
+            L.kda_rope_fwd.argtypes = [RP] + [V] * 9
+            L.kda_rope_bwd.argtypes = [RP] + [V] * 13 + [S, V]
+            L.kda_rope_frequencies.argtypes = [ctypes.c_int32, F64, I, F64, F64, F64, F64, V, V]
             L.kda_read_device_status.argtypes = [V, ctypes.POINTER(I), V]
             L.kda_selftest_wait_timeout.argtypes = [V, ctypes.c_uint32, V]
             L.kda_profile_enable.argtypes = [I]
@@ -130,7 +160,10 @@ def lib():
                          "kda_conv_bwd", "kda_conv_tail", "kda_conv_step", "kda_ssm_workspace_size",
                          "kda_ssm_fwd", "kda_ssm_bwd", "kda_ssm_step",
                          "kda_layernorm_workspace_size", "kda_layernorm_fwd",
-                         "kda_layernorm_bwd", "kda_read_device_status", "kda_selftest_wait_timeout",
+                         "kda_layernorm_bwd", "kda_linattn_workspace_size", "kda_linattn_fwd",
+                         "kda_linattn_bwd", "kda_linattn_step", "kda_rope_workspace_size",
+                         "kda_rope_fwd", "kda_rope_bwd", "kda_rope_frequencies",
+                         "kda_read_device_status", "kda_selftest_wait_timeout",
                          "kda_profile_enable",
                          "kda_profile_collect", "kda_kernel_count"):
                 getattr(L, name).restype = ctypes.c_int
@@ -717,6 +750,236 @@ def kda_layernorm_bwd(x, w, mean, rstd, dy, *, dsum=None, ws=None):
     _call(fn, dev, ctypes.byref(pr), x.data_ptr(), _at(w), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
           _at(dsum), out["dx"].data_ptr(), out["dw"].data_ptr(), out["db"].data_ptr(), ws.data_ptr(),
           ws_n)
+    return out
+
+
+@functools.lru_cache(maxsize=256)  # the sizes are a function of these numbers alone
+def kda_linattn_workspace_size(T, N, H, Hk, op):
+    """Returns (workspace bytes, saved-set bytes) of the linear attention's op."""
+    pr = kda_linattn_problem(int(T), int(N), int(H), int(Hk), D, KDA_DT_BF16, 1.0, 0, 0, 0, 16)  # cu_seqlens is not read
+    ws, sv = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("kda_linattn_workspace_size",
+           lib().kda_linattn_workspace_size(ctypes.byref(pr), int(op), ctypes.byref(ws), ctypes.byref(sv)))
+    return ws.value, sv.value
+
+
+def _check_rows(fn, name, t):
+    """Rows that the library copies by 16 bytes."""
+    if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
+        raise ValueError(f"{fn}: {name} is not aligned to 16 bytes (address {t.data_ptr():#x}, token stride {t.stride(0)})")
+
+
+def _linattn_problem(fn, q, k, v, slope, scale, N, cu_seqlens):
+    """Checks the linear attention's inputs and describes the call."""
+    if v.dim() != 3 or q.dim() != 3:
+        raise ValueError(f"{fn}: q and v have shapes {tuple(q.shape)} and {tuple(v.shape)}, expected [T, heads, {D}]")
+    (T, H, d), Hk, dev = v.shape, q.shape[1], v.device
+    if v.dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: v is {v.dtype}, expected {torch.bfloat16}")
+    if d != D:
+        raise ValueError(f"{fn}: v has head dim {d}, expected {D}")
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{fn}: {Hk} query and key heads do not divide {H} value heads")
+    _check_tensor(fn, "q", q, (T, Hk, D), torch.bfloat16, dev, True)
+    _check_tensor(fn, "k", k, (T, Hk, D), torch.bfloat16, dev, True)
+    _check_tensor(fn, "v", v, (T, H, D), torch.bfloat16, dev, True)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_rows(fn, name, t)
+    _check_tensor(fn, "slope", slope, (H,), torch.float32, dev)
+    if cu_seqlens is not None:
+        _check_tensor(fn, "cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    return kda_linattn_problem(T, N, H, Hk, D, KDA_DT_BF16, float(scale), _row_stride(q), _row_stride(k), _row_stride(v),
+                               None if cu_seqlens is None else cu_seqlens.data_ptr())
+
+
+def kda_linattn_fwd(q, k, v, slope, cu_seqlens, *, h0=None, scale=1.0, save=True, o=None, ht=None,
+                    saved=None, ws=None):
+    """Linear attention with a decay exp(slope[h]) for each head over packed documents: q, k
+    [T, Hk, 128], v [T, H, 128] bf16 (Hk divides H; views with a token stride are taken as they are),
+    slope [H], h0 [N, H, 128, 128] fp32.  Returns (o [T, H, 128], ht [N, H, 128, 128], saved) -- saved is
+    None when save=False."""
+    fn = "kda_linattn_fwd"
+    N, dev = cu_seqlens.numel() - 1, v.device
+    pr = _linattn_problem(fn, q, k, v, slope, scale, N, cu_seqlens)
+    ws_b, sv_b = kda_linattn_workspace_size(pr.T, N, pr.H, pr.Hk, KDA_OP_FWD)
+    state = (N, pr.H, D, D)
+    ws, ws_n = _workspace(fn, ws, ws_b, dev)
+    if not save:
+        saved = None
+    elif saved is None:
+        saved = _empty_bytes(sv_b, dev)
+    else:
+        _check_bytes(fn, "saved", saved, sv_b, dev)
+    if o is None:
+        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(fn, "o", o, v.shape, torch.bfloat16, dev)
+    if ht is None:
+        ht = torch.empty(state, dtype=torch.float32, device=dev)
+    else:
+        _check_tensor(fn, "ht", ht, state, torch.float32, dev)
+    _check_tensor(fn, "h0", h0, state, torch.float32, dev)
+    _call(fn, dev, ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), slope.data_ptr(), _at(h0), o.data_ptr(),
+          ht.data_ptr(), _at(saved), ws.data_ptr(), ws_n)
+    return o, ht, saved
+
+
+def kda_linattn_bwd(q, k, v, slope, cu_seqlens, dO, *, saved=None, h0=None, dht=None, scale=1.0,
+                    want_dh0=True, ws=None):
+    """Backward of the linear attention for L = sum(o * dO) + sum(ht * dht) (saved=None: what the forward
+    kept is recomputed).  Returns a dict: dq, dk [T, Hk, 128] and dv [T, H, 128] bf16, and dh0 fp32 when
+    wanted."""
+    fn = "kda_linattn_bwd"
+    N, dev = cu_seqlens.numel() - 1, v.device
+    pr = _linattn_problem(fn, q, k, v, slope, scale, N, cu_seqlens)
+    state = (N, pr.H, D, D)
+    _check_tensor(fn, "dO", dO, v.shape, torch.bfloat16, dev)
+    _check_tensor(fn, "h0", h0, state, torch.float32, dev)
+    _check_tensor(fn, "dht", dht, state, torch.float32, dev)
+    ws_b, sv_b = kda_linattn_workspace_size(pr.T, N, pr.H, pr.Hk, KDA_OP_BWD_REPLAY if saved is None else KDA_OP_BWD_SAVED)
+    if saved is not None:
+        _check_bytes(fn, "saved", saved, sv_b, dev)
+    ws, ws_n = _workspace(fn, ws, ws_b, dev)
+    rows = dict(dtype=torch.bfloat16, device=dev)
+    out = dict(dq=torch.empty(q.shape, **rows), dk=torch.empty(q.shape, **rows), dv=torch.empty(v.shape, **rows))
+    if want_dh0:
+        out["dh0"] = torch.empty(state, dtype=torch.float32, device=dev)
+    _call(fn, dev, ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), slope.data_ptr(), _at(h0), dO.data_ptr(),
+          _at(dht), _at(saved), out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(), _at(out.get("dh0")),
+          ws.data_ptr(), ws_n)
+    return out
+
+
+def kda_linattn_step(q, k, v, slope, h, *, scale=1.0, slots=None, h_out=None, o=None, ws=None):
+    """The linear attention of one token per sequence: q, k [N, Hk, 128], v [N, H, 128] bf16, h
+    [n_slots, H, 128, 128] fp32 the states (row n's is h[slots[n]], h[n] without slots).  Returns
+    (o [N, H, 128], h_out); h_out defaults to h, updated in place.  A negative slot marks an unused row;
+    ws (optional, >= 256 bytes) receives the device status of this call."""
+    fn = "kda_linattn_step"
+    N, dev = v.shape[0], v.device
+    pr = _linattn_problem(fn, q, k, v, slope, scale, N, None)
+    _check_tensor(fn, "h", h, (h.shape[0], pr.H, D, D), torch.float32, dev)
+    if h_out is None:
+        h_out = h
+    else:
+        _check_tensor(fn, "h_out", h_out, h.shape, torch.float32, dev)
+    if o is None:
+        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(fn, "o", o, v.shape, torch.bfloat16, dev)
+    _slots(fn, slots, N, h.shape[0], dev)
+    if ws is not None:
+        _check_bytes(fn, "ws", ws, 256, dev)
+    _call(fn, dev, ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), slope.data_ptr(), _at(slots), h.shape[0],
+          h.data_ptr(), h_out.data_ptr(), o.data_ptr(), _at(ws))
+    return o, h_out
+
+
+def kda_rope_frequencies(R, base=10000.0, *, scaling="plain", factor=1.0, trained=4096, slow=1.0, fast=32.0,
+                         device="cuda"):
+    """The frequencies [R / 2] (fp64, radians per token) of a rotation of R channels, and its factor.
+    scaling: 'plain', or for contexts `factor` times longer than the `trained` one 'linear' (positions
+    compressed), 'base' (a larger base) or 'ramp' (by the pairs' turns within the trained context, between
+    slow and fast)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"kda_rope_frequencies: scaling must be one of {', '.join(ROPE_SCALINGS)}, got {scaling!r}")
+    f, s = (ctypes.c_double * max(R // 2, 1))(), ctypes.c_float(0)
+    _check("kda_rope_frequencies",
+           lib().kda_rope_frequencies(int(R), float(base), ROPE_SCALINGS[scaling], float(factor), float(trained), float(slow),
+                                      float(fast), f, ctypes.byref(s)))
+    return torch.tensor(list(f[:R // 2]), dtype=torch.float64, device=device), s.value
+
+
+def _rope_rows(fn, name, t, shape, dtype, dev):
+    """One tensor of a rope call: dense heads, any token stride."""
+    _check_tensor(fn, name, t, shape, dtype, dev, True)
+
+
+def _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale):
+    """Checks what the forward and the backward share; k may be None (no key heads)."""
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError(f"{fn}: q and k must be [T, heads, channels]")
+    (T, Hq, C), dev, dtype = q.shape, q.device, q.dtype
+    Hk = 0 if k is None else k.shape[1]
+    if dtype not in _DTYPES:
+        raise ValueError(f"{fn}: q is {dtype}, expected one of bfloat16, float16, float32")
+    _rope_rows(fn, "q", q, (T, Hq, C), dtype, dev)
+    _rope_rows(fn, "k", k, (T, Hk, C), dtype, dev)
+    _check_tensor(fn, "pos", pos, (T,), torch.int32, dev)
+    _check_tensor(fn, "freq", freq, (freq.numel(),), torch.float64, dev)
+    if 2 * freq.numel() > C:
+        raise ValueError(f"{fn}: {freq.numel()} frequencies turn more channels than the {C} of a head")
+    if not norm and (wq is not None or wk is not None):
+        raise ValueError(f"{fn}: wq and wk belong to the norm (norm=True)")
+    _check_tensor(fn, "wq", wq, (C,), torch.float32, dev)
+    _check_tensor(fn, "wk", wk, (C,), torch.float32, dev)
+    return kda_rope_problem(T, Hq, Hk, C, 2 * freq.numel(), KDA_ROPE_PAIRS if interleaved else KDA_ROPE_HALF, int(bool(norm)),
+                            _DTYPES[dtype], float(eps), float(scale), _row_stride(q), _row_stride(k), 0, 0)
+
+
+def kda_rope_workspace_size(D, *, norm=True):
+    """Workspace bytes of kda_rope_bwd for heads of D channels."""
+    pr = kda_rope_problem(1, 1, 1, int(D), 0, KDA_ROPE_HALF, int(bool(norm)), KDA_DT_BF16, 1e-6, 1.0, 0, 0, 0, 0)
+    ws = ctypes.c_size_t(0)
+    _check("kda_rope_workspace_size", lib().kda_rope_workspace_size(ctypes.byref(pr), ctypes.byref(ws)))
+    return ws.value
+
+
+def kda_rope_fwd(q, k, pos, freq, *, wq=None, wk=None, norm=False, eps=1e-6, interleaved=False, scale=1.0,
+                 q_out=None, k_out=None):
+    """Norm of every head of q [T, Hq, D] and k [T, Hk, D] (bf16, fp16, fp32; k may be None) with weights
+    wq, wk fp32 [D] (norm=True), and the rotation of their first 2 * freq.numel() channels to positions
+    pos int32 [T] with freq fp64 (kda_rope_frequencies).  interleaved: pairs of neighbours, else of
+    halves; scale: the rotation's factor.  Views with a token stride are taken as they are, and q_out,
+    k_out may be q, k.  Returns (q_out, k_out)."""
+    fn = "kda_rope_fwd"
+    pr = _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif q_out is not q:
+        _rope_rows(fn, "q_out", q_out, q.shape, q.dtype, dev)
+    if k is None:
+        if k_out is not None:
+            raise ValueError(f"{fn}: k_out needs a k")
+    elif k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    elif k_out is not k:
+        _rope_rows(fn, "k_out", k_out, k.shape, q.dtype, dev)
+    pr.ld_qo, pr.ld_ko = _row_stride(q_out), _row_stride(k_out)
+    _call(fn, dev, ctypes.byref(pr), q.data_ptr(), _at(k), pos.data_ptr(), freq.data_ptr(), _at(wq), _at(wk),
+          q_out.data_ptr(), _at(k_out))
+    return q_out, k_out
+
+
+def kda_rope_bwd(q, k, pos, freq, dq_out, dk_out, *, wq=None, wk=None, norm=False, eps=1e-6, interleaved=False,
+                 scale=1.0, ws=None):
+    """Backward of kda_rope_fwd: q, k are the forward's inputs, dq_out, dk_out the gradients of its outputs
+    (views with a token stride are taken as they are).  Returns a dict: dq, dk (when k is given) dense, in
+    the inputs' type, and for weights that are given dwq, dwk fp32 [D]."""
+    fn = "kda_rope_bwd"
+    pr = _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale)
+    dev = q.device
+    _rope_rows(fn, "dq_out", dq_out, q.shape, q.dtype, dev)
+    if k is None:
+        if dk_out is not None:
+            raise ValueError(f"{fn}: dk_out needs a k")
+    else:
+        _rope_rows(fn, "dk_out", dk_out, k.shape, q.dtype, dev)
+    pr.ld_qo, pr.ld_ko = _row_stride(dq_out), _row_stride(dk_out)
+    out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev))
+    if k is not None:
+        out["dk"] = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    if wq is not None:
+        out["dwq"] = torch.empty_like(wq)
+    if wk is not None:
+        out["dwk"] = torch.empty_like(wk)
+    ws_n = 0
+    if "dwq" in out or "dwk" in out:
+        ws, ws_n = _workspace(fn, ws, kda_rope_workspace_size(pr.D), dev)
+    _call(fn, dev, ctypes.byref(pr), q.data_ptr(), _at(k), pos.data_ptr(), freq.data_ptr(), _at(wq), _at(wk),
+          dq_out.data_ptr(), _at(dk_out), out["dq"].data_ptr(), _at(out.get("dk")), _at(out.get("dwq")),
+          _at(out.get("dwk")), _at(ws) if ws_n else None, ws_n)
     return out
 
 
