@@ -1,70 +1,607 @@
-// Linear attention with a decay for each head: the walk over packed documents.
+// Linear attention with a decay for each head: the chunked walk over packed documents on tcgen05 tensor cores.
+//
+// Chunks of 128 tokens.  Per segment of a document (kda_lin_plan.cu), head and pass, chunk after chunk, with the
+// state X [128 key channels][128 value channels] in fp32 (forwards; n tokens in the chunk, i, j < n):
+//     P    = Query Key^T                              [i][j]
+//     P'   = P lambda^(i - j) for j <= i, else 0      rounded to bf16
+//     Out  = by (P' Value + lambda^(i + 1) Query X)   X as an operand rounded to bf16
+//     X   <- lambda^n X + (in lambda^(n - 1 - j) Value_j)^T Key_j, summed
+// Backwards (the state is Y, see kda_lin.cuh) the mask is j >= i with lambda^(j - i), Query Y takes lambda^(n - 1 - i)
+// and Value_j takes lambda^(j + 1).
+//
+// Bound by HBM: 1 KB of rows a token and head against 5 products of 128^3 a chunk (and 2 more of the state's), half
+// of the tensor cores' time at HBM's rate.  One block per multiprocessor; its state stays in tensor memory as X^T (lane
+// = value channel), the scaled values are the state product's left operand in tensor memory, split into three
+// bf16 planes (8 + 8 + 8 bits: exact, so the state's products are fp32 products), Q, K and V come by TMA, two chunks
+// deep, and every product reads them where they land:
+//     P      A = Query [tokens][keys],    B = Key [tokens][keys]
+//     QX     A = Query,                   B = X^T in shared memory, bf16 [values][keys]
+//     P'V    A = P' (tensor memory),      B = Value [tokens][values] read across
+//     state  A = values^T (tensor memory), B = Key read across
+// Four groups of warps work at once: A scales and splits the values, B masks and rounds the scores and scales Query X's
+// rows, C rounds and decays the state and stores the output, and two single threads issue loads and products.
+// Rows behind a document's end (another's) are cleared in K and V, so nothing of them, were it not finite, is multiplied.
 #include "kda_lin.cuh"
+#include "kda_ssm.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 
+void launch_lin_carry(const LinArgs& a, int pass, cudaStream_t st);
+
 namespace {
 
-constexpr int LIN_ROWS = 16;  // tokens staged together
+constexpr uint32_t TILE = LC * D * 2;  // bytes of one chunk's rows of one head
 
-// One block per document, head and pass; thread j holds column j of the state.
-__global__ void __launch_bounds__(128) k_lin_recur(LinArgs a) {
-    __shared__ float sq[LIN_ROWS][D], sk[LIN_ROWS][D];
-    const int j = threadIdx.x;
-    const int ps = int(blockIdx.x % unsigned(a.passes)), rest = int(blockIdx.x / unsigned(a.passes));
-    const int h = rest % a.H, n = rest / a.H;
-    const LinPass& p = a.pass[ps];
+// lambda^n = exp(slope n), 1 for n = 0 whatever the slope
+__device__ __forceinline__ float decay(float slope, int n) { return n == 0 ? 1.f : expf(slope * float(n)); }
+
+// ---- tensor memory, packed words ----
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread: A's row i is lane i, its 16-bit elements 2 c and 2 c + 1 lie in
+// column c.
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// One arrival for a warp whose lanes have all finished their part
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// 128-byte-swizzled tile pair [2 blocks of 64 channels][128 tokens][128 bytes]: clears the rows from n on.  128 threads.
+__device__ __forceinline__ void clear_rows(unsigned char* tile, int n, int tid) {
+    for (int i = tid; i < 2 * (LC - n) * 8; i += 128) {
+        const int c = i & 7, r = n + ((i >> 3) % (LC - n)), b = (i >> 3) / (LC - n);
+        *reinterpret_cast<uint4*>(tile + b * (TILE / 2) + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// The chunk's values of channel `ch` times the tokens' factors, split into three bf16 planes, as the rows of a product's
+// left operand in tensor memory: lane `ch`, token pairs in columns hi, mid, lo (taddrs with the lane set).
+// f: the factors in shared memory, times `all`.
+__device__ __forceinline__ void split_values(const unsigned char* tile, int ch, const float* f, float all, uint32_t hi,
+                                             uint32_t mid, uint32_t lo) {
+    const unsigned char* base = tile + (ch >> 6) * (TILE / 2) + (ch & 7) * 2;
+    const int c8 = (ch & 63) >> 3;
+    int off[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) off[j] = j * 128 + ((c8 ^ j) << 4);
+    const f2 all2 = pk2(all, all);
+    const uint32_t mask = 0xffff0000u, flip = 0x80000000u;
+#pragma unroll 1
+    for (int t0 = 0; t0 < LC; t0 += 32) {
+        uint32_t h[16], m[16], l[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int t = 2 * j;
+            const unsigned char* row = base + (t0 + (t & ~7)) * 128;
+            const float x0 = __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(row + off[t & 7])) << 16);
+            const float x1 = __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(row + off[(t & 7) + 1])) << 16);
+            const f2 y = mul2(mul2(*reinterpret_cast<const f2*>(f + t0 + t), all2), pk2(x0, x1));
+            float y0, y1, r0, r1;
+            up2(y, y0, y1);
+            h[j] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
+            const f2 r = add2(y, pk2(__uint_as_float((__float_as_uint(y0) & mask) ^ flip),
+                                     __uint_as_float((__float_as_uint(y1) & mask) ^ flip)));
+            up2(r, r0, r1);
+            m[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            const f2 q = add2(r, pk2(__uint_as_float((__float_as_uint(r0) & mask) ^ flip),
+                                     __uint_as_float((__float_as_uint(r1) & mask) ^ flip)));
+            up2(q, r0, r1);
+            l[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+        }
+        tmem_st16u(hi + t0 / 2, h);
+        tmem_st16u(mid + t0 / 2, m);
+        tmem_st16u(lo + t0 / 2, l);
+    }
+    tmem_wait_st();
+}
+
+// The segment of a block: {document, first token, length, flags as in LinPlan, w}; false: none (or malformed offsets)
+struct Seg {
+    int doc, t0, len, w;
+    bool first, last;
+};
+__device__ __forceinline__ bool lin_segment(const LinArgs& a, int i, Seg& s) {
+    if (!a.direct) {
+        if (i >= a.plan.counts[0]) return false;
+        const int4 e = a.plan.tab[i];
+        s.doc = e.x, s.t0 = e.y, s.len = e.z & 0xffff, s.w = e.w;
+        s.first = e.z >> 16 & 1, s.last = e.z >> 17 & 1;
+        return true;
+    }
+    const int c0 = a.cu[i], c1 = a.cu[i + 1];
+    bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && (i > 0 || c0 == 0) && (i < a.N - 1 || c1 == a.T);
     if (a.expected) {
         const int4 m = *a.expected;
-        if (m.x != a.sizes.x || m.y != a.sizes.y || m.z != a.sizes.z || m.w != a.sizes.w) {
-            if (j == 0) *a.status = KDA_ERR_DEVICE_CHECK;
-            return;
-        }
+        ok = ok && m.x == a.sizes.x && m.y == a.sizes.y && m.z == a.sizes.z && m.w == a.sizes.w;
     }
-    if (a.made_for && blockIdx.x == 0 && j == 0) *a.made_for = a.sizes;
-    const int c0 = a.cu[n], c1 = a.cu[n + 1];
-    if (c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0) || (n == a.N - 1 && c1 != a.T)) {
-        if (j == 0) *a.status = KDA_ERR_DEVICE_CHECK;
+    if (!ok) {
+        if (threadIdx.x == 0) *a.status = KDA_ERR_DEVICE_CHECK;
+        return false;
+    }
+    if (a.made_for && blockIdx.x == 0 && threadIdx.x == 0) *a.made_for = a.sizes;
+    s = {i, c0, c1 - c0, 0, true, true};
+    return true;
+}
+
+// ---- the walk ----
+
+constexpr int WALK_THREADS = 448;  // A: warps 0-3, B: 4-7, C: 8-11, loads: 12, products: 13
+constexpr int W_STAGE = 0;         // [2 stages][Query, Key, Value]
+constexpr int W_X = 6 * int(TILE);
+constexpr int W_TAB = W_X + int(TILE);   // decays [132], state factors of a full and of the short chunk [128], block factors [32]
+constexpr int W_BAR = W_TAB + (132 + 2 * 128 + 32) * 4;
+constexpr size_t WALK_SMEM = W_BAR + 192 + 1024;
+static_assert(WALK_SMEM <= 232448, "walk: shared memory above the opt-in limit");
+
+// tensor memory columns
+constexpr uint32_t C_P = 0, C_LO = 64, C_O = 128, C_X = 256, C_HI = 384, C_MID = 448;
+
+enum WalkBar { B_QK = 0, B_V = 2, B_EMPTY = 4, B_P = 6, B_PREAD, B_QX, B_B, B_A, B_S, B_C, B_O, B_OFREE, B_FIX, B_SPARE, B_END };
+
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const __grid_constant__ LinMaps tm) {
+    extern __shared__ unsigned char smraw[];
+    unsigned char* sm = tc::align1024(smraw);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int ps = int(blockIdx.x % unsigned(a.passes)), rest = int(blockIdx.x / unsigned(a.passes));
+    const int hd = rest % a.H;
+    const LinPass& p = a.pass[ps];
+    Seg g;
+    if (!lin_segment(a, rest / a.H, g)) return;
+    const bool back = p.back;
+    const size_t doc_state = (size_t(g.doc) * a.H + hd) * D * D;
+    // the state that the walk starts from, and where the document's last one goes
+    const bool starts = back ? g.last : g.first, ends = back ? g.first : g.last;
+    const float* x0 = starts ? (p.s0 ? p.s0 + doc_state : nullptr)
+                             : (back ? a.back + (size_t(g.w) * a.H + hd) * D * D
+                                     : a.front + (size_t(g.w - 1) * a.H + hd) * D * D);
+    float* x1 = ends && p.s_end ? p.s_end + doc_state : nullptr;
+    const int nc = (g.len + LC - 1) / LC;
+    if (nc == 0) {  // an empty document keeps its state
+        if (x1)
+            for (int i = tid; i < D * D; i += WALK_THREADS) x1[i] = x0 ? x0[i] : 0.f;
         return;
     }
-    const float lam = expf(a.slope[h]), pre = p.back ? 1.f : lam, post = p.back ? lam : 1.f;
-    const size_t sn = (size_t(n) * a.H + h) * D * D;
-    float S[D];
-#pragma unroll
-    for (int i = 0; i < D; ++i) S[i] = p.s0 ? p.s0[sn + (p.trans ? j * D + i : i * D + j)] : 0.f;
-    const int len = c1 - c0;
-    for (int r0 = 0; r0 < len; r0 += LIN_ROWS) {
-        const int m = min(LIN_ROWS, len - r0);
-        __syncthreads();
-        for (int r = 0; r < m; ++r) {
-            const int64_t t = p.back ? c1 - 1 - (r0 + r) : c0 + r0 + r;
-            sq[r][j] = bf2f(p.query[t * p.ldq + (h / p.rq) * D + j]);
-            sk[r][j] = bf2f(p.key[t * p.ldk + (h / p.rk) * D + j]);
-        }
-        __syncthreads();
-        for (int r = 0; r < m; ++r) {
-            const int64_t t = p.back ? c1 - 1 - (r0 + r) : c0 + r0 + r;
-            const float v = p.in * bf2f(p.value[t * p.ldv + (h / p.rv) * D + j]);
-            float o = 0.f;
-#pragma unroll
-            for (int i = 0; i < D; ++i) {
-                S[i] = fmaf(S[i], pre, sk[r][i] * v);
-                o = fmaf(sq[r][i], S[i], o);
-                S[i] *= post;
-            }
-            store_out(p.out, (size_t(t) * a.H + h) * D + j, p.by * o, p.out_fp32);
-        }
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + W_BAR);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + W_BAR + 8 * B_END);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + W_BAR + 8 * B_END + 4);
+    float* pw = reinterpret_cast<float*>(sm + W_TAB);  // lambda^i, i <= 128
+    float* fs = pw + 132;                              // a full chunk's state factors
+    float* fshort = fs + 128;                          // the short chunk's (of at most one)
+    float* fb = fshort + 128;                          // factors within 32 columns of the scores
+    const float slope = a.slope[hd];
+    if (tid == 0) {
+        for (int i = 0; i < B_SPARE; ++i)
+            tc::mbar_init(&bar[i], i == B_PREAD || i == B_B || i == B_A || i == B_C || i == B_OFREE || i == B_FIX ? 4 : 1);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
     }
-    if (p.s_end)
+    if (w == 0) tc::tmem_alloc(tslot, 512);
+    for (int i = tid; i <= LC; i += WALK_THREADS) pw[i] = decay(slope, i);
+    if (tid < LC) {
+        fs[tid] = p.in * decay(slope, back ? tid + 1 : LC - 1 - tid);
+        const int m = g.len - LC * (nc - 1);
+        fshort[tid] = tid < m ? p.in * decay(slope, back ? tid + 1 : m - 1 - tid) : 0.f;
+    }
+    if (tid < 32) fb[tid] = p.in * p.by * decay(slope, back ? tid : 31 - tid);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = *tslot;
+    const uint32_t tl = tbase + (uint32_t(32 * (w & 3)) << 16);  // this warp's lanes
+    const int row = 32 * (w & 3) + lane;
+
+    // chunk c of the walk: its place in the segment and its tokens
+    auto place = [&](int c) { return back ? nc - 1 - c : c; };
+    auto tokens = [&](int c) { return min(LC, g.len - LC * place(c)); };
+    auto tile = [&](int c, int which) { return sm + W_STAGE + ((c & 1) * 3 + which) * TILE; };
+    // whether chunk c's values still reach a state that is read
+    auto adds = [&](int c) { return c + 1 < nc || x1; };
+    // Waits for the turn-th completion of barrier b.  The lanes of a warp leave together (a wait that runs out of
+    // time ends the warp's part; every other wait runs out too, and the block reports and ends).
+    bool ok = true;
+    auto wait1 = [&](int b, int turn) {
+        if (ok && !tc::mbar_wait(&bar[b], uint32_t(turn) & 1u)) {
+            ok = false;
+            *abort_flag = 1;
+        }
+        tc::fence_after_sync();
+        return ok;
+    };
+    auto wait = [&](int b, int turn) { return ok = __all_sync(0xffffffffu, wait1(b, turn)); };
+
+    if (w < 4) {
+        // ---- A: the values, scaled and split ----
+        for (int c = 0; c < nc; ++c) {
+            const int n = tokens(c);
+            if (!wait(B_V + (c & 1), c >> 1)) break;
+            if (n < LC) {  // the rows of other documents: cleared before any product reads them (one chunk of a walk)
+                if (!wait(B_QK + (c & 1), c >> 1)) break;
+                clear_rows(tile(c, 1), n, tid);
+                clear_rows(tile(c, 2), n, tid);
+                tc::fence_async_smem();
+                warp_arrive(&bar[B_FIX], lane);
+                if (!wait(B_FIX, 0)) break;
+            }
+            if (!adds(c)) break;
+            if (c > 0 && !wait(B_S, c - 1)) break;
+            if (!wait(B_PREAD, c)) break;
+            split_values(tile(c, 2), row, n < LC ? fshort : fs, 1.f, tl + C_HI, tl + C_MID, tl + C_LO);
+            warp_arrive(&bar[B_A], lane);
+        }
+    } else if (w < 8) {
+        // ---- B: the scores; Query X's rows ----
+        const int q = w & 3;
+        const float both = p.in * p.by;
+        for (int c = 0; c < nc; ++c) {
+            const int n = tokens(c);
+            if (!wait(B_P, c)) break;
+            uint32_t o[4][16];
 #pragma unroll
-        for (int i = 0; i < D; ++i) p.s_end[sn + (p.trans ? j * D + i : i * D + j)] = S[i];
+            for (int j = 0; j < 4; ++j) {
+                const bool full = back ? j > q : j < q;
+                if (full || j == q) {
+                    float v[32];
+                    tc::tmem_ld32(tl + C_P + 32 * j, v);
+                    if (full) {
+                        // lambda^|row - s| in two factors, the second the same for every row
+                        const float e = pw[back ? 32 * j - row : row - 32 * j - 31];
+                        const f2 e2 = pk2(e, e);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const f2 y = mul2(mul2(*reinterpret_cast<const f2*>(fb + 2 * i), e2), pk2(v[2 * i], v[2 * i + 1]));
+                            up2(y, v[2 * i], v[2 * i + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int d = back ? i - lane : lane - i;
+                            v[i] = d >= 0 ? v[i] * (both * pw[max(d, 0)]) : 0.f;
+                        }
+                    }
+                    if (n < LC)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * j + i >= n) v[i] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[j][i] = pack2(v[2 * i], v[2 * i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[j][i] = 0u;
+                }
+            }
+            warp_arrive(&bar[B_PREAD], lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_st16u(tl + C_P + 16 * j, o[j]);
+            tmem_wait_st();
+            if (!wait(B_QX, c)) break;
+            const float f = p.by * pw[back ? max(n - 1 - row, 0) : row + 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v[32];
+                tc::tmem_ld32(tl + C_O + 32 * j, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= f;
+                tc::tmem_st32(tl + C_O + 32 * j, v);
+            }
+            warp_arrive(&bar[B_B], lane);
+        }
+    } else if (w < 12) {
+        // ---- C: the state as an operand, its decay; the output ----
+        unsigned char* xt = sm + W_X;
+        auto store_out = [&](int c) {
+            const int n = tokens(c), t = g.t0 + LC * place(c) + row;
+            const size_t off = (size_t(t) * a.H + hd) * D, ld = size_t(a.H) * D;
+            const int even = row & ~1;
+            float v[4][32];
+            if (p.out_fp32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    tc::tmem_ld32(tl + C_O + 32 * j, v[0]);
+                    tc::st_rows_paired_f32<32>(static_cast<float*>(p.out) + off + 32 * j, ld, v[0], lane, even < n, even + 1 < n);
+                }
+                warp_arrive(&bar[B_OFREE], lane);
+            } else {
+                uint4 x[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    tc::tmem_ld32(tl + C_O + 32 * j, v[j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[j][i] = make_uint4(pack2(v[j][8 * i], v[j][8 * i + 1]), pack2(v[j][8 * i + 2], v[j][8 * i + 3]),
+                                             pack2(v[j][8 * i + 4], v[j][8 * i + 5]), pack2(v[j][8 * i + 6], v[j][8 * i + 7]));
+                }
+                warp_arrive(&bar[B_OFREE], lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tc::st_rows_paired<4>(reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off + 32 * j), ld / 2,
+                                          x[j], lane, even < n, even + 1 < n);
+            }
+        };
+        for (int c = 0; c < nc; ++c) {
+            const float f = pw[tokens(c)];
+            if (c > 0 && !wait(B_S, c - 1)) break;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                float v[32];
+                if (c > 0) {
+                    tc::tmem_ld32(tl + C_X + 32 * j, v);
+                } else if (!x0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                } else if (p.trans) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(x0 + row * D + 32 * j + i);
+                        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = x0[(32 * j + i) * D + row];
+                }
+                uint32_t b[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
+                tc::st_sw128(xt + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= f;
+                tc::tmem_st32(tl + C_X + 32 * j, v);
+            }
+            tc::fence_async_smem();
+            warp_arrive(&bar[B_C], lane);
+            if (c > 0) {
+                if (!wait(B_O, c - 1)) break;
+                store_out(c - 1);
+            }
+        }
+        if (wait(B_O, nc - 1)) store_out(nc - 1);
+        if (x1 && wait(B_S, nc - 1)) {
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                float v[32];
+                tc::tmem_ld32(tl + C_X + 32 * j, v);
+                if (p.trans) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(x1 + row * D + 32 * j + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x1[(32 * j + i) * D + row] = v[i];
+                }
+            }
+        }
+    } else if (w == 12) {
+        // ---- loads ----
+        if (lane == 0) {
+            const CUtensorMap *mq = &tm.m[p.query], *mk = &tm.m[p.key], *mv = &tm.m[p.value];
+            int done = 0;
+            for (int c = 0; c < nc; ++c) {
+                const int s = c & 1, t = g.t0 + LC * place(c);
+                if (c >= 2 && !wait1(B_EMPTY + s, (c >> 1) - 1)) break;
+                tc::mbar_expect_tx(&bar[B_QK + s], 2 * TILE);
+                tc::tma4(tile(c, 1), mk, 0, t, 0, hd / p.rk, &bar[B_QK + s]);
+                tc::tma4(tile(c, 0), mq, 0, t, 0, hd / p.rq, &bar[B_QK + s]);
+                tc::mbar_expect_tx(&bar[B_V + s], TILE);
+                tc::tma4(tile(c, 2), mv, 0, t, 0, hd / p.rv, &bar[B_V + s]);
+                done = c + 1;
+            }
+            for (int c = max(done - 2, 0); c < done; ++c) {  // every copy has landed before the block ends
+                tc::mbar_wait(&bar[B_QK + (c & 1)], (c >> 1) & 1);
+                tc::mbar_wait(&bar[B_V + (c & 1)], (c >> 1) & 1);
+            }
+        }
+    } else if (lane == 0) {
+        // ---- products ----
+        const uint32_t ID = tc::idesc_bf16(128, 128, false, false), IDt = tc::idesc_bf16(128, 128, false, true);
+        const uint64_t dX = tc::sdesc(smem_u32(sm + W_X), 16, 1024);
+        auto kstep = [](int s) { return uint64_t(((s >> 2) * int(TILE / 2) + (s & 3) * 32) >> 4); };  // along the channels
+        auto tstep = [](int s) { return uint64_t((s * 2048) >> 4); };                                 // along the tokens
+        auto scores = [&](int c) {
+            if (!wait1(B_QK + (c & 1), c >> 1)) return false;
+            if (tokens(c) < LC && !wait1(B_FIX, 0)) return false;
+            const uint64_t dq = tc::sdesc(smem_u32(tile(c, 0)), 16, 1024), dk = tc::sdesc(smem_u32(tile(c, 1)), 16, 1024);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) tc::mma(tbase + C_P, dq + kstep(s), dk + kstep(s), ID, s > 0);
+            tc::mma_commit(&bar[B_P]);
+            return true;
+        };
+        if (scores(0)) {
+            for (int c = 0; c < nc; ++c) {
+                if (!wait1(B_C, c) || (c > 0 && !wait1(B_OFREE, c - 1))) break;
+                const uint64_t dq = tc::sdesc(smem_u32(tile(c, 0)), 16, 1024);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) tc::mma(tbase + C_O, dq + kstep(s), dX + kstep(s), ID, s > 0);
+                tc::mma_commit(&bar[B_QX]);
+                if (adds(c)) {
+                    if (!wait1(B_A, c)) break;
+                    const uint64_t dk = tc::sdesc(smem_u32(tile(c, 1)), TILE / 2, 1024);
+#pragma unroll
+                    for (int pl = 0; pl < 3; ++pl) {
+                        const uint32_t ap = tbase + (pl == 0 ? C_LO : pl == 1 ? C_MID : C_HI);
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) mma_ta(tbase + C_X, ap + 8 * s, dk + tstep(s), IDt, 1u);
+                    }
+                    tc::mma_commit(&bar[B_S]);
+                }
+                if (!wait1(B_B, c)) break;
+                const uint64_t dv = tc::sdesc(smem_u32(tile(c, 2)), TILE / 2, 1024);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) mma_ta(tbase + C_O, tbase + C_P + 8 * s, dv + tstep(s), IDt, 1u);
+                tc::mma_commit(&bar[B_O]);
+                tc::mma_commit(&bar[B_EMPTY + (c & 1)]);
+                if (c + 1 < nc && !scores(c + 1)) break;
+            }
+        }
+        if (!ok) tc::drain_mmas(&bar[B_SPARE], 100000000ull);
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) *a.status = KDA_ERR_TIMEOUT;
+    if (w == 0) tc::tmem_dealloc(tbase, 512);
+}
+
+// ---- what a segment adds to the state ----
+
+constexpr int STATE_THREADS = 320;  // two groups of four warps take the chunks in turn; loads: warp 8, products: 9
+constexpr int S_STAGES = 3;
+constexpr int S_TAB = S_STAGES * 2 * int(TILE);
+constexpr int S_BAR = S_TAB + 128 * 4;
+constexpr size_t STATE_SMEM = S_BAR + 128 + 1024;
+enum StateBar { SB_FULL = 0, SB_EMPTY = S_STAGES, SB_READY = 2 * S_STAGES, SB_FREE = SB_READY + 2, SB_DONE = SB_FREE + 2, SB_FIX, SB_SPARE, SB_END };
+
+// No decay of the state between chunks: a token's factor reaches to the segment's end, the products add up.
+__global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int ps, const __grid_constant__ LinMaps tm) {
+    extern __shared__ unsigned char smraw[];
+    unsigned char* sm = tc::align1024(smraw);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int hd = int(blockIdx.x % unsigned(a.H));
+    const LinPass& p = a.pass[ps];
+    Seg g;
+    if (!lin_segment(a, int(blockIdx.x / unsigned(a.H)), g)) return;
+    const bool back = p.back;
+    if (back ? g.first : g.last) return;  // nothing walks on from here
+    float* out = back ? a.back + (size_t(g.w - 1) * a.H + hd) * D * D : a.front + (size_t(g.w) * a.H + hd) * D * D;
+    const int nc = (g.len + LC - 1) / LC;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S_BAR);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S_BAR + 8 * SB_END);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S_BAR + 8 * SB_END + 4);
+    float* fs = reinterpret_cast<float*>(sm + S_TAB);
+    const float slope = a.slope[hd];
+    if (tid == 0) {
+        for (int i = 0; i < SB_SPARE; ++i)
+            tc::mbar_init(&bar[i], i == SB_READY || i == SB_READY + 1 || i == SB_FIX ? 4 : 1);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (w == 0) tc::tmem_alloc(tslot, 512);
+    if (tid < LC) fs[tid] = p.in * decay(slope, back ? tid + 1 : LC - 1 - tid);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = *tslot;
+    const uint32_t tl = tbase + (uint32_t(32 * (w & 3)) << 16);
+    const int row = 32 * (w & 3) + lane;
+    auto tile = [&](int c, int which) { return sm + ((c % S_STAGES) * 2 + which) * TILE; };
+    bool ok = true;  // waits as in the walk
+    auto wait1 = [&](int b, int turn) {
+        if (ok && !tc::mbar_wait(&bar[b], uint32_t(turn) & 1u)) {
+            ok = false;
+            *abort_flag = 1;
+        }
+        tc::fence_after_sync();
+        return ok;
+    };
+    auto wait = [&](int b, int turn) { return ok = __all_sync(0xffffffffu, wait1(b, turn)); };
+    constexpr uint32_t C_V = 128;  // columns: state 0, then two sets of three planes
+
+    if (w < 8) {
+        const int grp = w >> 2;
+        for (int c = grp; c < nc; c += 2) {
+            const int n = min(LC, g.len - LC * c);
+            if (!wait(SB_FULL + c % S_STAGES, c / S_STAGES)) break;
+            if (n < LC) {
+                clear_rows(tile(c, 0), n, tid & 127);
+                clear_rows(tile(c, 1), n, tid & 127);
+                tc::fence_async_smem();
+                warp_arrive(&bar[SB_FIX], lane);
+                if (!wait(SB_FIX, 0)) break;
+            }
+            if (c >= 2 && !wait(SB_FREE + grp, (c >> 1) - 1)) break;
+            const uint32_t v = tl + C_V + 192 * grp;
+            // forwards only full chunks come here (the last segment adds to nothing)
+            split_values(tile(c, 1), row, fs, decay(slope, back ? LC * c : g.len - LC * (c + 1)), v, v + 64, v + 128);
+            warp_arrive(&bar[SB_READY + grp], lane);
+        }
+        if (w < 4 && wait(SB_DONE, 0)) {
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                float x[32];
+                tc::tmem_ld32(tl + 32 * j, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) out[(32 * j + i) * D + row] = x[i];
+            }
+        }
+    } else if (w == 8) {
+        if (lane == 0) {
+            const CUtensorMap *mk = &tm.m[p.key], *mv = &tm.m[p.value];
+            int done = 0;
+            for (int c = 0; c < nc; ++c) {
+                const int s = c % S_STAGES, t = g.t0 + LC * c;
+                if (c >= S_STAGES && !wait1(SB_EMPTY + s, c / S_STAGES - 1)) break;
+                tc::mbar_expect_tx(&bar[SB_FULL + s], 2 * TILE);
+                tc::tma4(tile(c, 0), mk, 0, t, 0, hd / p.rk, &bar[SB_FULL + s]);
+                tc::tma4(tile(c, 1), mv, 0, t, 0, hd / p.rv, &bar[SB_FULL + s]);
+                done = c + 1;
+            }
+            for (int c = max(done - S_STAGES, 0); c < done; ++c) tc::mbar_wait(&bar[SB_FULL + c % S_STAGES], (c / S_STAGES) & 1);
+        }
+    } else if (lane == 0) {
+        const uint32_t IDt = tc::idesc_bf16(128, 128, false, true);
+        for (int c = 0; c < nc; ++c) {
+            if (!wait1(SB_READY + (c & 1), c >> 1)) break;
+            const uint64_t dk = tc::sdesc(smem_u32(tile(c, 0)), TILE / 2, 1024);
+#pragma unroll
+            for (int pl = 2; pl >= 0; --pl)
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_ta(tbase, tbase + C_V + 192 * (c & 1) + 64 * pl + 8 * s, dk + uint64_t((s * 2048) >> 4), IDt,
+                           c > 0 || pl < 2 || s > 0);
+            tc::mma_commit(&bar[SB_FREE + (c & 1)]);
+            tc::mma_commit(&bar[SB_EMPTY + c % S_STAGES]);
+        }
+        tc::mma_commit(&bar[SB_DONE]);
+        if (!ok) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) *a.status = KDA_ERR_TIMEOUT;
+    if (w == 0) tc::tmem_dealloc(tbase, 512);
 }
 
 }  // namespace
 
-void launch_lin_walk(const LinArgs& a, cudaStream_t st) {
+cudaError_t lin_setup() {
+    cudaError_t e = cudaFuncSetAttribute(k_lin_walk, cudaFuncAttributeMaxDynamicSharedMemorySize, int(WALK_SMEM));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(k_lin_state, cudaFuncAttributeMaxDynamicSharedMemorySize, int(STATE_SMEM));
+}
+
+// segments that the call may have
+static unsigned lin_segments(const LinArgs& a) { return unsigned(a.direct ? a.N : a.T / a.seg + a.N); }
+
+void launch_lin_states(const LinArgs& a, const LinMaps& tm, int pass, cudaStream_t st) {
+    {
+        ProfScope ps(KK_LIN_STATE, st);
+        k_lin_state<<<lin_segments(a) * unsigned(a.H), STATE_THREADS, STATE_SMEM, st>>>(a, pass, tm);
+    }
+    launch_lin_carry(a, pass, st);
+}
+
+void launch_lin_walk(const LinArgs& a, const LinMaps& tm, cudaStream_t st) {
     ProfScope ps(KK_LIN_WALK, st);
-    k_lin_recur<<<unsigned(a.N) * unsigned(a.H) * unsigned(a.passes), 128, 0, st>>>(a);
+    k_lin_walk<<<lin_segments(a) * unsigned(a.H) * unsigned(a.passes), WALK_THREADS, WALK_SMEM, st>>>(a, tm);
 }
 
 }  // namespace kda

@@ -17,8 +17,7 @@ namespace kda {
 //   backwards:  X_t = Y_t + in key_t value_t^T,  Y_{t-1} = lambda X_t (Y at the last token: s0, past the first: s_end)
 // and out_t = by X_t^T query_t.
 struct LinPass {
-    const __nv_bfloat16 *query, *key, *value;
-    int64_t ldq, ldk, ldv;  // token strides (elements)
+    int query, key, value;  // tensors of LinMaps
     int rq, rk, rv;         // heads that share a row of each
     void* out;              // dense [T, H, 128]
     int out_fp32;
@@ -29,17 +28,39 @@ struct LinPass {
     float in, by;
 };
 
+constexpr int LC = 128;  // tokens of a chunk
+constexpr int LIN_MAXSEG = 4096;
+
+// Documents are cut into segments of `seg` tokens (the last one shorter; an empty document has one empty
+// segment), which are walked side by side.  The state between two segments of a document lies in a slot.
+struct LinPlan {
+    int4* tab;     // per segment: {document, first token, length | first << 16 | last << 17, w}: w is the slot behind
+                   // the segment, w - 1 the one in front of it
+    int4* multi;   // per document of more than one segment: {document, slot behind its first segment, segments, tokens}
+    int* counts;   // segments, documents in multi
+};
+
 struct LinArgs {
     int64_t T;
     int N, H;
+    int seg;               // tokens of a segment
+    int direct;            // no document is longer than a segment: segment n is document n, no plan
     const int* cu;
     const float* slope;
     int* status;
     int4 sizes;            // of this call
     int4* made_for;        // forward with a saved set: where it notes them
     const int4* expected;  // backward from a saved set: what its forward noted
+    LinPlan plan;
+    float *front, *back;   // slots [][H][128][128] of the forward and of the backward walks
     int passes;
     LinPass pass[3];
+};
+
+// The rows of a call as TMA tensors: {64 channels, tokens, half of the head, head}, boxes of 128 tokens x one head,
+// which land as two 128-byte-swizzled tiles [64 channels of 128 tokens].  LinPass names them by index.
+struct LinMaps {
+    CUtensorMap m[4];
 };
 
 // single tokens (kda_lin_step.cu)
@@ -56,6 +77,10 @@ struct LinStepArgs {
 };
 void launch_lin_step(const LinStepArgs& a, cudaStream_t st);
 
-void launch_lin_walk(const LinArgs& a, cudaStream_t st);
+cudaError_t lin_setup();  // shared memory limits
+void launch_lin_plan(const LinArgs& a, cudaStream_t st);
+// the slots' states: what each segment adds (pass of a.pass whose walk they stand for), then their sums
+void launch_lin_states(const LinArgs& a, const LinMaps& tm, int pass, cudaStream_t st);
+void launch_lin_walk(const LinArgs& a, const LinMaps& tm, cudaStream_t st);
 
 }  // namespace kda

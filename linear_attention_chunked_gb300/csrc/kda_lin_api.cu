@@ -1,4 +1,6 @@
 // Host side of the linear attention's entry points: validation, workspace, launches.
+#include <mutex>
+
 #include "kda_lin.cuh"
 
 using namespace kda;
@@ -10,20 +12,49 @@ bool req(const void* p) { return p && al(p, 16); }
 bool opt(const void* p) { return al(p, 16); }
 int64_t ld_or(int64_t ld, int64_t dense) { return ld ? ld : dense; }
 
-// Once per device and process: that it is an sm_103 part.
+std::mutex g_mu;
+bool g_ready[128];
+
+// Once per device: that it is an sm_103 part, and the walks' shared memory limits.
 kda_status setup_lin() {
-    static unsigned long long ready[2];
     int dev = 0, major = 0, minor = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
     if (dev < 0 || dev >= 128) return KDA_ERR_UNSUPPORTED;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (__atomic_load_n(&ready[dev >> 6], __ATOMIC_ACQUIRE) & bit) return KDA_OK;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (g_ready[dev]) return KDA_OK;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (major != 10 || minor != 3) return KDA_ERR_UNSUPPORTED;
-    __atomic_fetch_or(&ready[dev >> 6], bit, __ATOMIC_RELEASE);
+    if (lin_setup() != cudaSuccess) return KDA_ERR_CUDA;
+    g_ready[dev] = true;
     return KDA_OK;
+}
+
+// cuTensorMapEncodeTiled, looked up once through the runtime (no link-time libcuda dependency).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    return fn;
+}
+
+// Tokens of a segment, a power of two that depends on the heads alone: a document's results must not depend on the
+// pack, and a document alone has to fill the machine.  16384 tokens cut so give 512 blocks at 16 and at 64 heads;
+// the states between segments cost a second pass over two of the rows (50% more reads of a forward).
+int segment(int H) {
+    int s = 512;
+    while (s < 32 * H && s < LIN_MAXSEG) s *= 2;
+    return s;
 }
 
 kda_status check_sizes(const kda_linattn_problem* p) {
@@ -43,67 +74,89 @@ kda_status check_problem(const kda_linattn_problem* p) {
     if (kda_status s = check_sizes(p)) return s;
     if (!p->cu_seqlens || !al(p->cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
     // one-dimensional grids
-    if (int64_t(p->N) * p->H > INT32_MAX / 3 || p->T * p->Hk / 8 >= INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    const int64_t segs = p->T / segment(p->H) + p->N;
+    if (segs * p->H > INT32_MAX / 16 || p->T * p->Hk / 8 >= INT32_MAX) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
 struct Regions {
-    size_t status, share_q, share_k;  // inside the workspace
-    size_t fwd, bwd;
-    size_t saved;
+    size_t status, tab, multi, counts, front, back, share_q, share_k;  // inside the workspace
+    size_t fwd, bwd_saved, bwd_replay;
+    size_t kept, saved;  // inside the saved set: the slots behind its header
 };
 
 Regions regions(const kda_linattn_problem* p) {
     Regions r{};
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
+    const size_t seg = size_t(segment(p->H)), multi = size_t(p->T) / seg;
+    const size_t slots = multi * size_t(p->H) * D * D * 4;
     r.status = take(256);
+    r.counts = take(2 * sizeof(int));
+    r.tab = take((multi + size_t(p->N)) * sizeof(int4));
+    r.multi = take(multi * sizeof(int4));
+    const size_t plan = o;
+    r.front = take(slots);
     r.fwd = o;
+    o = plan;
+    r.back = take(slots);
     if (p->Hk < p->H) {  // each head's part of dq and dk
         r.share_q = take(size_t(p->T) * p->H * D * 4);
         r.share_k = take(size_t(p->T) * p->H * D * 4);
     }
-    r.bwd = o;
-    r.saved = 256;
+    r.bwd_saved = o;
+    r.bwd_replay = o + slots;
+    r.kept = 256;
+    r.saved = 256 + slots;
     return r;
 }
 
-LinArgs make_args(const kda_linattn_problem* p, const float* slope, void* ws) {
+LinArgs make_args(const kda_linattn_problem* p, const Regions& r, const float* slope, void* ws) {
     LinArgs a{};
+    char* w = static_cast<char*>(ws);
     a.T = p->T;
     a.N = p->N;
     a.H = p->H;
+    a.seg = segment(p->H);
+    a.direct = p->T <= a.seg;
     a.cu = p->cu_seqlens;
     a.slope = slope;
     a.status = static_cast<int*>(ws);
     a.sizes = make_int4(int(p->T), p->N, p->H, p->Hk);
+    a.plan = {reinterpret_cast<int4*>(w + r.tab), reinterpret_cast<int4*>(w + r.multi), reinterpret_cast<int*>(w + r.counts)};
     return a;
 }
 
 using bf = __nv_bfloat16;
 
-// q, k, v and dO as a walk's rows
-struct Rows {
-    const bf* p;
-    int64_t ld;
-    int share;
-};
-struct Inputs {
-    Rows q, k, v, dO;
-    Inputs(const kda_linattn_problem* p, const void* q_, const void* k_, const void* v_, const void* dO_) {
-        const int64_t dk = int64_t(p->Hk) * D, dv = int64_t(p->H) * D;
-        const int share = p->H / p->Hk;
-        q = {static_cast<const bf*>(q_), ld_or(p->ld_q, dk), share};
-        k = {static_cast<const bf*>(k_), ld_or(p->ld_k, dk), share};
-        v = {static_cast<const bf*>(v_), ld_or(p->ld_v, dv), 1};
-        dO = {static_cast<const bf*>(dO_), dv, 1};
-    }
-};
+// The rows of a call, in the order of LinMaps
+enum { IN_Q, IN_K, IN_V, IN_DO };
 
-LinPass make_pass(const Rows& query, const Rows& key, const Rows& value, void* out, int out_fp32, const float* s0,
-                  float* s_end, int trans, int back, float in, float by) {
-    return {query.p, key.p, value.p, query.ld, key.ld, value.ld, query.share, key.share, value.share,
-            out, out_fp32, s0, s_end, trans, back, in, by};
+// share: heads that share a row of q and k
+LinPass make_pass(int query, int key, int value, int share, void* out, int out_fp32, const float* s0, float* s_end,
+                  int trans, int back, float in, float by) {
+    auto per = [&](int t) { return t == IN_Q || t == IN_K ? share : 1; };
+    return {query, key, value, per(query), per(key), per(value), out, out_fp32, s0, s_end, trans, back, in, by};
+}
+
+kda_status make_maps(const kda_linattn_problem* p, const void* q, const void* k, const void* v, const void* dO, LinMaps* tm) {
+    if (p->T == 0) return KDA_OK;  // no row is read
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return KDA_ERR_CUDA;
+    const void* ptr[4] = {q, k, v, dO};
+    const int64_t dk = int64_t(p->Hk) * D, dv = int64_t(p->H) * D;
+    const int64_t ld[4] = {ld_or(p->ld_q, dk), ld_or(p->ld_k, dk), ld_or(p->ld_v, dv), dv};
+    for (int i = 0; i < 4; ++i) {
+        if (!ptr[i]) continue;
+        const cuuint64_t dims[4] = {64, cuuint64_t(p->T), 2, cuuint64_t(i < 2 ? p->Hk : p->H)};
+        const cuuint64_t strides[3] = {cuuint64_t(ld[i]) * 2, 128, D * 2};
+        const cuuint32_t box[4] = {64, LC, 2, 1}, one[4] = {1, 1, 1, 1};
+        if (enc(&tm->m[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr[i]), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
 }
 
 // dq and dk of a shared head: the sum of its heads' parts, in head order, rounded once.
@@ -133,8 +186,8 @@ kda_status kda_linattn_workspace_size(const kda_linattn_problem* p, int op, size
     const Regions r = regions(p);
     size_t w = 0;
     if (op == KDA_OP_FWD) w = r.fwd;
-    else if (op == KDA_OP_BWD_SAVED) w = r.bwd;
-    else if (op == KDA_OP_BWD_REPLAY) w = r.bwd;
+    else if (op == KDA_OP_BWD_SAVED) w = r.bwd_saved;
+    else if (op == KDA_OP_BWD_REPLAY) w = r.bwd_replay;
     else return KDA_ERR_INVALID_ARG;
     if (ws_bytes) *ws_bytes = w;
     if (saved_bytes) *saved_bytes = r.saved;
@@ -151,13 +204,20 @@ kda_status kda_linattn_fwd(const kda_linattn_problem* p, const void* q, const vo
     if (ws_bytes < r.fwd) return KDA_ERR_WORKSPACE;
     if (kda_status s = setup_lin()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    LinArgs a = make_args(p, slope, ws);
-    const Inputs in(p, q, k, v, nullptr);
-    if (!clear_status(ws, st)) return KDA_ERR_CUDA;
+    LinArgs a = make_args(p, r, slope, ws);
+    LinMaps tm{};
+    if (kda_status s = make_maps(p, q, k, v, nullptr, &tm)) return s;
     a.made_for = static_cast<int4*>(saved);
+    a.front = reinterpret_cast<float*>(saved ? static_cast<char*>(saved) + r.kept : static_cast<char*>(ws) + r.front);
     a.passes = 1;
-    a.pass[0] = make_pass(in.q, in.k, in.v, o, 0, h0, ht, 0, 0, 1.f, p->scale);
-    launch_lin_walk(a, st);
+    a.pass[0] = make_pass(IN_Q, IN_K, IN_V, p->H / p->Hk, o, 0, h0, ht, 0, 0, 1.f, p->scale);
+    if (a.direct) {
+        if (!clear_status(ws, st)) return KDA_ERR_CUDA;
+    } else {
+        launch_lin_plan(a, st);
+        launch_lin_states(a, tm, 0, st);
+    }
+    launch_lin_walk(a, tm, st);
     return launched();
 }
 
@@ -170,26 +230,40 @@ kda_status kda_linattn_bwd(const kda_linattn_problem* p, const void* q, const vo
         return KDA_ERR_INVALID_ARG;
     if (!req(slope) || !opt(h0) || !opt(dht) || !opt(saved) || !opt(dh0) || !req(ws)) return KDA_ERR_INVALID_ARG;
     const Regions r = regions(p);
-    if (ws_bytes < r.bwd) return KDA_ERR_WORKSPACE;
+    if (ws_bytes < (saved ? r.bwd_saved : r.bwd_replay)) return KDA_ERR_WORKSPACE;
     if (kda_status s = setup_lin()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    LinArgs a = make_args(p, slope, ws);
-    const Inputs in(p, q, k, v, dO);
-    const int part = p->Hk < p->H;
-    float* pq = reinterpret_cast<float*>(static_cast<char*>(ws) + r.share_q);
-    float* pk = reinterpret_cast<float*>(static_cast<char*>(ws) + r.share_k);
-    if (!clear_status(ws, st)) return KDA_ERR_CUDA;
+    LinArgs a = make_args(p, r, slope, ws);
+    LinMaps tm{};
+    if (kda_status s = make_maps(p, q, k, v, dO, &tm)) return s;
+    char* w = static_cast<char*>(ws);
+    const int share = p->H / p->Hk, part = share > 1;
+    float* pq = reinterpret_cast<float*>(w + r.share_q);
+    float* pk = reinterpret_cast<float*>(w + r.share_k);
     a.expected = static_cast<const int4*>(saved);
+    a.front = reinterpret_cast<float*>(saved ? const_cast<char*>(static_cast<const char*>(saved)) + r.kept : w + r.bwd_saved);
+    a.back = reinterpret_cast<float*>(w + r.back);
+    if (a.direct) {
+        if (!clear_status(ws, st)) return KDA_ERR_CUDA;
+    } else {
+        launch_lin_plan(a, st);
+        if (!saved) {  // the states between segments, as the forward's
+            a.pass[0] = make_pass(IN_Q, IN_K, IN_V, share, nullptr, 0, h0, nullptr, 0, 0, 1.f, p->scale);
+            launch_lin_states(a, tm, 0, st);
+        }
+        a.pass[0] = make_pass(IN_K, IN_Q, IN_DO, share, nullptr, 0, dht, nullptr, 0, 1, p->scale, 1.f);
+        launch_lin_states(a, tm, 0, st);
+    }
     a.passes = 3;
-    a.pass[0] = make_pass(in.dO, in.v, in.k, part ? static_cast<void*>(pq) : dq, part, h0, nullptr, 1, 0, 1.f, p->scale);
-    a.pass[1] = make_pass(in.k, in.q, in.dO, dv, 0, dht, dh0, 0, 1, p->scale, 1.f);
-    a.pass[2] = make_pass(in.v, in.dO, in.q, part ? static_cast<void*>(pk) : dk, part, dht, nullptr, 1, 1, p->scale, 1.f);
-    launch_lin_walk(a, st);
+    a.pass[0] = make_pass(IN_DO, IN_V, IN_K, share, part ? static_cast<void*>(pq) : dq, part, h0, nullptr, 1, 0, 1.f, p->scale);
+    a.pass[1] = make_pass(IN_K, IN_Q, IN_DO, share, dv, 0, dht, dh0, 0, 1, p->scale, 1.f);
+    a.pass[2] = make_pass(IN_V, IN_DO, IN_Q, share, part ? static_cast<void*>(pk) : dk, part, dht, nullptr, 1, 1, p->scale, 1.f);
+    launch_lin_walk(a, tm, st);
     if (part && p->T > 0) {
         const int64_t rows = p->T * p->Hk;
         ProfScope ps(KK_LIN_SHARE, st);
         k_lin_share<<<dim3(unsigned((rows * D / 4 + 255) / 256), 2), 256, 0, st>>>(
-            pq, pk, static_cast<bf*>(dq), static_cast<bf*>(dk), rows, p->H / p->Hk, a.status);
+            pq, pk, static_cast<bf*>(dq), static_cast<bf*>(dk), rows, share, a.status);
     }
     return launched();
 }
@@ -205,9 +279,10 @@ kda_status kda_linattn_step(const kda_linattn_problem* p, const void* q, const v
     if (!req(q) || !req(k) || !req(v) || !req(slope) || !req(h_in) || !req(h_out) || !req(o) || !al(slots, 4) ||
         !opt(ws) || n_slots < 1 || (!slots && n_slots < pr.N))
         return KDA_ERR_INVALID_ARG;
-    const Inputs in(&pr, q, k, v, nullptr);
-    const LinStepArgs a{pr.N, pr.H, pr.H / pr.Hk, in.q.ld, in.k.ld, in.v.ld, n_slots, pr.scale, in.q.p, in.k.p,
-                        in.v.p, slope, h_in, slots, h_out, static_cast<bf*>(o), static_cast<int*>(ws)};
+    const int64_t dk = int64_t(pr.Hk) * D, dv = int64_t(pr.H) * D;
+    const LinStepArgs a{pr.N, pr.H, pr.H / pr.Hk, ld_or(pr.ld_q, dk), ld_or(pr.ld_k, dk), ld_or(pr.ld_v, dv), n_slots,
+                        pr.scale, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v), slope,
+                        h_in, slots, h_out, static_cast<bf*>(o), static_cast<int*>(ws)};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!clear_status(ws, st)) return KDA_ERR_CUDA;
     launch_lin_step(a, st);
