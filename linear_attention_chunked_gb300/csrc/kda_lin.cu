@@ -18,8 +18,9 @@
 //     QX     A = Query,                   B = X^T in shared memory, bf16 [values][keys]
 //     P'V    A = P' (tensor memory),      B = Value [tokens][values] read across
 //     state  A = values^T (tensor memory), B = Key read across
-// Four groups of warps work at once: A scales and splits the values, B masks and rounds the scores and scales Query X's
-// rows, C rounds and decays the state and stores the output, and two single threads issue loads and products.
+// Three groups of warps work at once: A scales and splits the values, B masks and rounds the scores and scales
+// Query X's rows, C rounds and decays the state and hands the output to TMA (through the chunk's spent value tile), and
+// two warps issue loads and products.
 // Rows behind a document's end (another's) are cleared in K and V, so nothing of them, were it not finite, is multiplied.
 #include "kda_lin.cuh"
 #include "kda_ssm.cuh"
@@ -45,6 +46,12 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// 16 lanes x 16 columns: lane i holds row i / 4 of column 4 j + i % 4 in word 2 j and row 8 + i / 4 in word 2 j + 1
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem], issued by one thread: A's row i is lane i, its 16-bit elements 2 c and 2 c + 1 lie in
@@ -56,7 +63,25 @@ __device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
         : "memory");
 }
+// True in one lane of a warp, always the same.  Products issued under it take their operands from uniform registers:
+// 76 clocks each (left operand in tensor memory; 108 in shared memory), where a branch on the thread's number costs 106.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void tma_store4(const CUtensorMap* map, int x, int y, int z, int u, const void* src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(src))
+                 : "memory");
+}
 
+// tc::mbar_wait with its polling out of line: a role's code has to stay in the instruction cache beside the others'
+__device__ __noinline__ bool poll(uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity); }
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity) {
+    return tc::mbar_try_wait(bar, parity) || poll(bar, parity);
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -75,45 +100,62 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int n, int tid) 
     }
 }
 
-// The chunk's values of channel `ch` times the tokens' factors, split into three bf16 planes, as the rows of a product's
-// left operand in tensor memory: lane `ch`, token pairs in columns hi, mid, lo (taddrs with the lane set).
-// f: the factors in shared memory, times `all`.
-__device__ __forceinline__ void split_values(const unsigned char* tile, int ch, const float* f, float all, uint32_t hi,
-                                             uint32_t mid, uint32_t lo) {
-    const unsigned char* base = tile + (ch >> 6) * (TILE / 2) + (ch & 7) * 2;
-    const int c8 = (ch & 63) >> 3;
-    int off[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) off[j] = j * 128 + ((c8 ^ j) << 4);
+// A quarter (32 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into three bf16
+// planes as the left operand of a product in tensor memory: lane = channel, token pairs in the columns taddr.. of
+// hi, mid and lo, 16 each.  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
+// the pairs that a 16-lane store takes.
+constexpr uint32_t PLANES = 48;  // columns of a quarter
+__device__ __forceinline__ void split_quarter(const unsigned char* tile, int quarter, int w, int lane, const float* f, float all,
+                                              uint32_t taddr) {
+    const int m = lane >> 3, r = lane & 7;
+    const unsigned char* base = tile + ((w & 3) >> 1) * (TILE / 2) + (32 * quarter + (m >> 1) * 8 + r) * 128;
+    const int c8 = (w & 1) * 4 + (m & 1);
     const f2 all2 = pk2(all, all);
-    const uint32_t mask = 0xffff0000u, flip = 0x80000000u;
-#pragma unroll 1
-    for (int t0 = 0; t0 < LC; t0 += 32) {
-        uint32_t h[16], m[16], l[16];
+    f2 fw[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int t = 2 * j;
-            const unsigned char* row = base + (t0 + (t & ~7)) * 128;
-            const float x0 = __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(row + off[t & 7])) << 16);
-            const float x1 = __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(row + off[(t & 7) + 1])) << 16);
-            const f2 y = mul2(mul2(*reinterpret_cast<const f2*>(f + t0 + t), all2), pk2(x0, x1));
+    for (int i = 0; i < 4; ++i)
+        fw[i] = mul2(*reinterpret_cast<const f2*>(f + 32 * quarter + 8 * i + 2 * (lane & 3)), all2);
+    constexpr uint32_t mask = 0xffff0000u, flip = 0x80000000u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 16 channels
+        uint32_t x[8], hi[8], mid[8], lo[8];
+        {
+            uint32_t t[4];
+            const unsigned char* at = base + (((c8 + 2 * h) ^ r) << 4);
+            ldsm4t(t, at);
+            x[0] = t[0], x[1] = t[1], x[2] = t[2], x[3] = t[3];
+            ldsm4t(t, at + 16 * 128);
+            x[4] = t[0], x[5] = t[1], x[6] = t[2], x[7] = t[3];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const f2 y = mul2(fw[j >> 1], pk2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & mask)));
             float y0, y1, r0, r1;
             up2(y, y0, y1);
-            h[j] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
-            const f2 r = add2(y, pk2(__uint_as_float((__float_as_uint(y0) & mask) ^ flip),
-                                     __uint_as_float((__float_as_uint(y1) & mask) ^ flip)));
-            up2(r, r0, r1);
-            m[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-            const f2 q = add2(r, pk2(__uint_as_float((__float_as_uint(r0) & mask) ^ flip),
-                                     __uint_as_float((__float_as_uint(r1) & mask) ^ flip)));
-            up2(q, r0, r1);
-            l[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            hi[j] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
+            const f2 rest = add2(y, pk2(__uint_as_float((__float_as_uint(y0) & mask) ^ flip),
+                                        __uint_as_float((__float_as_uint(y1) & mask) ^ flip)));
+            up2(rest, r0, r1);
+            mid[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            const f2 last = add2(rest, pk2(__uint_as_float((__float_as_uint(r0) & mask) ^ flip),
+                                           __uint_as_float((__float_as_uint(r1) & mask) ^ flip)));
+            up2(last, r0, r1);
+            lo[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
         }
-        tmem_st16u(hi + t0 / 2, h);
-        tmem_st16u(mid + t0 / 2, m);
-        tmem_st16u(lo + t0 / 2, l);
+        const uint32_t at = taddr + (uint32_t(16 * h) << 16);
+        tmem_st_16x16(at, hi);
+        tmem_st_16x16(at + 16, mid);
+        tmem_st_16x16(at + 32, lo);
     }
     tmem_wait_st();
+}
+// The products of a quarter: D += planes * rows 32 quarter.. of the key tile, read across
+__device__ __forceinline__ void quarter_products(uint32_t d, uint32_t planes, uint64_t key, int quarter, uint32_t idesc, bool first) {
+#pragma unroll
+    for (int pl = 2; pl >= 0; --pl)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            mma_ta(d, planes + 16 * pl + 8 * s, key + uint64_t(((2 * quarter + s) * 2048) >> 4), idesc, !first || pl < 2 || s > 0);
 }
 
 // The segment of a block: {document, first token, length, flags as in LinPlan, w}; false: none (or malformed offsets)
@@ -146,23 +188,26 @@ __device__ __forceinline__ bool lin_segment(const LinArgs& a, int i, Seg& s) {
 
 // ---- the walk ----
 
-constexpr int WALK_THREADS = 448;  // A: warps 0-3, B: 4-7, C: 8-11, loads: 12, products: 13
-constexpr int W_STAGE = 0;         // [2 stages][Query, Key, Value]
-constexpr int W_X = 6 * int(TILE);
-constexpr int W_TAB = W_X + int(TILE);   // decays [132], state factors of a full and of the short chunk [128], block factors [32]
-constexpr int W_BAR = W_TAB + (132 + 2 * 128 + 32) * 4;
-constexpr size_t WALK_SMEM = W_BAR + 192 + 1024;
+constexpr int WALK_THREADS = 448;  // A: warps 0-3, B: 4-7, C: 8-11, loads and stores: 12, products: 13
+constexpr int W_X = 6 * int(TILE);       // behind [2 stages][Query, Key, Value]
+constexpr int W_TAB = W_X + int(TILE);   // state factors of a full and of the short chunk, decays: [128] each
+constexpr int W_BAR = W_TAB + 3 * 128 * 4;
+constexpr size_t WALK_SMEM = W_BAR + 256 + 1024;
 static_assert(WALK_SMEM <= 232448, "walk: shared memory above the opt-in limit");
 
-// tensor memory columns
-constexpr uint32_t C_P = 0, C_LO = 64, C_O = 128, C_X = 256, C_HI = 384, C_MID = 448;
+// tensor memory columns: scores (their rounded form in the first half), output, state, two quarters of split values
+constexpr uint32_t C_P = 0, C_O = 128, C_X = 256, C_V = 384;
 
-enum WalkBar { B_QK = 0, B_V = 2, B_EMPTY = 4, B_P = 6, B_PREAD, B_QX, B_B, B_A, B_S, B_C, B_O, B_OFREE, B_FIX, B_SPARE, B_END };
+// Two of a kind: by stage (chunk & 1), or by quarter.  Loads have landed; a tile may be loaded again; ...
+enum WalkBar {
+    B_QK = 0, B_V = 2, B_QFREE = 4, B_KFREE = 6, B_STAGED = 8, B_A = 10, B_AFREE = 12,
+    B_P = 14, B_QX, B_B, B_S, B_C, B_O, B_OFREE, B_FIX, B_X0, B_SPARE, B_END
+};
 
 __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const __grid_constant__ LinMaps tm) {
     extern __shared__ unsigned char smraw[];
     unsigned char* sm = tc::align1024(smraw);
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int ps = int(blockIdx.x % unsigned(a.passes)), rest = int(blockIdx.x / unsigned(a.passes));
     const int hd = rest % a.H;
     const LinPass& p = a.pass[ps];
@@ -185,25 +230,26 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + W_BAR);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + W_BAR + 8 * B_END);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + W_BAR + 8 * B_END + 4);
-    float* pw = reinterpret_cast<float*>(sm + W_TAB);  // lambda^i, i <= 128
-    float* fs = pw + 132;                              // a full chunk's state factors
+    float* fs = reinterpret_cast<float*>(sm + W_TAB);  // a full chunk's state factors
     float* fshort = fs + 128;                          // the short chunk's (of at most one)
-    float* fb = fshort + 128;                          // factors within 32 columns of the scores
+    float* pw = fshort + 128;                          // lambda^i
     const float slope = a.slope[hd];
     if (tid == 0) {
-        for (int i = 0; i < B_SPARE; ++i)
-            tc::mbar_init(&bar[i], i == B_PREAD || i == B_B || i == B_A || i == B_C || i == B_OFREE || i == B_FIX ? 4 : 1);
+        for (int i = 0; i < B_SPARE; ++i) {
+            const bool four = (i >= B_STAGED && i < B_AFREE) || i == B_B || i == B_C || i == B_OFREE || i == B_FIX;
+            tc::mbar_init(&bar[i], i < B_V ? 2 : i == B_X0 ? 8 : four ? 4 : 1);
+        }
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
     if (w == 0) tc::tmem_alloc(tslot, 512);
-    for (int i = tid; i <= LC; i += WALK_THREADS) pw[i] = decay(slope, i);
+    if (w == 12 && lane < 3) tc::tma_prefetch_map(&tm.m[lane == 0 ? p.query : lane == 1 ? p.key : p.value]);
     if (tid < LC) {
         fs[tid] = p.in * decay(slope, back ? tid + 1 : LC - 1 - tid);
         const int m = g.len - LC * (nc - 1);
         fshort[tid] = tid < m ? p.in * decay(slope, back ? tid + 1 : m - 1 - tid) : 0.f;
+        pw[tid] = decay(slope, tid);
     }
-    if (tid < 32) fb[tid] = p.in * p.by * decay(slope, back ? tid : 31 - tid);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -214,24 +260,47 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     // chunk c of the walk: its place in the segment and its tokens
     auto place = [&](int c) { return back ? nc - 1 - c : c; };
     auto tokens = [&](int c) { return min(LC, g.len - LC * place(c)); };
-    auto tile = [&](int c, int which) { return sm + W_STAGE + ((c & 1) * 3 + which) * TILE; };
-    // whether chunk c's values still reach a state that is read
+    auto tile = [&](int c, int which) { return sm + ((c & 1) * 3 + which) * TILE; };
+    // whether chunk c's values still reach a state that is read; whether its output leaves by TMA
     auto adds = [&](int c) { return c + 1 < nc || x1; };
+    auto staged = [&](int c) { return !p.out_fp32 && tokens(c) == LC; };
     // Waits for the turn-th completion of barrier b.  The lanes of a warp leave together (a wait that runs out of
     // time ends the warp's part; every other wait runs out too, and the block reports and ends).
     bool ok = true;
-    auto wait1 = [&](int b, int turn) {
-        if (ok && !tc::mbar_wait(&bar[b], uint32_t(turn) & 1u)) {
-            ok = false;
-            *abort_flag = 1;
-        }
+    auto wait = [&](int b, int turn) {
+        const bool done = ok && bounded_wait(&bar[b], uint32_t(turn) & 1u);
+        ok = __all_sync(0xffffffffu, done);
+        if (!ok) *abort_flag = 1;
         tc::fence_after_sync();
         return ok;
     };
-    auto wait = [&](int b, int turn) { return ok = __all_sync(0xffffffffu, wait1(b, turn)); };
+    // 32 columns of the state that the walk starts from
+    auto start_block = [&](int j) {
+        float v[32];
+        if (!x0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        } else if (p.trans) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(x0 + row * D + 32 * j + i);
+                v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = x0[(32 * j + i) * D + row];
+        }
+        tc::tmem_st32(tl + C_X + 32 * j, v);
+    };
+    // the groups share the blocks: A takes the first, B the second, C the others
+    if (w < 12) {
+#pragma unroll 1
+        for (int j = w >> 2; j < ((w >> 2) == 2 ? 4 : (w >> 2) + 1); ++j) start_block(j);
+        if (w < 8) warp_arrive(&bar[B_X0], lane);
+    }
 
     if (w < 4) {
-        // ---- A: the values, scaled and split ----
+        // ---- A: the values, scaled and split, a quarter at a time ----
         for (int c = 0; c < nc; ++c) {
             const int n = tokens(c);
             if (!wait(B_V + (c & 1), c >> 1)) break;
@@ -244,59 +313,74 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 if (!wait(B_FIX, 0)) break;
             }
             if (!adds(c)) break;
-            if (c > 0 && !wait(B_S, c - 1)) break;
-            if (!wait(B_PREAD, c)) break;
-            split_values(tile(c, 2), row, n < LC ? fshort : fs, 1.f, tl + C_HI, tl + C_MID, tl + C_LO);
-            warp_arrive(&bar[B_A], lane);
+#pragma unroll 1
+            for (int q = 4 * c; q < 4 * c + 4; ++q) {
+                if (q >= 2 && !wait(B_AFREE + (q & 1), (q >> 1) - 1)) break;
+                split_quarter(tile(c, 2), q & 3, w, lane, n < LC ? fshort : fs, 1.f, tl + C_V + PLANES * (q & 1));
+                warp_arrive(&bar[B_A + (q & 1)], lane);
+            }
+            if (!ok) break;
         }
     } else if (w < 8) {
         // ---- B: the scores; Query X's rows ----
         const int q = w & 3;
-        const float both = p.in * p.by;
+        // factors within a block of 32 columns: before the diagonal block lambda^(31 - i) (times lambda^(rows to the block)),
+        // in it lambda^(row - column), backwards lambda^i and lambda^(column - row)
+        f2 near[16], diag[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float both = p.in * p.by;
+            float u[2], d[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                u[e] = both * pw[back ? i + e : 31 - i - e];
+                const int k = back ? i + e - lane : lane - i - e;
+                d[e] = k >= 0 ? both * pw[max(k, 0)] : 0.f;
+            }
+            near[i / 2] = pk2(u[0], u[1]);
+            diag[i / 2] = pk2(d[0], d[1]);
+        }
         for (int c = 0; c < nc; ++c) {
             const int n = tokens(c);
             if (!wait(B_P, c)) break;
-            uint32_t o[4][16];
-#pragma unroll
+            // a block is read, scaled and written back packed, into columns that were read before
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
-                const bool full = back ? j > q : j < q;
-                if (full || j == q) {
+                uint32_t o[16];
+                if (back ? j >= q : j <= q) {
                     float v[32];
                     tc::tmem_ld32(tl + C_P + 32 * j, v);
-                    if (full) {
-                        // lambda^|row - s| in two factors, the second the same for every row
+                    if (j != q) {
                         const float e = pw[back ? 32 * j - row : row - 32 * j - 31];
                         const f2 e2 = pk2(e, e);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const f2 y = mul2(mul2(*reinterpret_cast<const f2*>(fb + 2 * i), e2), pk2(v[2 * i], v[2 * i + 1]));
+                            const f2 y = mul2(pk2(v[2 * i], v[2 * i + 1]), mul2(near[i], e2));
                             up2(y, v[2 * i], v[2 * i + 1]);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int d = back ? i - lane : lane - i;
-                            v[i] = d >= 0 ? v[i] * (both * pw[max(d, 0)]) : 0.f;
+                        for (int i = 0; i < 16; ++i) {
+                            const f2 y = mul2(pk2(v[2 * i], v[2 * i + 1]), diag[i]);
+                            up2(y, v[2 * i], v[2 * i + 1]);
                         }
                     }
-                    if (n < LC)
+                    if (n < LC)  // (a growing state's factors may be infinite there)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (32 * j + i >= n) v[i] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[j][i] = pack2(v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < 16; ++i) o[i] = pack2(v[2 * i], v[2 * i + 1]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[j][i] = 0u;
+                    for (int i = 0; i < 16; ++i) o[i] = 0u;
                 }
+                tmem_st16u(tl + C_P + 16 * j, o);
             }
-            warp_arrive(&bar[B_PREAD], lane);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tmem_st16u(tl + C_P + 16 * j, o[j]);
             tmem_wait_st();
+            const float f = p.by * decay(slope, back ? max(n - 1 - row, 0) : row + 1);
             if (!wait(B_QX, c)) break;
-            const float f = p.by * pw[back ? max(n - 1 - row, 0) : row + 1];
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
                 float v[32];
                 tc::tmem_ld32(tl + C_O + 32 * j, v);
@@ -309,72 +393,63 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     } else if (w < 12) {
         // ---- C: the state as an operand, its decay; the output ----
         unsigned char* xt = sm + W_X;
-        auto store_out = [&](int c) {
-            const int n = tokens(c), t = g.t0 + LC * place(c) + row;
-            const size_t off = (size_t(t) * a.H + hd) * D, ld = size_t(a.H) * D;
-            const int even = row & ~1;
-            float v[4][32];
-            if (p.out_fp32) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    tc::tmem_ld32(tl + C_O + 32 * j, v[0]);
-                    tc::st_rows_paired_f32<32>(static_cast<float*>(p.out) + off + 32 * j, ld, v[0], lane, even < n, even + 1 < n);
-                }
-                warp_arrive(&bar[B_OFREE], lane);
-            } else {
-                uint4 x[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    tc::tmem_ld32(tl + C_O + 32 * j, v[j]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[j][i] = make_uint4(pack2(v[j][8 * i], v[j][8 * i + 1]), pack2(v[j][8 * i + 2], v[j][8 * i + 3]),
-                                             pack2(v[j][8 * i + 4], v[j][8 * i + 5]), pack2(v[j][8 * i + 6], v[j][8 * i + 7]));
-                }
-                warp_arrive(&bar[B_OFREE], lane);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tc::st_rows_paired<4>(reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off + 32 * j), ld / 2,
-                                          x[j], lane, even < n, even + 1 < n);
-            }
-        };
-        for (int c = 0; c < nc; ++c) {
-            const float f = pw[tokens(c)];
-            if (c > 0 && !wait(B_S, c - 1)) break;
+        for (int c = 0; c <= nc; ++c) {
+            if (c < nc) {
+                const float f = decay(slope, tokens(c));
+                if (!(c > 0 ? wait(B_S, c - 1) : wait(B_X0, 0))) break;
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                float v[32];
-                if (c > 0) {
+                for (int j = 0; j < 4; ++j) {
+                    float v[32];
                     tc::tmem_ld32(tl + C_X + 32 * j, v);
-                } else if (!x0) {
+                    uint32_t b[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                } else if (p.trans) {
+                    for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    tc::st_sw128(xt + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(x0 + row * D + 32 * j + i);
-                        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = x0[(32 * j + i) * D + row];
+                    for (int i = 0; i < 32; ++i) v[i] *= f;
+                    tc::tmem_st32(tl + C_X + 32 * j, v);
                 }
-                uint32_t b[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
-                tc::st_sw128(xt + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= f;
-                tc::tmem_st32(tl + C_X + 32 * j, v);
+                tc::fence_async_smem();
+                warp_arrive(&bar[B_C], lane);
             }
-            tc::fence_async_smem();
-            warp_arrive(&bar[B_C], lane);
-            if (c > 0) {
-                if (!wait(B_O, c - 1)) break;
-                store_out(c - 1);
+            if (c == 0) continue;
+            const int d = c - 1;  // the chunk whose output is ready
+            if (!wait(B_O, d)) break;
+            if (staged(d)) {
+                unsigned char* ot = tile(d, 2);
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    float v[32];
+                    tc::tmem_ld32(tl + C_O + 32 * j, v);
+                    uint32_t b[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    tc::st_sw128(ot + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
+                }
+                tc::fence_async_smem();
+            } else {
+                const int n = tokens(d), even = row & ~1;
+                const size_t off = (size_t(g.t0 + LC * place(d) + row) * a.H + hd) * D, ld = size_t(a.H) * D;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    float v[32];
+                    tc::tmem_ld32(tl + C_O + 32 * j, v);
+                    if (p.out_fp32) {
+                        tc::st_rows_paired_f32<32>(static_cast<float*>(p.out) + off + 32 * j, ld, v, lane, even < n, even + 1 < n);
+                    } else {
+                        uint4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
+                                              pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
+                        tc::st_rows_paired<4>(reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off + 32 * j),
+                                              ld / 2, x, lane, even < n, even + 1 < n);
+                    }
+                }
             }
+            warp_arrive(&bar[B_OFREE], lane);
+            if (lane == 0) mbar_arrive(&bar[B_STAGED + (d & 1)]);
         }
-        if (wait(B_O, nc - 1)) store_out(nc - 1);
         if (x1 && wait(B_S, nc - 1)) {
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
@@ -391,68 +466,102 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
             }
         }
     } else if (w == 12) {
-        // ---- loads ----
-        if (lane == 0) {
-            const CUtensorMap *mq = &tm.m[p.query], *mk = &tm.m[p.key], *mv = &tm.m[p.value];
-            int done = 0;
-            for (int c = 0; c < nc; ++c) {
-                const int s = c & 1, t = g.t0 + LC * place(c);
-                if (c >= 2 && !wait1(B_EMPTY + s, (c >> 1) - 1)) break;
-                tc::mbar_expect_tx(&bar[B_QK + s], 2 * TILE);
-                tc::tma4(tile(c, 1), mk, 0, t, 0, hd / p.rk, &bar[B_QK + s]);
-                tc::tma4(tile(c, 0), mq, 0, t, 0, hd / p.rq, &bar[B_QK + s]);
-                tc::mbar_expect_tx(&bar[B_V + s], TILE);
-                tc::tma4(tile(c, 2), mv, 0, t, 0, hd / p.rv, &bar[B_V + s]);
-                done = c + 1;
+        // ---- loads, two chunks ahead as their tiles are spent; the output's stores ----
+        const CUtensorMap *mq = &tm.m[p.query], *mk = &tm.m[p.key], *mv = &tm.m[p.value], *mo = &tm.m[p.store];
+        auto load = [&](int c, int which, const CUtensorMap* m, int share) {
+            uint64_t* b = &bar[(which == 2 ? B_V : B_QK) + (c & 1)];
+            if (elect()) {
+                tc::mbar_expect_tx(b, TILE);
+                tc::tma4(tile(c, which), m, 0, g.t0 + LC * place(c), 0, hd / share, b);
             }
-            for (int c = max(done - 2, 0); c < done; ++c) {  // every copy has landed before the block ends
-                tc::mbar_wait(&bar[B_QK + (c & 1)], (c >> 1) & 1);
-                tc::mbar_wait(&bar[B_V + (c & 1)], (c >> 1) & 1);
+            __syncwarp();
+        };
+        int lq = 0, lv = 0;  // chunks whose rows are on their way or here
+        for (int c = -2; c < nc; ++c) {
+            const int s = c & 1, ahead = c + 2;
+            const bool more = ahead < nc;
+            if (more) {
+                if (c >= 0 && !wait(B_QFREE + s, c >> 1)) break;
+                load(ahead, 0, mq, p.rq);
+                if (c >= 0 && !wait(B_KFREE + s, c >> 1)) break;
+                load(ahead, 1, mk, p.rk);
+                lq = ahead + 1;
+            }
+            if (c >= 0) {
+                if (!wait(B_STAGED + s, c >> 1)) break;
+                if (staged(c) && elect()) {
+                    tma_store4(mo, 0, g.t0 + LC * place(c), 0, hd, tile(c, 2));
+                    tc::bulk_commit();
+                    tc::bulk_wait_read0();
+                }
+                __syncwarp();
+            }
+            if (more) {
+                load(ahead, 2, mv, p.rv);
+                lv = ahead + 1;
             }
         }
-    } else if (lane == 0) {
+        if (elect()) tc::bulk_wait0();
+        __syncwarp();
+        if (!ok) {  // every copy has landed before the block ends
+            for (int c = max(lq - 2, 0); c < lq; ++c) tc::mbar_wait(&bar[B_QK + (c & 1)], (c >> 1) & 1, 100000000ull);
+            for (int c = max(lv - 2, 0); c < lv; ++c) tc::mbar_wait(&bar[B_V + (c & 1)], (c >> 1) & 1, 100000000ull);
+        }
+    } else {
         // ---- products ----
         const uint32_t ID = tc::idesc_bf16(128, 128, false, false), IDt = tc::idesc_bf16(128, 128, false, true);
         const uint64_t dX = tc::sdesc(smem_u32(sm + W_X), 16, 1024);
         auto kstep = [](int s) { return uint64_t(((s >> 2) * int(TILE / 2) + (s & 3) * 32) >> 4); };  // along the channels
         auto tstep = [](int s) { return uint64_t((s * 2048) >> 4); };                                 // along the tokens
-        auto scores = [&](int c) {
-            if (!wait1(B_QK + (c & 1), c >> 1)) return false;
-            if (tokens(c) < LC && !wait1(B_FIX, 0)) return false;
-            const uint64_t dq = tc::sdesc(smem_u32(tile(c, 0)), 16, 1024), dk = tc::sdesc(smem_u32(tile(c, 1)), 16, 1024);
+        for (int c = -1; c < nc; ++c) {
+            if (c >= 0) {
+                if (!wait(B_C, c) || (c > 0 && !wait(B_OFREE, c - 1))) break;
+                if (elect()) {
+                    const uint64_t dq = tc::sdesc(smem_u32(tile(c, 0)), 16, 1024);
 #pragma unroll
-            for (int s = 0; s < 8; ++s) tc::mma(tbase + C_P, dq + kstep(s), dk + kstep(s), ID, s > 0);
-            tc::mma_commit(&bar[B_P]);
-            return true;
-        };
-        if (scores(0)) {
-            for (int c = 0; c < nc; ++c) {
-                if (!wait1(B_C, c) || (c > 0 && !wait1(B_OFREE, c - 1))) break;
-                const uint64_t dq = tc::sdesc(smem_u32(tile(c, 0)), 16, 1024);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) tc::mma(tbase + C_O, dq + kstep(s), dX + kstep(s), ID, s > 0);
-                tc::mma_commit(&bar[B_QX]);
-                if (adds(c)) {
-                    if (!wait1(B_A, c)) break;
-                    const uint64_t dk = tc::sdesc(smem_u32(tile(c, 1)), TILE / 2, 1024);
-#pragma unroll
-                    for (int pl = 0; pl < 3; ++pl) {
-                        const uint32_t ap = tbase + (pl == 0 ? C_LO : pl == 1 ? C_MID : C_HI);
-#pragma unroll
-                        for (int s = 0; s < 8; ++s) mma_ta(tbase + C_X, ap + 8 * s, dk + tstep(s), IDt, 1u);
-                    }
-                    tc::mma_commit(&bar[B_S]);
+                    for (int s = 0; s < 8; ++s) tc::mma(tbase + C_O, dq + kstep(s), dX + kstep(s), ID, s > 0);
+                    tc::mma_commit(&bar[B_QX]);
+                    tc::mma_commit(&bar[B_QFREE + (c & 1)]);
                 }
-                if (!wait1(B_B, c)) break;
-                const uint64_t dv = tc::sdesc(smem_u32(tile(c, 2)), TILE / 2, 1024);
+                __syncwarp();
+                if (adds(c)) {
+                    for (int q = 4 * c; q < 4 * c + 4; ++q) {
+                        if (!wait(B_A + (q & 1), q >> 1)) break;
+                        if (elect()) {
+                            quarter_products(tbase + C_X, tbase + C_V + PLANES * (q & 1),
+                                             tc::sdesc(smem_u32(tile(c, 1)), TILE / 2, 1024), q & 3, IDt, false);
+                            tc::mma_commit(&bar[B_AFREE + (q & 1)]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (elect()) tc::mma_commit(&bar[B_S]);
+                    __syncwarp();
+                }
+                if (!wait(B_V + (c & 1), c >> 1) || !wait(B_B, c)) break;
+                if (elect()) {
+                    const uint64_t dv = tc::sdesc(smem_u32(tile(c, 2)), TILE / 2, 1024);
+                    tc::mma_commit(&bar[B_KFREE + (c & 1)]);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) mma_ta(tbase + C_O, tbase + C_P + 8 * s, dv + tstep(s), IDt, 1u);
-                tc::mma_commit(&bar[B_O]);
-                tc::mma_commit(&bar[B_EMPTY + (c & 1)]);
-                if (c + 1 < nc && !scores(c + 1)) break;
+                    for (int s = 0; s < 8; ++s) mma_ta(tbase + C_O, tbase + C_P + 8 * s, dv + tstep(s), IDt, 1u);
+                    tc::mma_commit(&bar[B_O]);
+                }
+                __syncwarp();
+            }
+            if (c + 1 < nc) {
+                const int d = c + 1;
+                if (!wait(B_QK + (d & 1), d >> 1)) break;
+                if (tokens(d) < LC && !wait(B_FIX, 0)) break;
+                if (elect()) {
+                    const uint64_t dq = tc::sdesc(smem_u32(tile(d, 0)), 16, 1024), dk = tc::sdesc(smem_u32(tile(d, 1)), 16, 1024);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) tc::mma(tbase + C_P, dq + kstep(s), dk + kstep(s), ID, s > 0);
+                    tc::mma_commit(&bar[B_P]);
+                }
+                __syncwarp();
             }
         }
-        if (!ok) tc::drain_mmas(&bar[B_SPARE], 100000000ull);
+        if (!ok && elect()) tc::drain_mmas(&bar[B_SPARE], 100000000ull);
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -463,18 +572,22 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
 
 // ---- what a segment adds to the state ----
 
-constexpr int STATE_THREADS = 320;  // two groups of four warps take the chunks in turn; loads: warp 8, products: 9
+constexpr int STATE_THREADS = 320;  // two groups of four warps take the quarters in turn; loads: warp 8, products: 9
 constexpr int S_STAGES = 3;
+constexpr int S_BUFS = 4;           // quarters of split values in tensor memory
 constexpr int S_TAB = S_STAGES * 2 * int(TILE);
 constexpr int S_BAR = S_TAB + 128 * 4;
-constexpr size_t STATE_SMEM = S_BAR + 128 + 1024;
-enum StateBar { SB_FULL = 0, SB_EMPTY = S_STAGES, SB_READY = 2 * S_STAGES, SB_FREE = SB_READY + 2, SB_DONE = SB_FREE + 2, SB_FIX, SB_SPARE, SB_END };
+constexpr size_t STATE_SMEM = S_BAR + 256 + 1024;
+enum StateBar {
+    SB_FULL = 0, SB_EMPTY = S_STAGES, SB_READY = 2 * S_STAGES, SB_FREE = SB_READY + S_BUFS, SB_DONE = SB_FREE + S_BUFS, SB_FIX,
+    SB_SPARE, SB_END
+};
 
 // No decay of the state between chunks: a token's factor reaches to the segment's end, the products add up.
 __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int ps, const __grid_constant__ LinMaps tm) {
     extern __shared__ unsigned char smraw[];
     unsigned char* sm = tc::align1024(smraw);
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int hd = int(blockIdx.x % unsigned(a.H));
     const LinPass& p = a.pass[ps];
     Seg g;
@@ -490,11 +603,12 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
     const float slope = a.slope[hd];
     if (tid == 0) {
         for (int i = 0; i < SB_SPARE; ++i)
-            tc::mbar_init(&bar[i], i == SB_READY || i == SB_READY + 1 || i == SB_FIX ? 4 : 1);
+            tc::mbar_init(&bar[i], (i >= SB_READY && i < SB_FREE) || i == SB_FIX ? 4 : 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
     if (w == 0) tc::tmem_alloc(tslot, 512);
+    if (w == 8 && lane < 2) tc::tma_prefetch_map(&tm.m[lane ? p.value : p.key]);
     if (tid < LC) fs[tid] = p.in * decay(slope, back ? tid + 1 : LC - 1 - tid);
     tc::fence_before_sync();
     __syncthreads();
@@ -504,34 +618,39 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
     const int row = 32 * (w & 3) + lane;
     auto tile = [&](int c, int which) { return sm + ((c % S_STAGES) * 2 + which) * TILE; };
     bool ok = true;  // waits as in the walk
-    auto wait1 = [&](int b, int turn) {
-        if (ok && !tc::mbar_wait(&bar[b], uint32_t(turn) & 1u)) {
-            ok = false;
-            *abort_flag = 1;
-        }
+    auto wait = [&](int b, int turn) {
+        const bool done = ok && bounded_wait(&bar[b], uint32_t(turn) & 1u);
+        ok = __all_sync(0xffffffffu, done);
+        if (!ok) *abort_flag = 1;
         tc::fence_after_sync();
         return ok;
     };
-    auto wait = [&](int b, int turn) { return ok = __all_sync(0xffffffffu, wait1(b, turn)); };
-    constexpr uint32_t C_V = 128;  // columns: state 0, then two sets of three planes
+    constexpr uint32_t C_V = 128;  // columns: state 0, then the quarters of split values
 
     if (w < 8) {
         const int grp = w >> 2;
-        for (int c = grp; c < nc; c += 2) {
+        for (int c = 0; c < nc; ++c) {
             const int n = min(LC, g.len - LC * c);
             if (!wait(SB_FULL + c % S_STAGES, c / S_STAGES)) break;
             if (n < LC) {
-                clear_rows(tile(c, 0), n, tid & 127);
-                clear_rows(tile(c, 1), n, tid & 127);
-                tc::fence_async_smem();
-                warp_arrive(&bar[SB_FIX], lane);
+                if (grp == 0) {
+                    clear_rows(tile(c, 0), n, tid);
+                    clear_rows(tile(c, 1), n, tid);
+                    tc::fence_async_smem();
+                    warp_arrive(&bar[SB_FIX], lane);
+                }
                 if (!wait(SB_FIX, 0)) break;
             }
-            if (c >= 2 && !wait(SB_FREE + grp, (c >> 1) - 1)) break;
-            const uint32_t v = tl + C_V + 192 * grp;
             // forwards only full chunks come here (the last segment adds to nothing)
-            split_values(tile(c, 1), row, fs, decay(slope, back ? LC * c : g.len - LC * (c + 1)), v, v + 64, v + 128);
-            warp_arrive(&bar[SB_READY + grp], lane);
+            const float all = decay(slope, back ? LC * c : g.len - LC * (c + 1));
+#pragma unroll 1
+            for (int q = 4 * c + grp; q < 4 * c + 4; q += 2) {
+                const int b = q % S_BUFS;
+                if (q >= S_BUFS && !wait(SB_FREE + b, q / S_BUFS - 1)) break;
+                split_quarter(tile(c, 1), q & 3, w, lane, fs, all, tl + C_V + PLANES * b);
+                warp_arrive(&bar[SB_READY + b], lane);
+            }
+            if (!ok) break;
         }
         if (w < 4 && wait(SB_DONE, 0)) {
 #pragma unroll 1
@@ -543,35 +662,36 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
             }
         }
     } else if (w == 8) {
-        if (lane == 0) {
-            const CUtensorMap *mk = &tm.m[p.key], *mv = &tm.m[p.value];
-            int done = 0;
-            for (int c = 0; c < nc; ++c) {
-                const int s = c % S_STAGES, t = g.t0 + LC * c;
-                if (c >= S_STAGES && !wait1(SB_EMPTY + s, c / S_STAGES - 1)) break;
-                tc::mbar_expect_tx(&bar[SB_FULL + s], 2 * TILE);
-                tc::tma4(tile(c, 0), mk, 0, t, 0, hd / p.rk, &bar[SB_FULL + s]);
-                tc::tma4(tile(c, 1), mv, 0, t, 0, hd / p.rv, &bar[SB_FULL + s]);
-                done = c + 1;
-            }
-            for (int c = max(done - S_STAGES, 0); c < done; ++c) tc::mbar_wait(&bar[SB_FULL + c % S_STAGES], (c / S_STAGES) & 1);
-        }
-    } else if (lane == 0) {
-        const uint32_t IDt = tc::idesc_bf16(128, 128, false, true);
+        const CUtensorMap *mk = &tm.m[p.key], *mv = &tm.m[p.value];
+        int done = 0;
         for (int c = 0; c < nc; ++c) {
-            if (!wait1(SB_READY + (c & 1), c >> 1)) break;
-            const uint64_t dk = tc::sdesc(smem_u32(tile(c, 0)), TILE / 2, 1024);
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ta(tbase, tbase + C_V + 192 * (c & 1) + 64 * pl + 8 * s, dk + uint64_t((s * 2048) >> 4), IDt,
-                           c > 0 || pl < 2 || s > 0);
-            tc::mma_commit(&bar[SB_FREE + (c & 1)]);
-            tc::mma_commit(&bar[SB_EMPTY + c % S_STAGES]);
+            const int s = c % S_STAGES, t = g.t0 + LC * c;
+            if (c >= S_STAGES && !wait(SB_EMPTY + s, c / S_STAGES - 1)) break;
+            if (elect()) {
+                tc::mbar_expect_tx(&bar[SB_FULL + s], 2 * TILE);
+                tc::tma4(tile(c, 1), mv, 0, t, 0, hd / p.rv, &bar[SB_FULL + s]);
+                tc::tma4(tile(c, 0), mk, 0, t, 0, hd / p.rk, &bar[SB_FULL + s]);
+            }
+            __syncwarp();
+            done = c + 1;
         }
-        tc::mma_commit(&bar[SB_DONE]);
-        if (!ok) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
+        if (!ok)
+            for (int c = max(done - S_STAGES, 0); c < done; ++c)
+                tc::mbar_wait(&bar[SB_FULL + c % S_STAGES], (c / S_STAGES) & 1, 100000000ull);
+    } else {
+        const uint32_t IDt = tc::idesc_bf16(128, 128, false, true);
+        for (int q = 0; q < 4 * nc; ++q) {
+            const int c = q >> 2, b = q % S_BUFS;
+            if (!wait(SB_READY + b, q / S_BUFS)) break;
+            if (elect()) {
+                quarter_products(tbase, tbase + C_V + PLANES * b, tc::sdesc(smem_u32(tile(c, 0)), TILE / 2, 1024), q & 3, IDt, q == 0);
+                tc::mma_commit(&bar[SB_FREE + b]);
+                if ((q & 3) == 3) tc::mma_commit(&bar[SB_EMPTY + c % S_STAGES]);
+                if (q == 4 * nc - 1) tc::mma_commit(&bar[SB_DONE]);
+            }
+            __syncwarp();
+        }
+        if (!ok && elect()) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
     }
     __syncwarp();
     tc::fence_before_sync();

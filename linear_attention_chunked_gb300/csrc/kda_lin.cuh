@@ -18,6 +18,7 @@ namespace kda {
 // and out_t = by X_t^T query_t.
 struct LinPass {
     int query, key, value;  // tensors of LinMaps
+    int store;              // the output's (bf16 outputs)
     int rq, rk, rv;         // heads that share a row of each
     void* out;              // dense [T, H, 128]
     int out_fp32;
@@ -29,7 +30,7 @@ struct LinPass {
 };
 
 constexpr int LC = 128;  // tokens of a chunk
-constexpr int LIN_MAXSEG = 4096;
+
 
 // Documents are cut into segments of `seg` tokens (the last one shorter; an empty document has one empty
 // segment), which are walked side by side.  The state between two segments of a document lies in a slot.
@@ -58,9 +59,9 @@ struct LinArgs {
 };
 
 // The rows of a call as TMA tensors: {64 channels, tokens, half of the head, head}, boxes of 128 tokens x one head,
-// which land as two 128-byte-swizzled tiles [64 channels of 128 tokens].  LinPass names them by index.
+// which land as two 128-byte-swizzled tiles [64 channels of 128 tokens]; the outputs likewise.  LinPass names them.
 struct LinMaps {
-    CUtensorMap m[4];
+    CUtensorMap m[7];
 };
 
 // single tokens (kda_lin_step.cu)

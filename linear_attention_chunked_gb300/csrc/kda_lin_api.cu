@@ -49,11 +49,11 @@ EncodeTiledFn encode_tiled() {
 }
 
 // Tokens of a segment, a power of two that depends on the heads alone: a document's results must not depend on the
-// pack, and a document alone has to fill the machine.  16384 tokens cut so give 512 blocks at 16 and at 64 heads;
-// the states between segments cost a second pass over two of the rows (50% more reads of a forward).
+// pack, and a document alone has to fill the machine.  Up to 16 heads the segments of 16384 tokens are 128 blocks, one
+// wave; the states between segments cost a second pass over two of the rows (50% more reads of a forward) and 64 KB each.
 int segment(int H) {
     int s = 512;
-    while (s < 32 * H && s < LIN_MAXSEG) s *= 2;
+    while (s < 128 * H && s < 2048) s *= 2;
     return s;
 }
 
@@ -130,28 +130,31 @@ LinArgs make_args(const kda_linattn_problem* p, const Regions& r, const float* s
 using bf = __nv_bfloat16;
 
 // The rows of a call, in the order of LinMaps
-enum { IN_Q, IN_K, IN_V, IN_DO };
+enum { IN_Q, IN_K, IN_V, IN_DO, OUT_O, OUT_DV, OUT_DK, OUT_DQ = OUT_O };
 
 // share: heads that share a row of q and k
-LinPass make_pass(int query, int key, int value, int share, void* out, int out_fp32, const float* s0, float* s_end,
-                  int trans, int back, float in, float by) {
+LinPass make_pass(int query, int key, int value, int share, int store, void* out, int out_fp32, const float* s0,
+                  float* s_end, int trans, int back, float in, float by) {
     auto per = [&](int t) { return t == IN_Q || t == IN_K ? share : 1; };
-    return {query, key, value, per(query), per(key), per(value), out, out_fp32, s0, s_end, trans, back, in, by};
+    return {query, key, value, store, per(query), per(key), per(value), out, out_fp32, s0, s_end, trans, back, in, by};
 }
 
-kda_status make_maps(const kda_linattn_problem* p, const void* q, const void* k, const void* v, const void* dO, LinMaps* tm) {
-    if (p->T == 0) return KDA_OK;  // no row is read
+struct Rows {
+    const void* p;
+    int heads;
+    int64_t ld;  // 0: dense
+};
+kda_status make_maps(int64_t T, const Rows (&rows)[7], LinMaps* tm) {
+    if (T == 0) return KDA_OK;  // no row is read
     EncodeTiledFn enc = encode_tiled();
     if (!enc) return KDA_ERR_CUDA;
-    const void* ptr[4] = {q, k, v, dO};
-    const int64_t dk = int64_t(p->Hk) * D, dv = int64_t(p->H) * D;
-    const int64_t ld[4] = {ld_or(p->ld_q, dk), ld_or(p->ld_k, dk), ld_or(p->ld_v, dv), dv};
-    for (int i = 0; i < 4; ++i) {
-        if (!ptr[i]) continue;
-        const cuuint64_t dims[4] = {64, cuuint64_t(p->T), 2, cuuint64_t(i < 2 ? p->Hk : p->H)};
-        const cuuint64_t strides[3] = {cuuint64_t(ld[i]) * 2, 128, D * 2};
+    for (int i = 0; i < 7; ++i) {
+        const Rows& r = rows[i];
+        if (!r.p) continue;
+        const cuuint64_t dims[4] = {64, cuuint64_t(T), 2, cuuint64_t(r.heads)};
+        const cuuint64_t strides[3] = {cuuint64_t(ld_or(r.ld, int64_t(r.heads) * D)) * 2, 128, D * 2};
         const cuuint32_t box[4] = {64, LC, 2, 1}, one[4] = {1, 1, 1, 1};
-        if (enc(&tm->m[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr[i]), dims, strides, box, one,
+        if (enc(&tm->m[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(r.p), dims, strides, box, one,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return KDA_ERR_CUDA;
@@ -206,11 +209,12 @@ kda_status kda_linattn_fwd(const kda_linattn_problem* p, const void* q, const vo
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LinArgs a = make_args(p, r, slope, ws);
     LinMaps tm{};
-    if (kda_status s = make_maps(p, q, k, v, nullptr, &tm)) return s;
+    const Rows rows[7] = {{q, p->Hk, p->ld_q}, {k, p->Hk, p->ld_k}, {v, p->H, p->ld_v}, {}, {o, p->H, 0}};
+    if (kda_status s = make_maps(p->T, rows, &tm)) return s;
     a.made_for = static_cast<int4*>(saved);
     a.front = reinterpret_cast<float*>(saved ? static_cast<char*>(saved) + r.kept : static_cast<char*>(ws) + r.front);
     a.passes = 1;
-    a.pass[0] = make_pass(IN_Q, IN_K, IN_V, p->H / p->Hk, o, 0, h0, ht, 0, 0, 1.f, p->scale);
+    a.pass[0] = make_pass(IN_Q, IN_K, IN_V, p->H / p->Hk, OUT_O, o, 0, h0, ht, 0, 0, 1.f, p->scale);
     if (a.direct) {
         if (!clear_status(ws, st)) return KDA_ERR_CUDA;
     } else {
@@ -235,9 +239,12 @@ kda_status kda_linattn_bwd(const kda_linattn_problem* p, const void* q, const vo
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LinArgs a = make_args(p, r, slope, ws);
     LinMaps tm{};
-    if (kda_status s = make_maps(p, q, k, v, dO, &tm)) return s;
     char* w = static_cast<char*>(ws);
     const int share = p->H / p->Hk, part = share > 1;
+    const Rows none{};
+    const Rows rows[7] = {{q, p->Hk, p->ld_q}, {k, p->Hk, p->ld_k}, {v, p->H, p->ld_v}, {dO, p->H, 0},
+                          part ? none : Rows{dq, p->H, 0}, {dv, p->H, 0}, part ? none : Rows{dk, p->H, 0}};
+    if (kda_status s = make_maps(p->T, rows, &tm)) return s;
     float* pq = reinterpret_cast<float*>(w + r.share_q);
     float* pk = reinterpret_cast<float*>(w + r.share_k);
     a.expected = static_cast<const int4*>(saved);
@@ -248,16 +255,16 @@ kda_status kda_linattn_bwd(const kda_linattn_problem* p, const void* q, const vo
     } else {
         launch_lin_plan(a, st);
         if (!saved) {  // the states between segments, as the forward's
-            a.pass[0] = make_pass(IN_Q, IN_K, IN_V, share, nullptr, 0, h0, nullptr, 0, 0, 1.f, p->scale);
+            a.pass[0] = make_pass(IN_Q, IN_K, IN_V, share, 0, nullptr, 0, h0, nullptr, 0, 0, 1.f, p->scale);
             launch_lin_states(a, tm, 0, st);
         }
-        a.pass[0] = make_pass(IN_K, IN_Q, IN_DO, share, nullptr, 0, dht, nullptr, 0, 1, p->scale, 1.f);
+        a.pass[0] = make_pass(IN_K, IN_Q, IN_DO, share, 0, nullptr, 0, dht, nullptr, 0, 1, p->scale, 1.f);
         launch_lin_states(a, tm, 0, st);
     }
     a.passes = 3;
-    a.pass[0] = make_pass(IN_DO, IN_V, IN_K, share, part ? static_cast<void*>(pq) : dq, part, h0, nullptr, 1, 0, 1.f, p->scale);
-    a.pass[1] = make_pass(IN_K, IN_Q, IN_DO, share, dv, 0, dht, dh0, 0, 1, p->scale, 1.f);
-    a.pass[2] = make_pass(IN_V, IN_DO, IN_Q, share, part ? static_cast<void*>(pk) : dk, part, dht, nullptr, 1, 1, p->scale, 1.f);
+    a.pass[0] = make_pass(IN_DO, IN_V, IN_K, share, OUT_DQ, part ? static_cast<void*>(pq) : dq, part, h0, nullptr, 1, 0, 1.f, p->scale);
+    a.pass[1] = make_pass(IN_K, IN_Q, IN_DO, share, OUT_DV, dv, 0, dht, dh0, 0, 1, p->scale, 1.f);
+    a.pass[2] = make_pass(IN_V, IN_DO, IN_Q, share, OUT_DK, part ? static_cast<void*>(pk) : dk, part, dht, nullptr, 1, 1, p->scale, 1.f);
     launch_lin_walk(a, tm, st);
     if (part && p->T > 0) {
         const int64_t rows = p->T * p->Hk;
