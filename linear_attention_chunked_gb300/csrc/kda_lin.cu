@@ -18,10 +18,12 @@
 //     QX     A = Query,                   B = X^T in shared memory, bf16 [values][keys]
 //     P'V    A = P' (tensor memory),      B = Value [tokens][values] read across
 //     state  A = values^T (tensor memory), B = Key read across
-// Three groups of warps work at once: A scales and splits the values, B masks and rounds the scores and scales
-// Query X's rows, C rounds and decays the state and hands the output to TMA (through the chunk's spent value tile), and
-// two warps issue loads and products.
+// Four groups of warps work at once: A (two groups) scales and splits the values, B masks and rounds the scores and
+// hands the output to TMA, C rounds and decays the state and scales Query X's rows; three warps issue loads, products and
+// stores.  The chunk's tiles go through a ring of five, each taken again as soon as its last product has read it.
 // Rows behind a document's end (another's) are cleared in K and V, so nothing of them, were it not finite, is multiplied.
+#include <limits.h>
+
 #include "kda_lin.cuh"
 #include "kda_ssm.cuh"
 #include "kda_tc.cuh"
@@ -46,10 +48,9 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// 16 lanes x 16 columns: lane i holds row i / 4 of column 4 j + i % 4 in word 2 j and row 8 + i / 4 in word 2 j + 1
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+// 16 lanes x 8 columns: lane i holds row i / 4 of column 4 j + i % 4 in word 2 j and row 8 + i / 4 in word 2 j + 1
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -100,36 +101,32 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int n, int tid) 
     }
 }
 
-// A quarter (32 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into three bf16
+// A piece (16 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into three bf16
 // planes as the left operand of a product in tensor memory: lane = channel, token pairs in the columns taddr.. of
-// hi, mid and lo, 16 each.  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
+// hi, mid and lo, 8 each.  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
 // the pairs that a 16-lane store takes.
-constexpr uint32_t PLANES = 48;  // columns of a quarter
-__device__ __forceinline__ void split_quarter(const unsigned char* tile, int quarter, int w, int lane, const float* f, float all,
-                                              uint32_t taddr) {
+constexpr int PIECES = LC / 16;
+constexpr uint32_t PLANES = 24;  // columns of a piece
+__device__ __forceinline__ void split_piece(const unsigned char* tile, int piece, int w, int lane, const float* f, float all,
+                                            uint32_t taddr) {
     const int m = lane >> 3, r = lane & 7;
-    const unsigned char* base = tile + ((w & 3) >> 1) * (TILE / 2) + (32 * quarter + (m >> 1) * 8 + r) * 128;
+    const unsigned char* base = tile + ((w & 3) >> 1) * (TILE / 2) + (16 * piece + (m >> 1) * 8 + r) * 128;
     const int c8 = (w & 1) * 4 + (m & 1);
+    uint32_t x[2][4];
+    ldsm4t(x[0], base + ((c8 ^ r) << 4));
+    ldsm4t(x[1], base + (((c8 + 2) ^ r) << 4));
     const f2 all2 = pk2(all, all);
-    f2 fw[4];
+    f2 fw[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        fw[i] = mul2(*reinterpret_cast<const f2*>(f + 32 * quarter + 8 * i + 2 * (lane & 3)), all2);
+    for (int i = 0; i < 2; ++i)
+        fw[i] = mul2(*reinterpret_cast<const f2*>(f + 16 * piece + 8 * i + 2 * (lane & 3)), all2);
     constexpr uint32_t mask = 0xffff0000u, flip = 0x80000000u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 channels
-        uint32_t x[8], hi[8], mid[8], lo[8];
-        {
-            uint32_t t[4];
-            const unsigned char* at = base + (((c8 + 2 * h) ^ r) << 4);
-            ldsm4t(t, at);
-            x[0] = t[0], x[1] = t[1], x[2] = t[2], x[3] = t[3];
-            ldsm4t(t, at + 16 * 128);
-            x[4] = t[0], x[5] = t[1], x[6] = t[2], x[7] = t[3];
-        }
+        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const f2 y = mul2(fw[j >> 1], pk2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & mask)));
+        for (int j = 0; j < 4; ++j) {
+            const f2 y = mul2(fw[j >> 1], pk2(__uint_as_float(x[h][j] << 16), __uint_as_float(x[h][j] & mask)));
             float y0, y1, r0, r1;
             up2(y, y0, y1);
             hi[j] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
@@ -143,19 +140,18 @@ __device__ __forceinline__ void split_quarter(const unsigned char* tile, int qua
             lo[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
         }
         const uint32_t at = taddr + (uint32_t(16 * h) << 16);
-        tmem_st_16x16(at, hi);
-        tmem_st_16x16(at + 16, mid);
-        tmem_st_16x16(at + 32, lo);
+        tmem_st_16x8(at, hi);
+        tmem_st_16x8(at + 8, mid);
+        tmem_st_16x8(at + 16, lo);
     }
     tmem_wait_st();
 }
-// The products of a quarter: D += planes * rows 32 quarter.. of the key tile, read across
-__device__ __forceinline__ void quarter_products(uint32_t d, uint32_t planes, uint64_t key, int quarter, uint32_t idesc, bool first) {
-#pragma unroll
-    for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-            mma_ta(d, planes + 16 * pl + 8 * s, key + uint64_t(((2 * quarter + s) * 2048) >> 4), idesc, !first || pl < 2 || s > 0);
+// The products of a piece: D += planes * rows 16 piece.. of the key tile, read across
+__device__ __forceinline__ void piece_products(uint32_t d, uint32_t planes, uint64_t key, int piece, uint32_t idesc, bool first) {
+    const uint64_t b = key + uint64_t((piece * 2048) >> 4);
+    mma_ta(d, planes + 16, b, idesc, !first);
+    mma_ta(d, planes + 8, b, idesc, 1u);
+    mma_ta(d, planes, b, idesc, 1u);
 }
 
 // The segment of a block: {document, first token, length, flags as in LinPlan, w}; false: none (or malformed offsets)
@@ -170,6 +166,17 @@ __device__ __forceinline__ bool lin_segment(const LinArgs& a, int i, Seg& s) {
         s.doc = e.x, s.t0 = e.y, s.len = e.z & 0xffff, s.w = e.w;
         s.first = e.z >> 16 & 1, s.last = e.z >> 17 & 1;
         return true;
+    }
+    // a document for every i: the longest first, by a warp's lanes, where they have a lane each
+    if (a.N > 1 && a.N <= 32) {
+        const int lane = threadIdx.x & 31;
+        const int own = lane < a.N ? a.cu[lane + 1] - a.cu[lane] : INT_MIN;
+        int rank = 0;
+        for (int k = 0; k < a.N; ++k) {
+            const int x = __shfl_sync(0xffffffffu, own, k);
+            rank += x > own || (x == own && k < lane);
+        }
+        i = __ffs(__ballot_sync(0xffffffffu, lane < a.N && rank == i)) - 1;
     }
     const int c0 = a.cu[i], c1 = a.cu[i + 1];
     bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && (i > 0 || c0 == 0) && (i < a.N - 1 || c1 == a.T);
@@ -188,21 +195,27 @@ __device__ __forceinline__ bool lin_segment(const LinArgs& a, int i, Seg& s) {
 
 // ---- the walk ----
 
-constexpr int WALK_THREADS = 448;  // A: warps 0-3, B: 4-7, C: 8-11, loads and stores: 12, products: 13
-constexpr int W_X = 6 * int(TILE);       // behind [2 stages][Query, Key, Value]
-constexpr int W_TAB = W_X + int(TILE);   // state factors of a full and of the short chunk, decays: [128] each
-constexpr int W_BAR = W_TAB + 3 * 128 * 4;
-constexpr size_t WALK_SMEM = W_BAR + 256 + 1024;
+// A: warps 0-7, B: 8-11, C: 12-15, loads: 16, products: 17, stores: 18
+constexpr int WALK_THREADS = 608;
+constexpr int W_TILES = 5;                         // ring of chunk tiles: Query, Key, Value of chunk 0, of chunk 1, ..
+constexpr int W_X = W_TILES * int(TILE);           // the state as an operand
+constexpr int W_OUT = W_X + int(TILE);             // an output on its way
+constexpr int W_TAB = W_OUT + int(TILE);           // state factors of a full and of the short chunk [128], score factors [32], [64]
+constexpr int W_BAR = W_TAB + (128 + 128 + 32 + 64) * 4;
+constexpr size_t WALK_SMEM = W_BAR + 320 + 1024;
 static_assert(WALK_SMEM <= 232448, "walk: shared memory above the opt-in limit");
 
-// tensor memory columns: scores (their rounded form in the first half), output, state, two quarters of split values
+// tensor memory columns: scores (their rounded form in the first half), output, state, pieces of split values
 constexpr uint32_t C_P = 0, C_O = 128, C_X = 256, C_V = 384;
+constexpr int W_PIECES = 4;
+static_assert(C_V + W_PIECES * PLANES <= 512, "walk: tensor memory");
 
-// Two of a kind: by stage (chunk & 1), or by quarter.  Loads have landed; a tile may be loaded again; ...
+// By tile: it has landed, it may be loaded again.  By piece: it is split, its columns may be written again.
 enum WalkBar {
-    B_QK = 0, B_V = 2, B_QFREE = 4, B_KFREE = 6, B_STAGED = 8, B_A = 10, B_AFREE = 12,
-    B_P = 14, B_QX, B_B, B_S, B_C, B_O, B_OFREE, B_FIX, B_X0, B_SPARE, B_END
+    B_FULL = 0, B_FREE = W_TILES, B_A = 2 * W_TILES, B_AFREE = B_A + W_PIECES,
+    B_P = B_AFREE + W_PIECES, B_QX, B_B, B_SCALED, B_S, B_C, B_O, B_OFREE, B_STAGED, B_STORED, B_FIX, B_X0, B_SPARE, B_END
 };
+static_assert(8 * B_END + 8 <= 320, "walk: barriers");
 
 __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const __grid_constant__ LinMaps tm) {
     extern __shared__ unsigned char smraw[];
@@ -232,23 +245,29 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + W_BAR + 8 * B_END + 4);
     float* fs = reinterpret_cast<float*>(sm + W_TAB);  // a full chunk's state factors
     float* fshort = fs + 128;                          // the short chunk's (of at most one)
-    float* pw = fshort + 128;                          // lambda^i
+    float* fn = fshort + 128;                          // score factors in a block off the diagonal, by column
+    float* fd = fn + 32;                               // and in it: [31 + row - column]
     const float slope = a.slope[hd];
     if (tid == 0) {
         for (int i = 0; i < B_SPARE; ++i) {
-            const bool four = (i >= B_STAGED && i < B_AFREE) || i == B_B || i == B_C || i == B_OFREE || i == B_FIX;
-            tc::mbar_init(&bar[i], i < B_V ? 2 : i == B_X0 ? 8 : four ? 4 : 1);
+            const bool four = (i >= B_A && i < B_AFREE) || i == B_B || i == B_SCALED || i == B_C || i == B_OFREE || i == B_STAGED;
+            tc::mbar_init(&bar[i], i == B_X0 ? 12 : i == B_FIX ? 8 : four ? 4 : 1);
         }
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
     if (w == 0) tc::tmem_alloc(tslot, 512);
-    if (w == 12 && lane < 3) tc::tma_prefetch_map(&tm.m[lane == 0 ? p.query : lane == 1 ? p.key : p.value]);
+    if (w == 16 && lane < 3) tc::tma_prefetch_map(&tm.m[lane == 0 ? p.query : lane == 1 ? p.key : p.value]);
     if (tid < LC) {
         fs[tid] = p.in * decay(slope, back ? tid + 1 : LC - 1 - tid);
         const int m = g.len - LC * (nc - 1);
         fshort[tid] = tid < m ? p.in * decay(slope, back ? tid + 1 : m - 1 - tid) : 0.f;
-        pw[tid] = decay(slope, tid);
+    } else if (tid < LC + 32) {
+        // lambda^(31 - i), times lambda^(row - the block's last column); backwards lambda^i, times lambda^(its first - row)
+        fn[tid - LC] = p.in * p.by * decay(slope, back ? tid - LC : LC + 31 - tid);
+    } else if (tid < LC + 96) {
+        const int d = (tid - LC - 32 - 31) * (back ? -1 : 1);
+        fd[tid - LC - 32] = d >= 0 ? p.in * p.by * decay(slope, d) : 0.f;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     // chunk c of the walk: its place in the segment and its tokens
     auto place = [&](int c) { return back ? nc - 1 - c : c; };
     auto tokens = [&](int c) { return min(LC, g.len - LC * place(c)); };
-    auto tile = [&](int c, int which) { return sm + ((c & 1) * 3 + which) * TILE; };
+    auto tile = [&](int i) { return sm + (i % W_TILES) * TILE; };  // tile 3 c: Query of chunk c, then Key, Value
     // whether chunk c's values still reach a state that is read; whether its output leaves by TMA
     auto adds = [&](int c) { return c + 1 < nc || x1; };
     auto staged = [&](int c) { return !p.out_fp32 && tokens(c) == LC; };
@@ -292,55 +311,91 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         }
         tc::tmem_st32(tl + C_X + 32 * j, v);
     };
-    // the groups share the blocks: A takes the first, B the second, C the others
-    if (w < 12) {
-#pragma unroll 1
-        for (int j = w >> 2; j < ((w >> 2) == 2 ? 4 : (w >> 2) + 1); ++j) start_block(j);
-        if (w < 8) warp_arrive(&bar[B_X0], lane);
+    auto landed = [&](int i) { return wait(B_FULL + i % W_TILES, i / W_TILES); };
+    // the groups share the blocks
+    if (w < 16) {
+        start_block(w >> 2);
+        if (w < 12) warp_arrive(&bar[B_X0], lane);
     }
 
-    if (w < 4) {
-        // ---- A: the values, scaled and split, a quarter at a time ----
+    if (w < 8) {
+        // ---- A: the values, scaled and split, a piece at a time ----
         for (int c = 0; c < nc; ++c) {
             const int n = tokens(c);
-            if (!wait(B_V + (c & 1), c >> 1)) break;
+            if (!landed(3 * c + 2)) break;
             if (n < LC) {  // the rows of other documents: cleared before any product reads them (one chunk of a walk)
-                if (!wait(B_QK + (c & 1), c >> 1)) break;
-                clear_rows(tile(c, 1), n, tid);
-                clear_rows(tile(c, 2), n, tid);
+                if (!landed(3 * c + 1)) break;
+                clear_rows(tile(3 * c + 1 + (w >> 2)), n, tid & 127);
                 tc::fence_async_smem();
                 warp_arrive(&bar[B_FIX], lane);
                 if (!wait(B_FIX, 0)) break;
             }
             if (!adds(c)) break;
-#pragma unroll 1
-            for (int q = 4 * c; q < 4 * c + 4; ++q) {
-                if (q >= 2 && !wait(B_AFREE + (q & 1), (q >> 1) - 1)) break;
-                split_quarter(tile(c, 2), q & 3, w, lane, n < LC ? fshort : fs, 1.f, tl + C_V + PLANES * (q & 1));
-                warp_arrive(&bar[B_A + (q & 1)], lane);
+            const float* f = n < LC ? fshort : fs;
+            for (int i = PIECES * c + (w >> 2); i < PIECES * (c + 1); i += 2) {
+                const int b = i % W_PIECES;
+                if (i >= W_PIECES && !wait(B_AFREE + b, i / W_PIECES - 1)) break;
+                split_piece(tile(3 * c + 2), i % PIECES, w, lane, f, 1.f, tl + C_V + PLANES * b);
+                warp_arrive(&bar[B_A + b], lane);
             }
             if (!ok) break;
         }
-    } else if (w < 8) {
-        // ---- B: the scores; Query X's rows ----
+    } else if (w < 12) {
+        // ---- B: the scores; the output ----
         const int q = w & 3;
-        // factors within a block of 32 columns: before the diagonal block lambda^(31 - i) (times lambda^(rows to the block)),
-        // in it lambda^(row - column), backwards lambda^i and lambda^(column - row)
-        f2 near[16], diag[16];
+        float e[3];  // the second factor of block j (back: j + 1)
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float both = p.in * p.by;
-            float u[2], d[2];
+        for (int j = 0; j < 3; ++j) e[j] = decay(slope, max(back ? 32 * (j + 1) - row : row - 32 * j - 31, 0));
+        const float* fr = fd + 31 + lane;
+        unsigned char* ot = sm + W_OUT;
+        for (int c = 0; c <= nc; ++c) {
+            if (c > 0) {
+                const int d = c - 1;  // the chunk whose output is ready
+                if (!wait(B_O, d)) break;
+                const int n = tokens(d);
+                if (staged(d)) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t o[2][16];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                u[e] = both * pw[back ? i + e : 31 - i - e];
-                const int k = back ? i + e - lane : lane - i - e;
-                d[e] = k >= 0 ? both * pw[max(k, 0)] : 0.f;
+                        for (int j = 0; j < 2; ++j) {
+                            float v[32];
+                            tc::tmem_ld32(tl + C_O + 64 * h + 32 * j, v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[j][i] = pack2(v[2 * i], v[2 * i + 1]);
+                        }
+                        if (h == 1) warp_arrive(&bar[B_OFREE], lane);
+                        else if (d > 0 && !wait(B_STORED, d - 1)) break;
+                        tc::st_sw128(ot + h * (TILE / 2), row, 0, o[0]);
+                        tc::st_sw128(ot + h * (TILE / 2), row, 32, o[1]);
+                    }
+                    if (!ok) break;
+                    tc::fence_async_smem();
+                } else {
+                    const int even = row & ~1;
+                    const size_t off = (size_t(g.t0 + LC * place(d) + row) * a.H + hd) * D, ld = size_t(a.H) * D;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        float v[32];
+                        tc::tmem_ld32(tl + C_O + 32 * j, v);
+                        if (p.out_fp32) {
+                            tc::st_rows_paired_f32<32>(static_cast<float*>(p.out) + off + 32 * j, ld, v, lane, even < n, even + 1 < n);
+                        } else {
+                            uint4 x[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
+                                                  pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
+                            tc::st_rows_paired<4>(reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off + 32 * j),
+                                                  ld / 2, x, lane, even < n, even + 1 < n);
+                        }
+                    }
+                    warp_arrive(&bar[B_OFREE], lane);
+                    if (d > 0 && !wait(B_STORED, d - 1)) break;
+                }
+                warp_arrive(&bar[B_STAGED], lane);
             }
-            near[i / 2] = pk2(u[0], u[1]);
-            diag[i / 2] = pk2(d[0], d[1]);
-        }
-        for (int c = 0; c < nc; ++c) {
+            if (c == nc) break;
             const int n = tokens(c);
             if (!wait(B_P, c)) break;
             // a block is read, scaled and written back packed, into columns that were read before
@@ -351,19 +406,17 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                     float v[32];
                     tc::tmem_ld32(tl + C_P + 32 * j, v);
                     if (j != q) {
-                        const float e = pw[back ? 32 * j - row : row - 32 * j - 31];
-                        const f2 e2 = pk2(e, e);
+                        const int k = back ? j - 1 : j;
+                        const float ej = k == 0 ? e[0] : k == 1 ? e[1] : e[2];
+                        const f2 e2 = pk2(ej, ej);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const f2 y = mul2(pk2(v[2 * i], v[2 * i + 1]), mul2(near[i], e2));
+                            const f2 y = mul2(pk2(v[2 * i], v[2 * i + 1]), mul2(*reinterpret_cast<const f2*>(fn + 2 * i), e2));
                             up2(y, v[2 * i], v[2 * i + 1]);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const f2 y = mul2(pk2(v[2 * i], v[2 * i + 1]), diag[i]);
-                            up2(y, v[2 * i], v[2 * i + 1]);
-                        }
+                        for (int i = 0; i < 32; ++i) v[i] *= fr[-i];
                     }
                     if (n < LC)  // (a growing state's factors may be infinite there)
 #pragma unroll
@@ -378,77 +431,39 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 tmem_st16u(tl + C_P + 16 * j, o);
             }
             tmem_wait_st();
-            const float f = p.by * decay(slope, back ? max(n - 1 - row, 0) : row + 1);
+            warp_arrive(&bar[B_B], lane);
+        }
+    } else if (w < 16) {
+        // ---- C: the state as an operand, its decay; Query X's rows ----
+        unsigned char* xt = sm + W_X;
+        for (int c = 0; c < nc; ++c) {
+            const int n = tokens(c);
+            const float fx = decay(slope, n), fo = p.by * decay(slope, back ? max(n - 1 - row, 0) : row + 1);
+            if (!(c > 0 ? wait(B_S, c - 1) : wait(B_X0, 0))) break;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                float v[32];
+                tc::tmem_ld32(tl + C_X + 32 * j, v);
+                uint32_t b[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
+                tc::st_sw128(xt + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= fx;
+                tc::tmem_st32(tl + C_X + 32 * j, v);
+            }
+            tc::fence_async_smem();
+            warp_arrive(&bar[B_C], lane);
             if (!wait(B_QX, c)) break;
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
                 float v[32];
                 tc::tmem_ld32(tl + C_O + 32 * j, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= f;
+                for (int i = 0; i < 32; ++i) v[i] *= fo;
                 tc::tmem_st32(tl + C_O + 32 * j, v);
             }
-            warp_arrive(&bar[B_B], lane);
-        }
-    } else if (w < 12) {
-        // ---- C: the state as an operand, its decay; the output ----
-        unsigned char* xt = sm + W_X;
-        for (int c = 0; c <= nc; ++c) {
-            if (c < nc) {
-                const float f = decay(slope, tokens(c));
-                if (!(c > 0 ? wait(B_S, c - 1) : wait(B_X0, 0))) break;
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    float v[32];
-                    tc::tmem_ld32(tl + C_X + 32 * j, v);
-                    uint32_t b[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
-                    tc::st_sw128(xt + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= f;
-                    tc::tmem_st32(tl + C_X + 32 * j, v);
-                }
-                tc::fence_async_smem();
-                warp_arrive(&bar[B_C], lane);
-            }
-            if (c == 0) continue;
-            const int d = c - 1;  // the chunk whose output is ready
-            if (!wait(B_O, d)) break;
-            if (staged(d)) {
-                unsigned char* ot = tile(d, 2);
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    float v[32];
-                    tc::tmem_ld32(tl + C_O + 32 * j, v);
-                    uint32_t b[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) b[i] = pack2(v[2 * i], v[2 * i + 1]);
-                    tc::st_sw128(ot + (j >> 1) * (TILE / 2), row, 32 * (j & 1), b);
-                }
-                tc::fence_async_smem();
-            } else {
-                const int n = tokens(d), even = row & ~1;
-                const size_t off = (size_t(g.t0 + LC * place(d) + row) * a.H + hd) * D, ld = size_t(a.H) * D;
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    float v[32];
-                    tc::tmem_ld32(tl + C_O + 32 * j, v);
-                    if (p.out_fp32) {
-                        tc::st_rows_paired_f32<32>(static_cast<float*>(p.out) + off + 32 * j, ld, v, lane, even < n, even + 1 < n);
-                    } else {
-                        uint4 x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
-                                              pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
-                        tc::st_rows_paired<4>(reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off + 32 * j),
-                                              ld / 2, x, lane, even < n, even + 1 < n);
-                    }
-                }
-            }
-            warp_arrive(&bar[B_OFREE], lane);
-            if (lane == 0) mbar_arrive(&bar[B_STAGED + (d & 1)]);
+            warp_arrive(&bar[B_SCALED], lane);
         }
         if (x1 && wait(B_S, nc - 1)) {
 #pragma unroll 1
@@ -465,72 +480,48 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 }
             }
         }
-    } else if (w == 12) {
-        // ---- loads, two chunks ahead as their tiles are spent; the output's stores ----
-        const CUtensorMap *mq = &tm.m[p.query], *mk = &tm.m[p.key], *mv = &tm.m[p.value], *mo = &tm.m[p.store];
-        auto load = [&](int c, int which, const CUtensorMap* m, int share) {
-            uint64_t* b = &bar[(which == 2 ? B_V : B_QK) + (c & 1)];
+    } else if (w == 16) {
+        // ---- loads ----
+        int i = 0;
+        for (; i < 3 * nc; ++i) {
+            const int b = i % W_TILES, c = i / 3, which = i - 3 * c;
+            if (i >= W_TILES && !wait(B_FREE + b, i / W_TILES - 1)) break;
             if (elect()) {
-                tc::mbar_expect_tx(b, TILE);
-                tc::tma4(tile(c, which), m, 0, g.t0 + LC * place(c), 0, hd / share, b);
+                tc::mbar_expect_tx(&bar[B_FULL + b], TILE);
+                tc::tma4(tile(i), &tm.m[which == 0 ? p.query : which == 1 ? p.key : p.value], 0, g.t0 + LC * place(c), 0,
+                         hd / (which == 0 ? p.rq : which == 1 ? p.rk : p.rv), &bar[B_FULL + b]);
             }
             __syncwarp();
-        };
-        int lq = 0, lv = 0;  // chunks whose rows are on their way or here
-        for (int c = -2; c < nc; ++c) {
-            const int s = c & 1, ahead = c + 2;
-            const bool more = ahead < nc;
-            if (more) {
-                if (c >= 0 && !wait(B_QFREE + s, c >> 1)) break;
-                load(ahead, 0, mq, p.rq);
-                if (c >= 0 && !wait(B_KFREE + s, c >> 1)) break;
-                load(ahead, 1, mk, p.rk);
-                lq = ahead + 1;
-            }
-            if (c >= 0) {
-                if (!wait(B_STAGED + s, c >> 1)) break;
-                if (staged(c) && elect()) {
-                    tma_store4(mo, 0, g.t0 + LC * place(c), 0, hd, tile(c, 2));
-                    tc::bulk_commit();
-                    tc::bulk_wait_read0();
-                }
-                __syncwarp();
-            }
-            if (more) {
-                load(ahead, 2, mv, p.rv);
-                lv = ahead + 1;
-            }
         }
-        if (elect()) tc::bulk_wait0();
-        __syncwarp();
-        if (!ok) {  // every copy has landed before the block ends
-            for (int c = max(lq - 2, 0); c < lq; ++c) tc::mbar_wait(&bar[B_QK + (c & 1)], (c >> 1) & 1, 100000000ull);
-            for (int c = max(lv - 2, 0); c < lv; ++c) tc::mbar_wait(&bar[B_V + (c & 1)], (c >> 1) & 1, 100000000ull);
-        }
-    } else {
+        if (!ok)  // every copy has landed before the block ends
+            for (int k = max(i - W_TILES, 0); k < i; ++k) tc::mbar_wait(&bar[B_FULL + k % W_TILES], (k / W_TILES) & 1, 100000000ull);
+    } else if (w == 17) {
         // ---- products ----
         const uint32_t ID = tc::idesc_bf16(128, 128, false, false), IDt = tc::idesc_bf16(128, 128, false, true);
         const uint64_t dX = tc::sdesc(smem_u32(sm + W_X), 16, 1024);
         auto kstep = [](int s) { return uint64_t(((s >> 2) * int(TILE / 2) + (s & 3) * 32) >> 4); };  // along the channels
         auto tstep = [](int s) { return uint64_t((s * 2048) >> 4); };                                 // along the tokens
+        auto spent = [&](int i) { tc::mma_commit(&bar[B_FREE + i % W_TILES]); };
         for (int c = -1; c < nc; ++c) {
             if (c >= 0) {
                 if (!wait(B_C, c) || (c > 0 && !wait(B_OFREE, c - 1))) break;
                 if (elect()) {
-                    const uint64_t dq = tc::sdesc(smem_u32(tile(c, 0)), 16, 1024);
+                    const uint64_t dq = tc::sdesc(smem_u32(tile(3 * c)), 16, 1024);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) tc::mma(tbase + C_O, dq + kstep(s), dX + kstep(s), ID, s > 0);
                     tc::mma_commit(&bar[B_QX]);
-                    tc::mma_commit(&bar[B_QFREE + (c & 1)]);
+                    spent(3 * c);
                 }
                 __syncwarp();
                 if (adds(c)) {
-                    for (int q = 4 * c; q < 4 * c + 4; ++q) {
-                        if (!wait(B_A + (q & 1), q >> 1)) break;
+                    const uint64_t dk = tc::sdesc(smem_u32(tile(3 * c + 1)), TILE / 2, 1024);
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) {
+                        const int b = i % W_PIECES;
+                        if (!wait(B_A + b, c * (PIECES / W_PIECES) + i / W_PIECES)) break;
                         if (elect()) {
-                            quarter_products(tbase + C_X, tbase + C_V + PLANES * (q & 1),
-                                             tc::sdesc(smem_u32(tile(c, 1)), TILE / 2, 1024), q & 3, IDt, false);
-                            tc::mma_commit(&bar[B_AFREE + (q & 1)]);
+                            piece_products(tbase + C_X, tbase + C_V + PLANES * b, dk, i, IDt, false);
+                            tc::mma_commit(&bar[B_AFREE + b]);
                         }
                         __syncwarp();
                     }
@@ -538,22 +529,23 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                     if (elect()) tc::mma_commit(&bar[B_S]);
                     __syncwarp();
                 }
-                if (!wait(B_V + (c & 1), c >> 1) || !wait(B_B, c)) break;
+                if (!landed(3 * c + 2) || !wait(B_B, c) || !wait(B_SCALED, c)) break;
                 if (elect()) {
-                    const uint64_t dv = tc::sdesc(smem_u32(tile(c, 2)), TILE / 2, 1024);
-                    tc::mma_commit(&bar[B_KFREE + (c & 1)]);
+                    const uint64_t dv = tc::sdesc(smem_u32(tile(3 * c + 2)), TILE / 2, 1024);
+                    spent(3 * c + 1);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) mma_ta(tbase + C_O, tbase + C_P + 8 * s, dv + tstep(s), IDt, 1u);
+                    spent(3 * c + 2);
                     tc::mma_commit(&bar[B_O]);
                 }
                 __syncwarp();
             }
             if (c + 1 < nc) {
                 const int d = c + 1;
-                if (!wait(B_QK + (d & 1), d >> 1)) break;
+                if (!landed(3 * d) || !landed(3 * d + 1)) break;
                 if (tokens(d) < LC && !wait(B_FIX, 0)) break;
                 if (elect()) {
-                    const uint64_t dq = tc::sdesc(smem_u32(tile(d, 0)), 16, 1024), dk = tc::sdesc(smem_u32(tile(d, 1)), 16, 1024);
+                    const uint64_t dq = tc::sdesc(smem_u32(tile(3 * d)), 16, 1024), dk = tc::sdesc(smem_u32(tile(3 * d + 1)), 16, 1024);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) tc::mma(tbase + C_P, dq + kstep(s), dk + kstep(s), ID, s > 0);
                     tc::mma_commit(&bar[B_P]);
@@ -562,6 +554,21 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
             }
         }
         if (!ok && elect()) tc::drain_mmas(&bar[B_SPARE], 100000000ull);
+    } else {
+        // ---- stores ----
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(B_STAGED, c)) break;
+            if (elect()) {
+                if (staged(c)) {
+                    tma_store4(&tm.m[p.store], 0, g.t0 + LC * place(c), 0, hd, sm + W_OUT);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read0();
+                }
+                mbar_arrive(&bar[B_STORED]);
+            }
+            __syncwarp();
+        }
+        if (elect()) tc::bulk_wait0();
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -572,9 +579,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
 
 // ---- what a segment adds to the state ----
 
-constexpr int STATE_THREADS = 320;  // two groups of four warps take the quarters in turn; loads: warp 8, products: 9
+constexpr int STATE_THREADS = 320;  // two groups of four warps take the pieces in turn; loads: warp 8, products: 9
 constexpr int S_STAGES = 3;
-constexpr int S_BUFS = 4;           // quarters of split values in tensor memory
+constexpr int S_BUFS = PIECES;      // pieces of split values in tensor memory: a chunk's
 constexpr int S_TAB = S_STAGES * 2 * int(TILE);
 constexpr int S_BAR = S_TAB + 128 * 4;
 constexpr size_t STATE_SMEM = S_BAR + 256 + 1024;
@@ -625,7 +632,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
         tc::fence_after_sync();
         return ok;
     };
-    constexpr uint32_t C_V = 128;  // columns: state 0, then the quarters of split values
+    constexpr uint32_t C_V = 128;  // columns: state 0, then the pieces of split values
 
     if (w < 8) {
         const int grp = w >> 2;
@@ -643,12 +650,10 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
             }
             // forwards only full chunks come here (the last segment adds to nothing)
             const float all = decay(slope, back ? LC * c : g.len - LC * (c + 1));
-#pragma unroll 1
-            for (int q = 4 * c + grp; q < 4 * c + 4; q += 2) {
-                const int b = q % S_BUFS;
-                if (q >= S_BUFS && !wait(SB_FREE + b, q / S_BUFS - 1)) break;
-                split_quarter(tile(c, 1), q & 3, w, lane, fs, all, tl + C_V + PLANES * b);
-                warp_arrive(&bar[SB_READY + b], lane);
+            for (int i = grp; i < PIECES; i += 2) {
+                if (c > 0 && !wait(SB_FREE + i, c - 1)) break;
+                split_piece(tile(c, 1), i, w, lane, fs, all, tl + C_V + PLANES * i);
+                warp_arrive(&bar[SB_READY + i], lane);
             }
             if (!ok) break;
         }
@@ -680,16 +685,20 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
                 tc::mbar_wait(&bar[SB_FULL + c % S_STAGES], (c / S_STAGES) & 1, 100000000ull);
     } else {
         const uint32_t IDt = tc::idesc_bf16(128, 128, false, true);
-        for (int q = 0; q < 4 * nc; ++q) {
-            const int c = q >> 2, b = q % S_BUFS;
-            if (!wait(SB_READY + b, q / S_BUFS)) break;
-            if (elect()) {
-                quarter_products(tbase, tbase + C_V + PLANES * b, tc::sdesc(smem_u32(tile(c, 0)), TILE / 2, 1024), q & 3, IDt, q == 0);
-                tc::mma_commit(&bar[SB_FREE + b]);
-                if ((q & 3) == 3) tc::mma_commit(&bar[SB_EMPTY + c % S_STAGES]);
-                if (q == 4 * nc - 1) tc::mma_commit(&bar[SB_DONE]);
+        for (int c = 0; c < nc; ++c) {
+            const uint64_t dk = tc::sdesc(smem_u32(tile(c, 0)), TILE / 2, 1024);
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                if (!wait(SB_READY + i, c)) break;
+                if (elect()) {
+                    piece_products(tbase, tbase + C_V + PLANES * i, dk, i, IDt, c == 0 && i == 0);
+                    tc::mma_commit(&bar[SB_FREE + i]);
+                    if (i == PIECES - 1) tc::mma_commit(&bar[SB_EMPTY + c % S_STAGES]);
+                    if (i == PIECES - 1 && c == nc - 1) tc::mma_commit(&bar[SB_DONE]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
         if (!ok && elect()) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
     }

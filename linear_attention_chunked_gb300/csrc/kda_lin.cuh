@@ -32,8 +32,11 @@ struct LinPass {
 constexpr int LC = 128;  // tokens of a chunk
 
 
-// Documents are cut into segments of `seg` tokens (the last one shorter; an empty document has one empty
-// segment), which are walked side by side.  The state between two segments of a document lies in a slot.
+// With few heads, documents longer than LIN_WHOLE tokens are cut into segments of `seg` tokens (the last one shorter),
+// which are walked side by side; the others are one segment.  The state between two segments of a document lies in a
+// slot.
+constexpr int LIN_WHOLE = 2048;
+
 struct LinPlan {
     int4* tab;     // per segment: {document, first token, length | first << 16 | last << 17, w}: w is the slot behind
                    // the segment, w - 1 the one in front of it
@@ -45,7 +48,7 @@ struct LinArgs {
     int64_t T;
     int N, H;
     int seg;               // tokens of a segment
-    int direct;            // no document is longer than a segment: segment n is document n, no plan
+    int direct;            // no document is cut: no plan
     const int* cu;
     const float* slope;
     int* status;

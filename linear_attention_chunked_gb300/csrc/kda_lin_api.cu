@@ -48,13 +48,21 @@ EncodeTiledFn encode_tiled() {
     return fn;
 }
 
-// Tokens of a segment, a power of two that depends on the heads alone: a document's results must not depend on the
-// pack, and a document alone has to fill the machine.  Up to 16 heads the segments of 16384 tokens are 128 blocks, one
-// wave; the states between segments cost a second pass over two of the rows (50% more reads of a forward) and 64 KB each.
+// Whether long documents are cut into segments, and the tokens of one (a power of two).  This depends on the heads
+// alone: a document's results must not depend on the pack.  A walk takes 2.3 us a chunk where it has its multiprocessor
+// and HBM to itself, so a document of 16384 tokens takes 0.29 ms uncut; cut, its states between segments cost a second
+// pass over two of the rows: at 64 heads 0.34 ms in all, at 16 heads 0.11.  A backward walks three times as many heads.
+// Segments of 2048 tokens make a wave of blocks of 16384 tokens and 16 heads; fewer heads take shorter ones.
+bool cuts(int H, bool back) { return H < (back ? 24 : 64); }
 int segment(int H) {
     int s = 512;
-    while (s < 128 * H && s < 2048) s *= 2;
+    while (s < 128 * H && s < LIN_WHOLE) s *= 2;
     return s;
+}
+// Segments that a document set may have, and slots between them
+int64_t max_segments(const kda_linattn_problem* p) { return p->T / segment(p->H) + p->N; }
+size_t slot_bytes(const kda_linattn_problem* p, bool back) {
+    return cuts(p->H, back) && p->T > LIN_WHOLE ? size_t(p->T / segment(p->H)) * size_t(p->H) * D * D * 4 : 0;
 }
 
 kda_status check_sizes(const kda_linattn_problem* p) {
@@ -74,8 +82,7 @@ kda_status check_problem(const kda_linattn_problem* p) {
     if (kda_status s = check_sizes(p)) return s;
     if (!p->cu_seqlens || !al(p->cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
     // one-dimensional grids
-    const int64_t segs = p->T / segment(p->H) + p->N;
-    if (segs * p->H > INT32_MAX / 16 || p->T * p->Hk / 8 >= INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (max_segments(p) * p->H > INT32_MAX / 16 || p->T * p->Hk / 8 >= INT32_MAX) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -89,36 +96,34 @@ Regions regions(const kda_linattn_problem* p) {
     Regions r{};
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
-    const size_t seg = size_t(segment(p->H)), multi = size_t(p->T) / seg;
-    const size_t slots = multi * size_t(p->H) * D * D * 4;
     r.status = take(256);
     r.counts = take(2 * sizeof(int));
-    r.tab = take((multi + size_t(p->N)) * sizeof(int4));
-    r.multi = take(multi * sizeof(int4));
-    const size_t plan = o;
-    r.front = take(slots);
+    r.tab = take(size_t(max_segments(p)) * sizeof(int4));
+    r.multi = take(size_t(p->T / LIN_WHOLE) * sizeof(int4));
+    const size_t plan = o, kept = slot_bytes(p, true);  // the backward reads the forward's slots where it cuts
+    r.front = take(slot_bytes(p, false));
     r.fwd = o;
     o = plan;
-    r.back = take(slots);
+    r.back = take(kept);
     if (p->Hk < p->H) {  // each head's part of dq and dk
         r.share_q = take(size_t(p->T) * p->H * D * 4);
         r.share_k = take(size_t(p->T) * p->H * D * 4);
     }
     r.bwd_saved = o;
-    r.bwd_replay = o + slots;
+    r.bwd_replay = o + kept;
     r.kept = 256;
-    r.saved = 256 + slots;
+    r.saved = 256 + kept;
     return r;
 }
 
-LinArgs make_args(const kda_linattn_problem* p, const Regions& r, const float* slope, void* ws) {
+LinArgs make_args(const kda_linattn_problem* p, const Regions& r, bool back, const float* slope, void* ws) {
     LinArgs a{};
     char* w = static_cast<char*>(ws);
     a.T = p->T;
     a.N = p->N;
     a.H = p->H;
     a.seg = segment(p->H);
-    a.direct = p->T <= a.seg;
+    a.direct = !cuts(p->H, back) || p->T <= LIN_WHOLE;
     a.cu = p->cu_seqlens;
     a.slope = slope;
     a.status = static_cast<int*>(ws);
@@ -207,12 +212,13 @@ kda_status kda_linattn_fwd(const kda_linattn_problem* p, const void* q, const vo
     if (ws_bytes < r.fwd) return KDA_ERR_WORKSPACE;
     if (kda_status s = setup_lin()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    LinArgs a = make_args(p, r, slope, ws);
+    LinArgs a = make_args(p, r, false, slope, ws);
     LinMaps tm{};
     const Rows rows[7] = {{q, p->Hk, p->ld_q}, {k, p->Hk, p->ld_k}, {v, p->H, p->ld_v}, {}, {o, p->H, 0}};
     if (kda_status s = make_maps(p->T, rows, &tm)) return s;
     a.made_for = static_cast<int4*>(saved);
-    a.front = reinterpret_cast<float*>(saved ? static_cast<char*>(saved) + r.kept : static_cast<char*>(ws) + r.front);
+    a.front = reinterpret_cast<float*>(saved && cuts(p->H, true) ? static_cast<char*>(saved) + r.kept
+                                                                 : static_cast<char*>(ws) + r.front);
     a.passes = 1;
     a.pass[0] = make_pass(IN_Q, IN_K, IN_V, p->H / p->Hk, OUT_O, o, 0, h0, ht, 0, 0, 1.f, p->scale);
     if (a.direct) {
@@ -237,7 +243,7 @@ kda_status kda_linattn_bwd(const kda_linattn_problem* p, const void* q, const vo
     if (ws_bytes < (saved ? r.bwd_saved : r.bwd_replay)) return KDA_ERR_WORKSPACE;
     if (kda_status s = setup_lin()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    LinArgs a = make_args(p, r, slope, ws);
+    LinArgs a = make_args(p, r, true, slope, ws);
     LinMaps tm{};
     char* w = static_cast<char*>(ws);
     const int share = p->H / p->Hk, part = share > 1;

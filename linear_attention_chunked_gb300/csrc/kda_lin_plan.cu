@@ -21,8 +21,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_lin_plan(LinArgs a) {
     for (int n = n0; n < n1; ++n) {
         const long long len = (long long)a.cu[n + 1] - a.cu[n];
         bad |= len < 0;
-        segs += len > L ? (len + L - 1) / L : 1;
-        muls += len > L;
+        segs += len > LIN_WHOLE ? (len + L - 1) / L : 1;
+        muls += len > LIN_WHOLE;
     }
     if (tid == 0) {
         bad |= a.cu[0] != 0 || int64_t(a.cu[a.N]) != a.T;
@@ -53,11 +53,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_lin_plan(LinArgs a) {
     }
     if (bad) return;
     for (int n = n0; n < n1; ++n) {
-        const int at = a.cu[n], len = a.cu[n + 1] - at, k = len > L ? (len + L - 1) / L : 1;
+        const int at = a.cu[n], len = a.cu[n + 1] - at, k = len > LIN_WHOLE ? (len + L - 1) / L : 1, l = k > 1 ? L : len;
         const int base = int(s) - n;  // slots in front: one less than its segments for every document
         if (k > 1) a.plan.multi[m++] = make_int4(n, base, k, len);
         for (int j = 0; j < k; ++j)
-            a.plan.tab[s + j] = make_int4(n, at + j * L, min(L, len - j * L) | (j == 0) << 16 | (j == k - 1) << 17, base + j);
+            a.plan.tab[s + j] = make_int4(n, at + j * l, min(l, len - j * l) | (j == 0) << 16 | (j == k - 1) << 17, base + j);
         s += k;
     }
 }
@@ -104,8 +104,8 @@ void launch_lin_plan(const LinArgs& a, cudaStream_t st) {
 void launch_lin_carry(const LinArgs& a, int pass, cudaStream_t st) {
     const LinPass& p = a.pass[pass];
     ProfScope ps(KK_LIN_CARRY, st);
-    // at most T / seg documents are longer than a segment
-    k_lin_carry<<<unsigned(a.T / a.seg) * unsigned(a.H) * (D * D / 1024), 256, 0, st>>>(a, p.back, p.s0,
+    // at most T / LIN_WHOLE documents have more than one segment
+    k_lin_carry<<<unsigned(a.T / LIN_WHOLE) * unsigned(a.H) * (D * D / 1024), 256, 0, st>>>(a, p.back, p.s0,
                                                                                    p.back ? a.back : a.front);
 }
 
