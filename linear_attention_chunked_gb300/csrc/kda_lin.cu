@@ -101,12 +101,13 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int n, int tid) 
     }
 }
 
-// A piece (16 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into three bf16
-// planes as the left operand of a product in tensor memory: lane = channel, token pairs in the columns taddr.. of
-// hi, mid and lo, 8 each.  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
+// A piece (16 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into bf16 planes
+// as the left operand of a product in tensor memory: lane = channel, token pairs in the columns taddr.. of hi, mid and
+// lo, 8 each.  Three planes are cut off (8 bits each: exact), two are rounded (off by 2^-18 at most, 2.5e-6 in the 2-norm).  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
 // the pairs that a 16-lane store takes.
 constexpr int PIECES = LC / 16;
 constexpr uint32_t PLANES = 24;  // columns of a piece
+template <int N>
 __device__ __forceinline__ void split_piece(const unsigned char* tile, int piece, int w, int lane, const float* f, float all,
                                             uint32_t taddr) {
     const int m = lane >> 3, r = lane & 7;
@@ -120,36 +121,41 @@ __device__ __forceinline__ void split_piece(const unsigned char* tile, int piece
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         fw[i] = mul2(*reinterpret_cast<const f2*>(f + 16 * piece + 8 * i + 2 * (lane & 3)), all2);
-    constexpr uint32_t mask = 0xffff0000u, flip = 0x80000000u;
+    constexpr uint32_t mask = 0xffff0000u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 channels
         uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const f2 y = mul2(fw[j >> 1], pk2(__uint_as_float(x[h][j] << 16), __uint_as_float(x[h][j] & mask)));
+            const f2 minus = pk2(-1.f, -1.f);
             float y0, y1, r0, r1;
             up2(y, y0, y1);
-            hi[j] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
-            const f2 rest = add2(y, pk2(__uint_as_float((__float_as_uint(y0) & mask) ^ flip),
-                                        __uint_as_float((__float_as_uint(y1) & mask) ^ flip)));
-            up2(rest, r0, r1);
-            mid[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-            const f2 last = add2(rest, pk2(__uint_as_float((__float_as_uint(r0) & mask) ^ flip),
-                                           __uint_as_float((__float_as_uint(r1) & mask) ^ flip)));
-            up2(last, r0, r1);
-            lo[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            if (N == 2) {
+                hi[j] = pack2(y0, y1);
+                up2(fma2(pk2(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & mask)), minus, y), r0, r1);
+                mid[j] = pack2(r0, r1);
+            } else {
+                hi[j] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
+                const f2 rest = fma2(pk2(__uint_as_float(__float_as_uint(y0) & mask), __uint_as_float(__float_as_uint(y1) & mask)), minus, y);
+                up2(rest, r0, r1);
+                mid[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+                up2(fma2(pk2(__uint_as_float(__float_as_uint(r0) & mask), __uint_as_float(__float_as_uint(r1) & mask)), minus, rest), r0, r1);
+                lo[j] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            }
         }
         const uint32_t at = taddr + (uint32_t(16 * h) << 16);
         tmem_st_16x8(at, hi);
         tmem_st_16x8(at + 8, mid);
-        tmem_st_16x8(at + 16, lo);
+        if (N == 3) tmem_st_16x8(at + 16, lo);
     }
     tmem_wait_st();
 }
 // The products of a piece: D += planes * rows 16 piece.. of the key tile, read across
-__device__ __forceinline__ void piece_products(uint32_t d, uint32_t planes, uint64_t key, int piece, uint32_t idesc, bool first) {
+__device__ __forceinline__ void piece_products(uint32_t d, uint32_t planes, uint64_t key, int piece, uint32_t idesc, bool first,
+                                               bool three) {
     const uint64_t b = key + uint64_t((piece * 2048) >> 4);
-    mma_ta(d, planes + 16, b, idesc, !first);
+    if (three) mma_ta(d, planes + 16, b, idesc, !first);
     mma_ta(d, planes + 8, b, idesc, 1u);
     mma_ta(d, planes, b, idesc, 1u);
 }
@@ -282,6 +288,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     auto tile = [&](int i) { return sm + (i % W_TILES) * TILE; };  // tile 3 c: Query of chunk c, then Key, Value
     // whether chunk c's values still reach a state that is read; whether its output leaves by TMA
     auto adds = [&](int c) { return c + 1 < nc || x1; };
+    // The state that a document ends in is an fp32 output: the values that still weigh more than 1/32 in it are split into three
+    // planes, exactly; those before them, and a state that only bf16 rows are made of, get two.
+    auto three = [&](int c) {
+        const int beyond = back ? LC * place(c) : max(g.len - LC * (c + 1), 0);  // tokens that the walk still meets
+        return x1 && (beyond == 0 || slope * float(beyond) > -3.5f);
+    };
     auto staged = [&](int c) { return !p.out_fp32 && tokens(c) == LC; };
     // Waits for the turn-th completion of barrier b.  The lanes of a warp leave together (a wait that runs out of
     // time ends the warp's part; every other wait runs out too, and the block reports and ends).
@@ -332,10 +344,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
             }
             if (!adds(c)) break;
             const float* f = n < LC ? fshort : fs;
+            const bool exact = three(c);
             for (int i = PIECES * c + (w >> 2); i < PIECES * (c + 1); i += 2) {
                 const int b = i % W_PIECES;
                 if (i >= W_PIECES && !wait(B_AFREE + b, i / W_PIECES - 1)) break;
-                split_piece(tile(3 * c + 2), i % PIECES, w, lane, f, 1.f, tl + C_V + PLANES * b);
+                if (exact) split_piece<3>(tile(3 * c + 2), i % PIECES, w, lane, f, 1.f, tl + C_V + PLANES * b);
+                else split_piece<2>(tile(3 * c + 2), i % PIECES, w, lane, f, 1.f, tl + C_V + PLANES * b);
                 warp_arrive(&bar[B_A + b], lane);
             }
             if (!ok) break;
@@ -515,12 +529,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 __syncwarp();
                 if (adds(c)) {
                     const uint64_t dk = tc::sdesc(smem_u32(tile(3 * c + 1)), TILE / 2, 1024);
+                    const bool exact = three(c);
 #pragma unroll
                     for (int i = 0; i < PIECES; ++i) {
                         const int b = i % W_PIECES;
                         if (!wait(B_A + b, c * (PIECES / W_PIECES) + i / W_PIECES)) break;
                         if (elect()) {
-                            piece_products(tbase + C_X, tbase + C_V + PLANES * b, dk, i, IDt, false);
+                            piece_products(tbase + C_X, tbase + C_V + PLANES * b, dk, i, IDt, false, exact);
                             tc::mma_commit(&bar[B_AFREE + b]);
                         }
                         __syncwarp();
@@ -652,7 +667,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
             const float all = decay(slope, back ? LC * c : g.len - LC * (c + 1));
             for (int i = grp; i < PIECES; i += 2) {
                 if (c > 0 && !wait(SB_FREE + i, c - 1)) break;
-                split_piece(tile(c, 1), i, w, lane, fs, all, tl + C_V + PLANES * i);
+                split_piece<3>(tile(c, 1), i, w, lane, fs, all, tl + C_V + PLANES * i);
                 warp_arrive(&bar[SB_READY + i], lane);
             }
             if (!ok) break;
@@ -691,7 +706,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
             for (int i = 0; i < PIECES; ++i) {
                 if (!wait(SB_READY + i, c)) break;
                 if (elect()) {
-                    piece_products(tbase, tbase + C_V + PLANES * i, dk, i, IDt, c == 0 && i == 0);
+                    piece_products(tbase, tbase + C_V + PLANES * i, dk, i, IDt, c == 0 && i == 0, true);
                     tc::mma_commit(&bar[SB_FREE + i]);
                     if (i == PIECES - 1) tc::mma_commit(&bar[SB_EMPTY + c % S_STAGES]);
                     if (i == PIECES - 1 && c == nc - 1) tc::mma_commit(&bar[SB_DONE]);
