@@ -78,19 +78,30 @@ __device__ __forceinline__ void tma_store4(const CUtensorMap* map, int x, int y,
                  : "memory");
 }
 
-// tc::mbar_wait with its polling out of line: a role's code has to stay in the instruction cache beside the others'
-__device__ __noinline__ bool poll(uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity); }
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity) {
-    return tc::mbar_try_wait(bar, parity) || poll(bar, parity);
+// Waits for the phase of the given parity; false if it has not come after WAIT_TRIES suspensions of some 7800 clocks
+// each: about a second.  The loop has no instruction but its own and reads no clock: a chunk's chain of hand-overs pays
+// for every one, and the roles' code has to share the instruction cache (with the clock read here the walk takes 8% longer).
+constexpr uint32_t WAIT_TRIES = 250000;
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+        "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " @p bra D%=;\n add.u32 n, n, 1;\n setp.lt.u32 p, n, %3;\n @p bra W%=;\n setp.ne.u32 p, 0, 0;\n"
+        "D%=: selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "n"(WAIT_TRIES)
+        : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // One arrival for a warp whose lanes have all finished their part
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
+    asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane) : "memory");
 }
 
 // 128-byte-swizzled tile pair [2 blocks of 64 channels][128 tokens][128 bytes]: clears the rows from n on.  128 threads.
@@ -247,6 +258,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         return;
     }
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + W_BAR);
+    const uint32_t sbar = smem_u32(bar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + W_BAR + 8 * B_END);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + W_BAR + 8 * B_END + 4);
     float* fs = reinterpret_cast<float*>(sm + W_TAB);  // a full chunk's state factors
@@ -295,13 +307,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         return x1 && (beyond == 0 || slope * float(beyond) > -3.5f);
     };
     auto staged = [&](int c) { return !p.out_fp32 && tokens(c) == LC; };
-    // Waits for the turn-th completion of barrier b.  The lanes of a warp leave together (a wait that runs out of
-    // time ends the warp's part; every other wait runs out too, and the block reports and ends).
+    // Waits for the turn-th completion of barrier b.  A wait that runs out of tries ends the warp's part; every other
+    // wait runs out too, and the block reports and ends.
     bool ok = true;
     auto wait = [&](int b, int turn) {
-        const bool done = ok && bounded_wait(&bar[b], uint32_t(turn) & 1u);
-        ok = __all_sync(0xffffffffu, done);
-        if (!ok) *abort_flag = 1;
+        ok = ok && bounded_wait(sbar + 8 * b, uint32_t(turn) & 1u);
+        __syncwarp();
         tc::fence_after_sync();
         return ok;
     };
@@ -324,10 +335,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         tc::tmem_st32(tl + C_X + 32 * j, v);
     };
     auto landed = [&](int i) { return wait(B_FULL + i % W_TILES, i / W_TILES); };
+    auto arrive = [&](int b) { warp_arrive(sbar + 8 * b, lane); };
     // the groups share the blocks
     if (w < 16) {
         start_block(w >> 2);
-        if (w < 12) warp_arrive(&bar[B_X0], lane);
+        if (w < 12) arrive(B_X0);
     }
 
     if (w < 8) {
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 if (!landed(3 * c + 1)) break;
                 clear_rows(tile(3 * c + 1 + (w >> 2)), n, tid & 127);
                 tc::fence_async_smem();
-                warp_arrive(&bar[B_FIX], lane);
+                arrive(B_FIX);
                 if (!wait(B_FIX, 0)) break;
             }
             if (!adds(c)) break;
@@ -350,7 +362,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 if (i >= W_PIECES && !wait(B_AFREE + b, i / W_PIECES - 1)) break;
                 if (exact) split_piece<3>(tile(3 * c + 2), i % PIECES, w, lane, f, 1.f, tl + C_V + PLANES * b);
                 else split_piece<2>(tile(3 * c + 2), i % PIECES, w, lane, f, 1.f, tl + C_V + PLANES * b);
-                warp_arrive(&bar[B_A + b], lane);
+                arrive(B_A + b);
             }
             if (!ok) break;
         }
@@ -378,7 +390,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[j][i] = pack2(v[2 * i], v[2 * i + 1]);
                         }
-                        if (h == 1) warp_arrive(&bar[B_OFREE], lane);
+                        if (h == 1) arrive(B_OFREE);
                         else if (d > 0 && !wait(B_STORED, d - 1)) break;
                         tc::st_sw128(ot + h * (TILE / 2), row, 0, o[0]);
                         tc::st_sw128(ot + h * (TILE / 2), row, 32, o[1]);
@@ -404,10 +416,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                                                   ld / 2, x, lane, even < n, even + 1 < n);
                         }
                     }
-                    warp_arrive(&bar[B_OFREE], lane);
+                    arrive(B_OFREE);
                     if (d > 0 && !wait(B_STORED, d - 1)) break;
                 }
-                warp_arrive(&bar[B_STAGED], lane);
+                arrive(B_STAGED);
             }
             if (c == nc) break;
             const int n = tokens(c);
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 tmem_st16u(tl + C_P + 16 * j, o);
             }
             tmem_wait_st();
-            warp_arrive(&bar[B_B], lane);
+            arrive(B_B);
         }
     } else if (w < 16) {
         // ---- C: the state as an operand, its decay; Query X's rows ----
@@ -467,7 +479,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 tc::tmem_st32(tl + C_X + 32 * j, v);
             }
             tc::fence_async_smem();
-            warp_arrive(&bar[B_C], lane);
+            arrive(B_C);
             if (!wait(B_QX, c)) break;
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 for (int i = 0; i < 32; ++i) v[i] *= fo;
                 tc::tmem_st32(tl + C_O + 32 * j, v);
             }
-            warp_arrive(&bar[B_SCALED], lane);
+            arrive(B_SCALED);
         }
         if (x1 && wait(B_S, nc - 1)) {
 #pragma unroll 1
@@ -579,12 +591,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                     tc::bulk_commit();
                     tc::bulk_wait_read0();
                 }
-                mbar_arrive(&bar[B_STORED]);
+                mbar_arrive(sbar + 8 * B_STORED);
             }
             __syncwarp();
         }
         if (elect()) tc::bulk_wait0();
     }
+    if (!ok) *abort_flag = 1;
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
@@ -619,6 +632,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
     float* out = back ? a.back + (size_t(g.w - 1) * a.H + hd) * D * D : a.front + (size_t(g.w) * a.H + hd) * D * D;
     const int nc = (g.len + LC - 1) / LC;
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S_BAR);
+    const uint32_t sbar = smem_u32(bar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S_BAR + 8 * SB_END);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S_BAR + 8 * SB_END + 4);
     float* fs = reinterpret_cast<float*>(sm + S_TAB);
@@ -641,12 +655,12 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
     auto tile = [&](int c, int which) { return sm + ((c % S_STAGES) * 2 + which) * TILE; };
     bool ok = true;  // waits as in the walk
     auto wait = [&](int b, int turn) {
-        const bool done = ok && bounded_wait(&bar[b], uint32_t(turn) & 1u);
-        ok = __all_sync(0xffffffffu, done);
-        if (!ok) *abort_flag = 1;
+        ok = ok && bounded_wait(sbar + 8 * b, uint32_t(turn) & 1u);
+        __syncwarp();
         tc::fence_after_sync();
         return ok;
     };
+    auto arrive = [&](int b) { warp_arrive(sbar + 8 * b, lane); };
     constexpr uint32_t C_V = 128;  // columns: state 0, then the pieces of split values
 
     if (w < 8) {
@@ -659,7 +673,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
                     clear_rows(tile(c, 0), n, tid);
                     clear_rows(tile(c, 1), n, tid);
                     tc::fence_async_smem();
-                    warp_arrive(&bar[SB_FIX], lane);
+                    arrive(SB_FIX);
                 }
                 if (!wait(SB_FIX, 0)) break;
             }
@@ -668,7 +682,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
             for (int i = grp; i < PIECES; i += 2) {
                 if (c > 0 && !wait(SB_FREE + i, c - 1)) break;
                 split_piece<3>(tile(c, 1), i, w, lane, fs, all, tl + C_V + PLANES * i);
-                warp_arrive(&bar[SB_READY + i], lane);
+                arrive(SB_READY + i);
             }
             if (!ok) break;
         }
@@ -717,6 +731,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
         }
         if (!ok && elect()) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
     }
+    if (!ok) *abort_flag = 1;
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
