@@ -6,9 +6,10 @@
 //              dx = (g - xh sum_c(g xh) / D) / sqrt(..)          (norm; else dx = d)
 //
 // Bound by HBM: forward 2, backward 3 (2 without the norm) row transfers.  A row of D channels belongs to a
-// group of lanes that each hold four pairs (two vectors of four elements; both members of a pair lie in one
-// lane, so the turn needs no exchange), the norm's sum is one exchange over the group.  A group takes one
-// token's heads in turn, several rows in flight: the token's cosines and sines are computed once for them.
+// group of lanes that each hold 8 pairs (4 of fp32) as two 16-byte accesses; both members of a pair lie in one lane, so
+// the turn needs no exchange, and the norm's sum is one exchange over the group.  A block takes a tile of tokens of
+// one of the two tensors: its threads compute the tile's cosines and sines once, a group keeps those of one
+// token and the weights in registers and walks the token's heads, several rows in flight.
 //
 // Angles.  A position times a frequency in fp32 is off by a thousandth of a turn at position 10^4 already.
 // Here a frequency is a 64-bit fraction of a turn per token, F = freq / (2 pi) 2^64 mod 2^64, so pos F mod
@@ -22,26 +23,30 @@ namespace kda {
 
 namespace {
 
+// One tensor: q or k
+struct RopeSide {
+    const void *x, *g;  // input; gradient of the output (backward)
+    void* out;
+    const float* w;
+    float* dw;
+    int64_t ldx, ldg, ldo;  // token strides
+    int H;
+    int blocks;         // of the launch
+    float* part;        // [blocks][D] partial dw
+};
 struct RopeArgs {
     int64_t T;
-    int Hq, Hk, D, R, norm;
+    int D, R, norm;
     float eps, scale, inv_d;
-    const void *q, *k, *gq, *gk;  // inputs; gradients of the outputs (backward)
-    void *oq, *ok;
     const int* pos;
     const double* freq;
-    const float *wq, *wk;
-    int64_t ldq, ldk;    // token strides of q, k
-    int64_t ldgq, ldgk;  // of gq, gk
-    int64_t ldoq, ldok;  // of the outputs
-    int split, per;      // parts that a token's heads are cut into, heads of a part
-    float* part;         // [blocks][2][D] partial dwq, dwk
-    float *dwq, *dwk;
-    int blocks;
+    int per_token;      // groups that share a token's heads
+    RopeSide side[2];
 };
 
 constexpr int RP_THREADS = 256;
 constexpr int RP_MAXD = 256;
+constexpr int RP_TOKENS = 16;  // most tokens of a tile
 
 // freq / (2 pi) as a 64-bit fraction of a turn.  freq = M 2^(E - 63) with a 64-bit M, 1 / (2 pi) = C 2^-66:
 // their product's upper half times 2^(E - 1) is the fraction (whole turns fall out at the top).
@@ -64,11 +69,18 @@ __device__ __forceinline__ void cos_sin(int pos, unsigned long long F, float sca
     s *= scale;
 }
 
-template <class E> struct alignas(4 * sizeof(E)) Quad { E e[4]; };
+template <class E, int N> struct alignas(N * sizeof(E)) Pack { E e[N]; };
 template <class E> __device__ __forceinline__ E rp_cast(float v);
 template <> __device__ __forceinline__ float rp_cast<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 rp_cast<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half rp_cast<__half>(float v) { return __float2half_rn(v); }
+// two values as one store's neighbours
+template <class E> __device__ __forceinline__ void rp_put(E* e, f2 v) {
+    float a, b;
+    up2(v, a, b);
+    e[0] = rp_cast<E>(a);
+    e[1] = rp_cast<E>(b);
+}
 
 // Channels of pair p of a row (p >= R / 2: channels that are not turned, two by two)
 __device__ __forceinline__ void pair_at(int p, int R, bool pairs, int& a, int& b) {
@@ -76,48 +88,42 @@ __device__ __forceinline__ void pair_at(int p, int R, bool pairs, int& a, int& b
     else a = 2 * p, b = 2 * p + 1;
 }
 
-// A lane's row values: NP pairs (x[i], y[i])
-template <int NP> struct Row { float x[NP], y[NP]; };
+// A lane's row: NP pairs (x, y), two to a register pair
+template <int NP> struct Row { f2 x[NP / 2], y[NP / 2]; };
 
-// The channels of a lane.  VEC: one unit of eight channels, two quads at o0 and o1 (halves: the members of
-// four pairs; otherwise eight neighbours).  Else up to NP single pairs.
+// The channels of a lane.  VEC: 2 NP channels, two packs of NP: the members of NP pairs (halves), otherwise neighbours.
+// Else up to NP single pairs, pair i at l + i G.
 template <class E, int NP, bool PAIRS, bool VEC>
 struct Lane {
-    // VEC: NP = 4
-    int o0, o1;       // VEC: the quads' channels
-    int l, D, R, G;   // otherwise pair i is l + i G
+    int o0, o1;
+    int l, D, R, G;
     bool on, neighbours;
     __device__ __forceinline__ Lane(int lane, int D_, int R_, int G_) : l(lane), D(D_), R(R_), G(G_) {
-        if (VEC) {
-            on = 8 * l < D;
-            neighbours = PAIRS || 8 * l >= R;
-            o0 = neighbours ? 8 * l : 4 * l;
-            o1 = neighbours ? 8 * l + 4 : R / 2 + 4 * l;
-        } else {
-            on = true;
-        }
+        on = !VEC || 2 * NP * l < D;
+        neighbours = PAIRS || 2 * NP * l >= R;
+        o0 = neighbours ? 2 * NP * l : NP * l;
+        o1 = neighbours ? 2 * NP * l + NP : R / 2 + NP * l;
     }
     __device__ __forceinline__ bool has(int i) const { return VEC ? on : l + i * G < D / 2; }
-    __device__ __forceinline__ bool turns(int i) const { return VEC ? 8 * l < R : l + i * G < R / 2; }
-    __device__ __forceinline__ int pair(int i) const { return VEC ? 4 * l + i : l + i * G; }
-    // the raw elements of a row, to be kept while others load
-    struct Raw { Quad<E> a, b; };
-    __device__ __forceinline__ Raw load(const void* base, int64_t at) const {
+    __device__ __forceinline__ bool turns(int i) const { return VEC ? 2 * NP * l < R : l + i * G < R / 2; }
+    __device__ __forceinline__ int pair(int i) const { return VEC ? NP * l + i : l + i * G; }
+    struct Raw { Pack<E, NP> a, b; };
+    __device__ __forceinline__ Raw load(const void* base, int64_t at, bool use) const {
         Raw r;
         const E* p = static_cast<const E*>(base) + at;
         if constexpr (VEC) {
-            if (on) {
-                r.a = *reinterpret_cast<const Quad<E>*>(p + o0);
-                r.b = *reinterpret_cast<const Quad<E>*>(p + o1);
+            if (on && use) {
+                r.a = *reinterpret_cast<const Pack<E, NP>*>(p + o0);
+                r.b = *reinterpret_cast<const Pack<E, NP>*>(p + o1);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
+                for (int i = 0; i < NP; ++i) r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
-                if (has(i)) {
+                if (has(i) && use) {
                     int ca, cb;
                     pair_at(l + i * G, R, PAIRS, ca, cb);
                     r.a.e[i] = p[ca];
@@ -127,58 +133,70 @@ struct Lane {
         }
         return r;
     }
+    __device__ __forceinline__ Row<NP> values(const Raw& r) const {
+        Row<NP> v;
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) {
+            // neighbours: element 2 k of the pack of 2 NP is x of pair k, 2 k + 1 its y
+            const Pack<E, NP>& n = 4 * i < NP ? r.a : r.b;
+            const int k = (4 * i) % NP;
+            const bool nb = VEC && (PAIRS || neighbours);
+            v.x[i] = nb ? pk2(ssm_f<E>(n.e[k]), ssm_f<E>(n.e[k + 2])) : pk2(ssm_f<E>(r.a.e[2 * i]), ssm_f<E>(r.a.e[2 * i + 1]));
+            v.y[i] = nb ? pk2(ssm_f<E>(n.e[k + 1]), ssm_f<E>(n.e[k + 3])) : pk2(ssm_f<E>(r.b.e[2 * i]), ssm_f<E>(r.b.e[2 * i + 1]));
+        }
+        return v;
+    }
     __device__ __forceinline__ void store(void* base, int64_t at, const Row<NP>& v) const {
         E* p = static_cast<E*>(base) + at;
+        float x[NP], y[NP];
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) {
+            up2(v.x[i], x[2 * i], x[2 * i + 1]);
+            up2(v.y[i], y[2 * i], y[2 * i + 1]);
+        }
         if constexpr (VEC) {
             if (!on) return;
-            Quad<E> a, b;
+            Pack<E, NP> a, b;
+            if (PAIRS || neighbours) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // neighbours: pair i is channels 2 i, 2 i + 1 of the eight
-                if (neighbours) {
-                    (i < 2 ? a : b).e[2 * (i & 1)] = rp_cast<E>(v.x[i]);
-                    (i < 2 ? a : b).e[2 * (i & 1) + 1] = rp_cast<E>(v.y[i]);
-                } else {
-                    a.e[i] = rp_cast<E>(v.x[i]);
-                    b.e[i] = rp_cast<E>(v.y[i]);
+                for (int i = 0; i < NP / 2; ++i) {
+                    rp_put<E>(a.e + 2 * i, pk2(x[i], y[i]));
+                    rp_put<E>(b.e + 2 * i, pk2(x[NP / 2 + i], y[NP / 2 + i]));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NP / 2; ++i) {
+                    rp_put<E>(a.e + 2 * i, v.x[i]);
+                    rp_put<E>(b.e + 2 * i, v.y[i]);
                 }
             }
-            *reinterpret_cast<Quad<E>*>(p + o0) = a;
-            *reinterpret_cast<Quad<E>*>(p + o1) = b;
+            *reinterpret_cast<Pack<E, NP>*>(p + o0) = a;
+            *reinterpret_cast<Pack<E, NP>*>(p + o1) = b;
         } else {
 #pragma unroll
             for (int i = 0; i < NP; ++i)
                 if (has(i)) {
                     int ca, cb;
                     pair_at(l + i * G, R, PAIRS, ca, cb);
-                    p[ca] = rp_cast<E>(v.x[i]);
-                    p[cb] = rp_cast<E>(v.y[i]);
+                    p[ca] = rp_cast<E>(x[i]);
+                    p[cb] = rp_cast<E>(y[i]);
                 }
         }
-    }
-    __device__ __forceinline__ Row<NP> values(const Raw& r) const {
-        Row<NP> v;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            if (VEC && neighbours) {
-                v.x[i] = ssm_f<E>((i < 2 ? r.a : r.b).e[2 * (i & 1)]);
-                v.y[i] = ssm_f<E>((i < 2 ? r.a : r.b).e[2 * (i & 1) + 1]);
-            } else {
-                v.x[i] = ssm_f<E>(r.a.e[i]);
-                v.y[i] = ssm_f<E>(r.b.e[i]);
-            }
-        }
-        return v;
     }
     // fp32 parameters of the lane's channels (w null: ones)
     __device__ __forceinline__ Row<NP> weights(const float* w) const {
         Row<NP> v;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            v.x[i] = v.y[i] = 1.f;
-            int ca, cb;
-            pair_at(pair(i), R, PAIRS, ca, cb);
-            if (w && has(i)) v.x[i] = w[ca], v.y[i] = w[cb];
+        for (int i = 0; i < NP / 2; ++i) {
+            float t[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                int ca, cb;
+                pair_at(pair(2 * i + e), R, PAIRS, ca, cb);
+                if (w && has(2 * i + e)) t[e] = w[ca], t[2 + e] = w[cb];
+            }
+            v.x[i] = pk2(t[0], t[1]);
+            v.y[i] = pk2(t[2], t[3]);
         }
         return v;
     }
@@ -188,150 +206,168 @@ __device__ __forceinline__ float group_sum(float v, int G) {
     for (int o = G >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ float both_sum(f2 v) {
+    float a, b;
+    up2(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ f2 twice(float x) { return pk2(x, x); }
 
-constexpr int RP_ROWS = 4;  // rows of a group in flight
-
-// BWD: q, k and the gradients in, gradients out; otherwise q, k in, turned out.  A work unit is one part
-// of one token's heads (q's heads, then k's).
+// BWD: inputs and gradients in, gradients out; otherwise inputs in, turned out.  The first side[0].blocks blocks do q, the
+// others k.  tokens = groups / per_token tokens a tile.
 template <class E, int NP, bool PAIRS, bool VEC, bool BWD>
-__global__ void __launch_bounds__(RP_THREADS) k_rope(RopeArgs a, int G) {
-    const int tid = threadIdx.x, lane = tid & (G - 1), groups = RP_THREADS / G;
+__global__ void __launch_bounds__(RP_THREADS, 2) k_rope(RopeArgs a, int G) {
+    constexpr int ROWS = BWD ? 2 : 4;  // rows of a group in flight
+    __shared__ __align__(16) float cs[RP_TOKENS][RP_MAXD];  // cosines of R / 2 pairs, then sines
+    const int tid = threadIdx.x, lane = tid & (G - 1), groups = RP_THREADS / G, group = tid / G;
+    const int which = int(blockIdx.x) >= a.side[0].blocks;
+    const RopeSide& sd = a.side[which];
+    const int block = int(blockIdx.x) - (which ? a.side[0].blocks : 0);
     const Lane<E, NP, PAIRS, VEC> L(lane, a.D, a.R, G);
-    unsigned long long F[NP];
+    const int half = a.R / 2, tokens = groups / a.per_token;
+    const Row<NP> w = L.weights(a.norm ? sd.w : nullptr);
+    Row<NP> sum;  // of dw
 #pragma unroll
-    for (int i = 0; i < NP; ++i) F[i] = L.has(i) && L.turns(i) ? turns_per_token(a.freq[L.pair(i)]) : 0;
-    const Row<NP> wq = L.weights(a.norm ? a.wq : nullptr), wk = L.weights(a.norm ? a.wk : nullptr);
-    Row<NP> sq, sk;  // sums of dwq, dwk
-#pragma unroll
-    for (int i = 0; i < NP; ++i) sq.x[i] = sq.y[i] = sk.x[i] = sk.y[i] = 0.f;
-    const int H = a.Hq + a.Hk;
-    const int64_t units = a.T * a.split, per_wave = int64_t(gridDim.x) * groups;
-    // the lanes of a warp run the same number of rounds (exchanges over the group are warp-wide)
-    const int64_t rounds = (units + per_wave - 1) / per_wave;
-    for (int64_t round = 0; round < rounds; ++round) {
-        const int64_t u = round * per_wave + int64_t(blockIdx.x) * groups + tid / G;
-        const bool live = u < units;
-        const int64_t t = live ? u / a.split : 0;
-        const int h0 = live ? int(u % a.split) * a.per : 0, h1 = live ? min(h0 + a.per, H) : 0;
-        float c[NP], s[NP];
-        const int pos = live ? a.pos[t] : 0;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            c[i] = 1.f, s[i] = 0.f;
-            if (L.has(i) && L.turns(i)) cos_sin(pos, F[i], a.scale, c[i], s[i]);
+    for (int i = 0; i < NP / 2; ++i) sum.x[i] = sum.y[i] = twice(0.f);
+    const int64_t tiles = (a.T + tokens - 1) / tokens;
+    for (int64_t tile = block; tile < tiles; tile += sd.blocks) {
+        __syncthreads();
+        for (int i = tid; i < tokens * half; i += RP_THREADS) {
+            const int t = i / half, k = i - t * half;
+            float c = 1.f, s = 0.f;
+            if (tile * tokens + t < a.T) cos_sin(a.pos[tile * tokens + t], turns_per_token(a.freq[k]), a.scale, c, s);
+            cs[t][k] = c;
+            cs[t][half + k] = s;
         }
-        for (int hb = 0; hb < a.per; hb += RP_ROWS) {
-            typename Lane<E, NP, PAIRS, VEC>::Raw x[RP_ROWS], g[RP_ROWS];
+        __syncthreads();
+        const int own = group / a.per_token, first = group - own * a.per_token;
+        const int64_t t = tile * tokens + own;
+        const bool live = own < tokens && t < a.T;
+        f2 c[NP / 2], s[NP / 2];
 #pragma unroll
-            for (int r = 0; r < RP_ROWS; ++r) {
-                const int h = h0 + hb + r;
-                if (h >= h1) continue;
-                const bool isq = h < a.Hq;
-                const int hh = isq ? h : h - a.Hq;
-                if (!BWD || a.norm) x[r] = L.load(isq ? a.q : a.k, t * (isq ? a.ldq : a.ldk) + int64_t(hh) * a.D);
-                if (BWD) g[r] = L.load(isq ? a.gq : a.gk, t * (isq ? a.ldgq : a.ldgk) + int64_t(hh) * a.D);
+        for (int i = 0; i < NP / 2; ++i) {
+            if constexpr (VEC) {
+                c[i] = twice(1.f), s[i] = twice(0.f);
+                if (live && L.turns(0)) {
+                    c[i] = *reinterpret_cast<const f2*>(&cs[own][L.pair(2 * i)]);
+                    // (R / 2 is a multiple of NP)
+                    s[i] = *reinterpret_cast<const f2*>(&cs[own][half + L.pair(2 * i)]);
+                }
+            } else {
+                float u[4] = {1.f, 1.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (live && L.has(2 * i + e) && L.turns(2 * i + e))
+                        u[e] = cs[own][L.pair(2 * i + e)], u[2 + e] = cs[own][half + L.pair(2 * i + e)];
+                c[i] = pk2(u[0], u[1]);
+                s[i] = pk2(u[2], u[3]);
+            }
+        }
+        const int64_t x0 = t * sd.ldx, g0 = t * sd.ldg, y0 = t * sd.ldo;
+        // (every lane of a warp runs every round: the exchanges are warp-wide)
+        for (int hb = 0; hb < sd.H; hb += ROWS * a.per_token) {
+            typename Lane<E, NP, PAIRS, VEC>::Raw x[ROWS], g[ROWS];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const int h = hb + r * a.per_token + first;
+                const bool use = live && h < sd.H;
+                if (!BWD || a.norm) x[r] = L.load(sd.x, x0 + int64_t(h) * a.D, use);
+                if (BWD) g[r] = L.load(sd.g, g0 + int64_t(h) * a.D, use);
             }
 #pragma unroll
-            for (int r = 0; r < RP_ROWS; ++r) {
-                const int h = h0 + hb + r;
-                const bool use = h < h1;
-                const bool isq = h < a.Hq;
-                const int hh = isq ? h : h - a.Hq;
-                const Row<NP>& w = isq ? wq : wk;
+            for (int r = 0; r < ROWS; ++r) {
+                const int h = hb + r * a.per_token + first;
+                const bool use = live && h < sd.H;
                 Row<NP> v;
                 float rs = 1.f;
+                if (!BWD || a.norm) v = L.values(x[r]);
                 if (a.norm) {
-                    float ss = 0.f;
-                    if (use) {
-                        v = L.values(x[r]);
+                    f2 ss = twice(0.f);
 #pragma unroll
-                        for (int i = 0; i < NP; ++i) ss = fmaf(v.x[i], v.x[i], fmaf(v.y[i], v.y[i], ss));
-                    }
-                    rs = 1.f / sqrtf(fmaf(group_sum(ss, G), a.inv_d, a.eps));
-                } else if (!BWD && use) {
-                    v = L.values(x[r]);
+                    for (int i = 0; i < NP / 2; ++i) ss = fma2(v.x[i], v.x[i], fma2(v.y[i], v.y[i], ss));
+                    rs = rsqrtf(fmaf(group_sum(both_sum(ss), G), a.inv_d, a.eps));
                 }
+                const f2 rs2 = twice(rs), minus = twice(-1.f);
+                Row<NP> o;
                 if (!BWD) {
-                    if (!use) continue;
-                    Row<NP> y;
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        float p = v.x[i], z = v.y[i];
-                        if (a.norm) p *= rs * w.x[i], z *= rs * w.y[i];
-                        y.x[i] = L.turns(i) ? fmaf(p, c[i], -(z * s[i])) : p;
-                        y.y[i] = L.turns(i) ? fmaf(p, s[i], z * c[i]) : z;
+                    for (int i = 0; i < NP / 2; ++i) {
+                        f2 p = v.x[i], z = v.y[i];
+                        if (a.norm) p = mul2(p, mul2(w.x[i], rs2)), z = mul2(z, mul2(w.y[i], rs2));
+                        o.x[i] = fma2(p, c[i], mul2(mul2(z, s[i]), minus));
+                        o.y[i] = fma2(p, s[i], mul2(z, c[i]));
                     }
-                    L.store(isq ? a.oq : a.ok, t * (isq ? a.ldoq : a.ldok) + int64_t(hh) * a.D, y);
                 } else {
-                    Row<NP> d;
-                    float dot = 0.f;
-                    if (use) {
-                        const Row<NP> y = L.values(g[r]);
+                    o = L.values(g[r]);
+                    f2 dot = twice(0.f);
 #pragma unroll
-                        for (int i = 0; i < NP; ++i) {
-                            d.x[i] = L.turns(i) ? fmaf(y.x[i], c[i], y.y[i] * s[i]) : y.x[i];
-                            d.y[i] = L.turns(i) ? fmaf(y.y[i], c[i], -(y.x[i] * s[i])) : y.y[i];
-                            if (a.norm) {
-                                v.x[i] *= rs, v.y[i] *= rs;
-                                Row<NP>& sw = isq ? sq : sk;
-                                sw.x[i] = fmaf(d.x[i], v.x[i], sw.x[i]);
-                                sw.y[i] = fmaf(d.y[i], v.y[i], sw.y[i]);
-                                d.x[i] *= w.x[i], d.y[i] *= w.y[i];
-                                dot = fmaf(d.x[i], v.x[i], fmaf(d.y[i], v.y[i], dot));
-                            }
+                    for (int i = 0; i < NP / 2; ++i) {
+                        const f2 p = o.x[i], z = o.y[i];
+                        o.x[i] = fma2(p, c[i], mul2(z, s[i]));
+                        o.y[i] = fma2(z, c[i], mul2(mul2(p, s[i]), minus));
+                        if (a.norm) {
+                            v.x[i] = mul2(v.x[i], rs2), v.y[i] = mul2(v.y[i], rs2);
+                            sum.x[i] = fma2(o.x[i], v.x[i], sum.x[i]);
+                            sum.y[i] = fma2(o.y[i], v.y[i], sum.y[i]);
+                            o.x[i] = mul2(o.x[i], w.x[i]), o.y[i] = mul2(o.y[i], w.y[i]);
+                            dot = fma2(o.x[i], v.x[i], fma2(o.y[i], v.y[i], dot));
                         }
                     }
-                    if (a.norm) dot = group_sum(dot, G) * a.inv_d;
-                    if (!use) continue;
-                    if (a.norm)
+                    if (a.norm) {
+                        const f2 d2 = twice(-group_sum(both_sum(dot), G) * a.inv_d);
 #pragma unroll
-                        for (int i = 0; i < NP; ++i) {
-                            d.x[i] = rs * fmaf(-v.x[i], dot, d.x[i]);
-                            d.y[i] = rs * fmaf(-v.y[i], dot, d.y[i]);
+                        for (int i = 0; i < NP / 2; ++i) {
+                            o.x[i] = mul2(rs2, fma2(v.x[i], d2, o.x[i]));
+                            o.y[i] = mul2(rs2, fma2(v.y[i], d2, o.y[i]));
                         }
-                    L.store(isq ? a.oq : a.ok, t * (isq ? a.ldoq : a.ldok) + int64_t(hh) * a.D, d);
+                    }
                 }
+                if (use) L.store(sd.out, y0 + int64_t(h) * a.D, o);
             }
         }
     }
-    if (BWD && a.part) {  // the groups' sums, added in their order
-        __shared__ float red[2][RP_MAXD];
+    if (BWD && sd.part) {  // the groups' sums, added in their order
+        float* red = &cs[0][0];
         for (int gi = 0; gi < groups; ++gi) {
-            if (tid / G == gi) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    if (L.has(i)) {
-                        int ca, cb;
-                        pair_at(L.pair(i), a.R, PAIRS, ca, cb);
-                        red[0][ca] = gi ? red[0][ca] + sq.x[i] : sq.x[i];
-                        red[0][cb] = gi ? red[0][cb] + sq.y[i] : sq.y[i];
-                        red[1][ca] = gi ? red[1][ca] + sk.x[i] : sk.x[i];
-                        red[1][cb] = gi ? red[1][cb] + sk.y[i] : sk.y[i];
-                    }
-            }
             __syncthreads();
+            if (group == gi) {
+#pragma unroll
+                for (int i = 0; i < NP / 2; ++i) {
+                    float u[4];
+                    up2(sum.x[i], u[0], u[1]);
+                    up2(sum.y[i], u[2], u[3]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (L.has(2 * i + e)) {
+                            int ca, cb;
+                            pair_at(L.pair(2 * i + e), a.R, PAIRS, ca, cb);
+                            red[ca] = gi ? red[ca] + u[e] : u[e];
+                            red[cb] = gi ? red[cb] + u[2 + e] : u[2 + e];
+                        }
+                }
+            }
         }
-        for (int i = tid; i < 2 * a.D; i += RP_THREADS)
-            a.part[int64_t(blockIdx.x) * 2 * a.D + i] = red[i / a.D][i % a.D];
+        __syncthreads();
+        for (int i = tid; i < a.D; i += RP_THREADS) sd.part[int64_t(block) * a.D + i] = red[i];
     }
 }
 
 // dwq and dwk: the blocks' sums, one warp per channel, in an order that depends on their number alone
 __global__ void __launch_bounds__(256) k_rope_reduce(RopeArgs a) {
     const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (c >= 2 * a.D) return;
+    const RopeSide& sd = a.side[blockIdx.y];
+    if (c >= a.D || !sd.dw) return;
     float v = 0.f;
-    for (int b = lane; b < a.blocks; b += 32) v += a.part[int64_t(b) * 2 * a.D + c];
+    for (int b = lane; b < sd.blocks; b += 32) v += sd.part[int64_t(b) * a.D + c];
     v = warp_sum(v);
-    float* out = c < a.D ? a.dwq : a.dwk;
-    if (lane == 0 && out) out[c % a.D] = v;
+    if (lane == 0) sd.dw[c] = v;
 }
 
 bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 size_t esize(int dtype) { return dtype == KDA_DT_FP32 ? 4 : 2; }
 int64_t ld_or(int64_t ld, int64_t dense) { return ld ? ld : dense; }
 
-constexpr int RP_BWD_BLOCKS = 152 * 4;  // most blocks of a backward that sums dw
+constexpr int RP_BLOCKS = 152 * 4;  // most blocks of a launch (and one more)
 
 kda_status check_problem(const kda_rope_problem* p) {
     if (!p || p->T < 0 || p->T > INT32_MAX || p->Hq < 0 || p->Hq > 65535 || p->Hk < 0 || p->Hk > 65535 ||
@@ -348,37 +384,54 @@ kda_status check_problem(const kda_rope_problem* p) {
     return KDA_OK;
 }
 
-template <class E, bool BWD>
-void launch(RopeArgs a, int layout, cudaStream_t st) {
-    const bool pairs = layout == KDA_ROPE_PAIRS;
-    // four pairs a lane where the channels and every row allow quads, else one pair at a time
-    auto wide = [&](const void* p, int64_t ld) { return !p || (al(p, 4 * sizeof(E)) && ld % 4 == 0); };
-    const bool vec = a.D % 8 == 0 && a.R % 8 == 0 && wide(a.q, a.ldq) && wide(a.k, a.ldk) && wide(a.gq, a.ldgq) &&
-                     wide(a.gk, a.ldgk) && wide(a.oq, a.ldoq) && wide(a.ok, a.ldok);
+template <class E, int NP, bool VEC, bool BWD>
+void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     int G = 1;
-    while (G < 32 && G * (vec ? 8 : 2) < a.D) G *= 2;
-    const int groups = RP_THREADS / G, H = a.Hq + a.Hk;
-    // a group takes 16 heads of a token, fewer where that leaves too few groups
-    a.per = 16;
-    while (a.per > RP_ROWS && a.T * ((H + a.per - 1) / a.per) < int64_t(152) * 8 * groups) a.per /= 2;
-    a.split = (H + a.per - 1) / a.per;
-    const int64_t blocks = (a.T * a.split + groups - 1) / groups;
-    const int64_t most = BWD && a.part ? RP_BWD_BLOCKS : 152 * 8;
-    a.blocks = int(blocks < most ? blocks : most);
+    while (G < 32 && G * (VEC ? 2 * NP : 2) < a.D) G *= 2;
+    const int groups = RP_THREADS / G, H = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
+    // a group takes 8 heads of a token, fewer where that leaves less than two waves of blocks; tiles of at most
+    // RP_TOKENS tokens
+    int per = 1;
+    while (per < groups && (groups / per > RP_TOKENS || H > 8 * per)) per *= 2;
+    while (per < groups && per < H && a.T * per < int64_t(2) * RP_BLOCKS * groups) per *= 2;
+    a.per_token = per;
+    const int64_t tiles = (a.T + groups / per - 1) / (groups / per);
+    // blocks in proportion to the heads
+    const int all = a.side[0].H + a.side[1].H;
+    for (RopeSide& s : a.side) {
+        const int64_t share = (int64_t(RP_BLOCKS) * s.H + all - 1) / all;
+        s.blocks = int(s.H == 0 ? 0 : share < tiles ? share : tiles);
+    }
+    if (a.side[1].part) a.side[1].part = a.side[0].part + size_t(a.side[0].blocks) * a.D;
+    const unsigned grid = unsigned(a.side[0].blocks + a.side[1].blocks);
     {
         ProfScope ps(BWD ? KK_ROPE_BWD : KK_ROPE_FWD, st);
-        if (vec) {
-            if (pairs) k_rope<E, 4, true, true, BWD><<<a.blocks, RP_THREADS, 0, st>>>(a, G);
-            else k_rope<E, 4, false, true, BWD><<<a.blocks, RP_THREADS, 0, st>>>(a, G);
-        } else {
-            if (pairs) k_rope<E, 4, true, false, BWD><<<a.blocks, RP_THREADS, 0, st>>>(a, G);
-            else k_rope<E, 4, false, false, BWD><<<a.blocks, RP_THREADS, 0, st>>>(a, G);
-        }
+        if (pairs) k_rope<E, NP, true, VEC, BWD><<<grid, RP_THREADS, 0, st>>>(a, G);
+        else k_rope<E, NP, false, VEC, BWD><<<grid, RP_THREADS, 0, st>>>(a, G);
     }
-    if (BWD && a.part) {
+    if (BWD && a.side[0].part) {
         ProfScope ps(KK_ROPE_REDUCE, st);
-        k_rope_reduce<<<(2 * a.D + 7) / 8, 256, 0, st>>>(a);
+        k_rope_reduce<<<dim3((a.D + 7) / 8, 2), 256, 0, st>>>(a);
     }
+}
+
+template <class E, bool BWD>
+void launch(const RopeArgs& a, int layout, cudaStream_t st) {
+    constexpr int V = 16 / int(sizeof(E));
+    // whole 16-byte accesses where the channels and every row allow them, 8-byte ones of 16-bit rows, else one pair at
+    // a time
+    auto fits = [&](int n) {
+        if (a.D % (2 * n) || a.R % (2 * n)) return false;
+        for (const RopeSide& s : a.side)
+            if (s.H && (!al(s.x, n * sizeof(E)) || s.ldx % n || !al(s.g, n * sizeof(E)) || s.ldg % n ||
+                        !al(s.out, n * sizeof(E)) || s.ldo % n))
+                return false;
+        return true;
+    };
+    const bool pairs = layout == KDA_ROPE_PAIRS;
+    if (fits(V)) launch_as<E, V, true, BWD>(a, pairs, st);
+    else if (V == 8 && fits(4)) launch_as<E, 4, true, BWD>(a, pairs, st);
+    else launch_as<E, 4, false, BWD>(a, pairs, st);
 }
 
 template <bool BWD>
@@ -390,11 +443,12 @@ void launch_any(const RopeArgs& a, int layout, int dtype, cudaStream_t st) {
 
 RopeArgs make_args(const kda_rope_problem* p, const int32_t* pos, const double* freq, const float* wq, const float* wk) {
     RopeArgs a{};
-    a.T = p->T, a.Hq = p->Hq, a.Hk = p->Hk, a.D = p->D, a.R = p->R, a.norm = p->norm;
+    a.T = p->T, a.D = p->D, a.R = p->R, a.norm = p->norm;
     a.eps = p->eps, a.scale = p->scale, a.inv_d = 1.f / float(p->D);
-    a.pos = pos, a.freq = freq, a.wq = wq, a.wk = wk;
-    const int64_t q = int64_t(p->Hq) * p->D, k = int64_t(p->Hk) * p->D;
-    a.ldq = ld_or(p->ld_q, q), a.ldk = ld_or(p->ld_k, k);
+    a.pos = pos, a.freq = freq;
+    a.side[0].H = p->Hq, a.side[1].H = p->Hk;
+    a.side[0].w = wq, a.side[1].w = wk;
+    a.side[0].ldx = ld_or(p->ld_q, int64_t(p->Hq) * p->D), a.side[1].ldx = ld_or(p->ld_k, int64_t(p->Hk) * p->D);
     return a;
 }
 
@@ -408,7 +462,7 @@ bool rows_ok(const kda_rope_problem* p, const void* q, const void* k) {
 }
 
 size_t part_bytes(const kda_rope_problem* p) {
-    return p->norm ? size_t(RP_BWD_BLOCKS) * 2 * size_t(p->D) * 4 : 0;
+    return p->norm ? size_t(RP_BLOCKS + 1) * size_t(p->D) * 4 : 0;
 }
 
 kda_status launched() { return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
@@ -433,9 +487,9 @@ kda_status kda_rope_fwd(const kda_rope_problem* p, const void* q, const void* k,
     if (p->T == 0) return KDA_OK;
     if (!inputs_ok(p, pos, freq, wq, wk) || !rows_ok(p, q, k) || !rows_ok(p, q_out, k_out)) return KDA_ERR_INVALID_ARG;
     RopeArgs a = make_args(p, pos, freq, wq, wk);
-    a.q = p->Hq ? q : nullptr, a.k = p->Hk ? k : nullptr;
-    a.oq = p->Hq ? q_out : nullptr, a.ok = p->Hk ? k_out : nullptr;
-    a.ldoq = ld_or(p->ld_qo, int64_t(p->Hq) * p->D), a.ldok = ld_or(p->ld_ko, int64_t(p->Hk) * p->D);
+    a.side[0].x = q, a.side[1].x = k;
+    a.side[0].out = q_out, a.side[1].out = k_out;
+    a.side[0].ldo = ld_or(p->ld_qo, int64_t(p->Hq) * p->D), a.side[1].ldo = ld_or(p->ld_ko, int64_t(p->Hk) * p->D);
     launch_any<false>(a, p->layout, p->dtype, reinterpret_cast<cudaStream_t>(stream));
     return launched();
 }
@@ -459,13 +513,14 @@ kda_status kda_rope_bwd(const kda_rope_problem* p, const void* q, const void* k,
     if (sums && ws_bytes < part_bytes(p)) return KDA_ERR_WORKSPACE;
     RopeArgs a = make_args(p, pos, freq, wq, wk);
     const int64_t dense_q = int64_t(p->Hq) * p->D, dense_k = int64_t(p->Hk) * p->D;
-    if (p->norm) a.q = p->Hq ? q : nullptr, a.k = p->Hk ? k : nullptr;
-    a.gq = p->Hq ? dq_out : nullptr, a.gk = p->Hk ? dk_out : nullptr;
-    a.ldgq = ld_or(p->ld_qo, dense_q), a.ldgk = ld_or(p->ld_ko, dense_k);
-    a.oq = p->Hq ? dq : nullptr, a.ok = p->Hk ? dk : nullptr;
-    a.ldoq = dense_q, a.ldok = dense_k;
-    if (sums) a.part = static_cast<float*>(ws);
-    a.dwq = dwq, a.dwk = dwk;
+    if (p->norm) a.side[0].x = q, a.side[1].x = k;
+    else a.side[0].ldx = a.side[1].ldx = 0;  // (not read: no bar to wide accesses)
+    a.side[0].g = dq_out, a.side[1].g = dk_out;
+    a.side[0].ldg = ld_or(p->ld_qo, dense_q), a.side[1].ldg = ld_or(p->ld_ko, dense_k);
+    a.side[0].out = dq, a.side[1].out = dk;
+    a.side[0].ldo = dense_q, a.side[1].ldo = dense_k;
+    if (sums) a.side[0].part = a.side[1].part = static_cast<float*>(ws);
+    a.side[0].dw = dwq, a.side[1].dw = dwk;
     launch_any<true>(a, p->layout, p->dtype, st);
     return launched();
 }
