@@ -4,12 +4,15 @@
 //   y  = scale R(pos freq) n on the first R channels, in pairs, n on the others
 //   backward:  d = the turn undone on dy (scale kept),  dw = sum_rows d xh,  g = d w
 //              dx = (g - xh sum_c(g xh) / D) / sqrt(..)          (norm; else dx = d)
+//   sum x^2 and sum g x go through one exchange: dx = rs g - x rs^3 sum(g x) / D with rs = 1 / sqrt(..)
 //
 // Bound by HBM: forward 2, backward 3 (2 without the norm) row transfers.  A row of D channels belongs to a
 // group of lanes that each hold 8 pairs (4 of fp32) as two 16-byte accesses; both members of a pair lie in one lane, so
 // the turn needs no exchange, and the norm's sum is one exchange over the group.  A block takes a tile of tokens of
 // one of the two tensors: its threads compute the tile's cosines and sines once, a group keeps those of one
-// token and the weights in registers and walks the token's heads, several rows in flight.
+// token and the weights in registers and walks the token's heads.  The rows come through a ring in shared memory that
+// cp.async fills ahead, over the ends of tiles too; a thread copies exactly the bytes that it reads, so the ring needs no
+// barrier.
 //
 // Angles.  A position times a frequency in fp32 is off by a thousandth of a turn at position 10^4 already.
 // Here a frequency is a 64-bit fraction of a turn per token, F = freq / (2 pi) 2^64 mod 2^64, so pos F mod
@@ -91,44 +94,49 @@ __device__ __forceinline__ void pair_at(int p, int R, bool pairs, int& a, int& b
 // A lane's row: NP pairs (x, y), two to a register pair
 template <int NP> struct Row { f2 x[NP / 2], y[NP / 2]; };
 
-// The channels of a lane.  VEC: 2 NP channels, two packs of NP: the members of NP pairs (halves), otherwise neighbours.
-// Else up to NP single pairs, pair i at l + i G.
+// The channels of a lane.  VEC: two packs of NP channels, so that neighbouring lanes' packs are neighbours in memory.
+// Halves: the first and the second members of NP pairs (lanes past R: a channel of each half of the rest, which is not
+// turned).  Pairs: the pairs of NP channels in each half of the row.  Else up to NP single pairs, pair i at l + i G.
 template <class E, int NP, bool PAIRS, bool VEC>
 struct Lane {
     int o0, o1;
     int l, D, R, G;
-    bool on, neighbours;
+    bool on;
     __device__ __forceinline__ Lane(int lane, int D_, int R_, int G_) : l(lane), D(D_), R(R_), G(G_) {
         on = !VEC || 2 * NP * l < D;
-        neighbours = PAIRS || 2 * NP * l >= R;
-        o0 = neighbours ? 2 * NP * l : NP * l;
-        o1 = neighbours ? 2 * NP * l + NP : R / 2 + NP * l;
+        const bool turned = 2 * NP * l < R;
+        o0 = PAIRS || turned ? NP * l : R + NP * l - R / 2;
+        o1 = PAIRS ? D / 2 + NP * l : turned ? R / 2 + NP * l : R + (D - R) / 2 + NP * l - R / 2;
     }
     __device__ __forceinline__ bool has(int i) const { return VEC ? on : l + i * G < D / 2; }
-    __device__ __forceinline__ bool turns(int i) const { return VEC ? 2 * NP * l < R : l + i * G < R / 2; }
-    __device__ __forceinline__ int pair(int i) const { return VEC ? NP * l + i : l + i * G; }
+    // the pair of the rotation that pair i of the lane is (VEC: one that turns)
+    __device__ __forceinline__ int pair(int i) const {
+        if (!VEC) return l + i * G;
+        return !PAIRS ? NP * l + i : (2 * i < NP ? o0 : o1) / 2 + i % (NP / 2);
+    }
+    __device__ __forceinline__ bool turns(int i) const {
+        if (!VEC) return l + i * G < R / 2;
+        return !PAIRS ? 2 * NP * l < R : (2 * i < NP ? o0 : o1) < R;
+    }
+    // the channels of pair i's members
+    __device__ __forceinline__ void channels(int i, int& a, int& b) const {
+        if (!VEC) pair_at(l + i * G, R, PAIRS, a, b);
+        else if (!PAIRS) a = o0 + i, b = o1 + i;
+        else a = (2 * i < NP ? o0 : o1) + 2 * (i % (NP / 2)), b = a + 1;
+    }
     struct Raw { Pack<E, NP> a, b; };
+    // one element at a time
     __device__ __forceinline__ Raw load(const void* base, int64_t at, bool use) const {
         Raw r;
         const E* p = static_cast<const E*>(base) + at;
-        if constexpr (VEC) {
-            if (on && use) {
-                r.a = *reinterpret_cast<const Pack<E, NP>*>(p + o0);
-                r.b = *reinterpret_cast<const Pack<E, NP>*>(p + o1);
-            } else {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
-                if (has(i) && use) {
-                    int ca, cb;
-                    pair_at(l + i * G, R, PAIRS, ca, cb);
-                    r.a.e[i] = p[ca];
-                    r.b.e[i] = p[cb];
-                }
+        for (int i = 0; i < NP; ++i) {
+            r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
+            if (has(i) && use) {
+                int ca, cb;
+                channels(i, ca, cb);
+                r.a.e[i] = p[ca];
+                r.b.e[i] = p[cb];
             }
         }
         return r;
@@ -137,12 +145,15 @@ struct Lane {
         Row<NP> v;
 #pragma unroll
         for (int i = 0; i < NP / 2; ++i) {
-            // neighbours: element 2 k of the pack of 2 NP is x of pair k, 2 k + 1 its y
-            const Pack<E, NP>& n = 4 * i < NP ? r.a : r.b;
-            const int k = (4 * i) % NP;
-            const bool nb = VEC && (PAIRS || neighbours);
-            v.x[i] = nb ? pk2(ssm_f<E>(n.e[k]), ssm_f<E>(n.e[k + 2])) : pk2(ssm_f<E>(r.a.e[2 * i]), ssm_f<E>(r.a.e[2 * i + 1]));
-            v.y[i] = nb ? pk2(ssm_f<E>(n.e[k + 1]), ssm_f<E>(n.e[k + 3])) : pk2(ssm_f<E>(r.b.e[2 * i]), ssm_f<E>(r.b.e[2 * i + 1]));
+            if (VEC && PAIRS) {
+                const Pack<E, NP>& n = 4 * i < NP ? r.a : r.b;
+                const int k = (4 * i) % NP;
+                v.x[i] = pk2(ssm_f<E>(n.e[k]), ssm_f<E>(n.e[k + 2]));
+                v.y[i] = pk2(ssm_f<E>(n.e[k + 1]), ssm_f<E>(n.e[k + 3]));
+            } else {
+                v.x[i] = pk2(ssm_f<E>(r.a.e[2 * i]), ssm_f<E>(r.a.e[2 * i + 1]));
+                v.y[i] = pk2(ssm_f<E>(r.b.e[2 * i]), ssm_f<E>(r.b.e[2 * i + 1]));
+            }
         }
         return v;
     }
@@ -157,18 +168,10 @@ struct Lane {
         if constexpr (VEC) {
             if (!on) return;
             Pack<E, NP> a, b;
-            if (PAIRS || neighbours) {
 #pragma unroll
-                for (int i = 0; i < NP / 2; ++i) {
-                    rp_put<E>(a.e + 2 * i, pk2(x[i], y[i]));
-                    rp_put<E>(b.e + 2 * i, pk2(x[NP / 2 + i], y[NP / 2 + i]));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NP / 2; ++i) {
-                    rp_put<E>(a.e + 2 * i, v.x[i]);
-                    rp_put<E>(b.e + 2 * i, v.y[i]);
-                }
+            for (int i = 0; i < NP / 2; ++i) {
+                rp_put<E>(a.e + 2 * i, PAIRS ? pk2(x[i], y[i]) : v.x[i]);
+                rp_put<E>(b.e + 2 * i, PAIRS ? pk2(x[NP / 2 + i], y[NP / 2 + i]) : v.y[i]);
             }
             *reinterpret_cast<Pack<E, NP>*>(p + o0) = a;
             *reinterpret_cast<Pack<E, NP>*>(p + o1) = b;
@@ -177,7 +180,7 @@ struct Lane {
             for (int i = 0; i < NP; ++i)
                 if (has(i)) {
                     int ca, cb;
-                    pair_at(l + i * G, R, PAIRS, ca, cb);
+                    channels(i, ca, cb);
                     p[ca] = rp_cast<E>(x[i]);
                     p[cb] = rp_cast<E>(y[i]);
                 }
@@ -192,7 +195,7 @@ struct Lane {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 int ca, cb;
-                pair_at(pair(2 * i + e), R, PAIRS, ca, cb);
+                channels(2 * i + e, ca, cb);
                 if (w && has(2 * i + e)) t[e] = w[ca], t[2 + e] = w[cb];
             }
             v.x[i] = pk2(t[0], t[1]);
@@ -202,9 +205,17 @@ struct Lane {
     }
 };
 
-__device__ __forceinline__ float group_sum(float v, int G) {
-    for (int o = G >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+template <int BYTES>
+__device__ __forceinline__ void cp_bytes(void* smem, const void* gmem) {
+    if constexpr (BYTES == 16) cp16(smem, gmem);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(smem)), "l"(gmem));
+}
+
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], int G) {
+    for (int o = G >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 __device__ __forceinline__ float both_sum(f2 v) {
     float a, b;
@@ -213,11 +224,21 @@ __device__ __forceinline__ float both_sum(f2 v) {
 }
 __device__ __forceinline__ f2 twice(float x) { return pk2(x, x); }
 
+// Rows ahead in the ring, and blocks of a multiprocessor that its shared memory is sized for
+template <bool BWD> constexpr int rp_depth() { return BWD ? 4 : 8; }
+constexpr int RP_OCCUPANCY = 2;
+template <bool BWD> constexpr size_t rp_smem(int pack_bytes) {
+    return size_t(rp_depth<BWD>()) * (BWD ? 4 : 2) * pack_bytes * RP_THREADS;
+}
+
 // BWD: inputs and gradients in, gradients out; otherwise inputs in, turned out.  The first side[0].blocks blocks do q, the
 // others k.  tokens = groups / per_token tokens a tile.
 template <class E, int NP, bool PAIRS, bool VEC, bool BWD>
-__global__ void __launch_bounds__(RP_THREADS, 2) k_rope(RopeArgs a, int G) {
-    constexpr int ROWS = BWD ? 2 : 4;  // rows of a group in flight
+__global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, int G) {
+    using P = Pack<E, NP>;
+    constexpr int DEPTH = rp_depth<BWD>(), ROWS = BWD ? 1 : 2;  // ROWS rows of a group are worked on together
+    extern __shared__ __align__(16) unsigned char ring_raw[];
+    P* ring = reinterpret_cast<P*>(ring_raw);  // [DEPTH][x, then g: two packs][thread]
     __shared__ __align__(16) float cs[RP_TOKENS][RP_MAXD];  // cosines of R / 2 pairs, then sines
     const int tid = threadIdx.x, lane = tid & (G - 1), groups = RP_THREADS / G, group = tid / G;
     const int which = int(blockIdx.x) >= a.side[0].blocks;
@@ -225,11 +246,40 @@ __global__ void __launch_bounds__(RP_THREADS, 2) k_rope(RopeArgs a, int G) {
     const int block = int(blockIdx.x) - (which ? a.side[0].blocks : 0);
     const Lane<E, NP, PAIRS, VEC> L(lane, a.D, a.R, G);
     const int half = a.R / 2, tokens = groups / a.per_token;
+    const int own = group / a.per_token, first = group - own * a.per_token;
+    const int rows = (sd.H + ROWS * a.per_token - 1) / (ROWS * a.per_token) * ROWS;  // of a group in a tile
     const Row<NP> w = L.weights(a.norm ? sd.w : nullptr);
     Row<NP> sum;  // of dw
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) sum.x[i] = sum.y[i] = twice(0.f);
     const int64_t tiles = (a.T + tokens - 1) / tokens;
+    auto slot = [&](int d, int k) { return ring + (d * (BWD ? 4 : 2) + k) * RP_THREADS + tid; };
+    // the next row to be copied, and its place in the ring
+    int64_t ahead = block;
+    int ahead_row = 0, ahead_at = 0;
+    auto copy_next = [&]() {
+        if constexpr (VEC) {
+            const int64_t t = ahead * tokens + own;
+            const int h = ahead_row * a.per_token + first;
+            if (ahead < tiles && t < a.T && h < sd.H && L.on) {
+                if (!BWD || a.norm) {
+                    const E* p = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(h) * a.D;
+                    cp_bytes<sizeof(P)>(slot(ahead_at, 0), p + L.o0);
+                    cp_bytes<sizeof(P)>(slot(ahead_at, 1), p + L.o1);
+                }
+                if constexpr (BWD) {
+                    const E* p = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(h) * a.D;
+                    cp_bytes<sizeof(P)>(slot(ahead_at, 2), p + L.o0);
+                    cp_bytes<sizeof(P)>(slot(ahead_at, 3), p + L.o1);
+                }
+            }
+            cp_commit();
+            ahead_at = ahead_at + 1 == DEPTH ? 0 : ahead_at + 1;
+            if (++ahead_row == rows) ahead_row = 0, ahead += sd.blocks;
+        }
+    };
+    for (int d = 0; d < DEPTH; ++d) copy_next();
+    int at = 0;
     for (int64_t tile = block; tile < tiles; tile += sd.blocks) {
         __syncthreads();
         for (int i = tid; i < tokens * half; i += RP_THREADS) {
@@ -240,24 +290,22 @@ __global__ void __launch_bounds__(RP_THREADS, 2) k_rope(RopeArgs a, int G) {
             cs[t][half + k] = s;
         }
         __syncthreads();
-        const int own = group / a.per_token, first = group - own * a.per_token;
         const int64_t t = tile * tokens + own;
-        const bool live = own < tokens && t < a.T;
+        const bool live = t < a.T;
         f2 c[NP / 2], s[NP / 2];
 #pragma unroll
         for (int i = 0; i < NP / 2; ++i) {
             if constexpr (VEC) {
                 c[i] = twice(1.f), s[i] = twice(0.f);
-                if (live && L.turns(0)) {
+                if (L.turns(2 * i)) {  // (their pairs are neighbours, and R / 2 is even)
                     c[i] = *reinterpret_cast<const f2*>(&cs[own][L.pair(2 * i)]);
-                    // (R / 2 is a multiple of NP)
                     s[i] = *reinterpret_cast<const f2*>(&cs[own][half + L.pair(2 * i)]);
                 }
             } else {
                 float u[4] = {1.f, 1.f, 0.f, 0.f};
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (live && L.has(2 * i + e) && L.turns(2 * i + e))
+                    if (L.has(2 * i + e) && L.turns(2 * i + e))
                         u[e] = cs[own][L.pair(2 * i + e)], u[2 + e] = cs[own][half + L.pair(2 * i + e)];
                 c[i] = pk2(u[0], u[1]);
                 s[i] = pk2(u[2], u[3]);
@@ -265,67 +313,89 @@ __global__ void __launch_bounds__(RP_THREADS, 2) k_rope(RopeArgs a, int G) {
         }
         const int64_t x0 = t * sd.ldx, g0 = t * sd.ldg, y0 = t * sd.ldo;
         // (every lane of a warp runs every round: the exchanges are warp-wide)
-        for (int hb = 0; hb < sd.H; hb += ROWS * a.per_token) {
+        for (int r0 = 0; r0 < rows; r0 += ROWS) {
             typename Lane<E, NP, PAIRS, VEC>::Raw x[ROWS], g[ROWS];
+            if constexpr (VEC) cp_wait<DEPTH - ROWS>();
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const int h = hb + r * a.per_token + first;
+                const int h = (r0 + r) * a.per_token + first;
                 const bool use = live && h < sd.H;
-                if (!BWD || a.norm) x[r] = L.load(sd.x, x0 + int64_t(h) * a.D, use);
-                if (BWD) g[r] = L.load(sd.g, g0 + int64_t(h) * a.D, use);
+                if constexpr (VEC) {
+                    const bool full = use && L.on;  // (else what the ring holds is of no row)
+                    const P none{};
+                    if (!BWD || a.norm) x[r].a = full ? *slot(at, 0) : none, x[r].b = full ? *slot(at, 1) : none;
+                    if constexpr (BWD) g[r].a = full ? *slot(at, 2) : none, g[r].b = full ? *slot(at, 3) : none;
+                    at = at + 1 == DEPTH ? 0 : at + 1;
+                } else {
+                    if (!BWD || a.norm) x[r] = L.load(sd.x, x0 + int64_t(h) * a.D, use);
+                    if (BWD) g[r] = L.load(sd.g, g0 + int64_t(h) * a.D, use);
+                }
+            }
+            Row<NP> v[ROWS], o[ROWS];
+            float all[2 * ROWS];  // the rows' sums over channels: x^2, and g x (backward)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                if (!BWD || a.norm) v[r] = L.values(x[r]);
+                f2 xx = twice(0.f), gx = twice(0.f);
+                if (a.norm)
+#pragma unroll
+                    for (int i = 0; i < NP / 2; ++i) xx = fma2(v[r].x[i], v[r].x[i], fma2(v[r].y[i], v[r].y[i], xx));
+                if constexpr (BWD) {  // the turn undone
+                    o[r] = L.values(g[r]);
+#pragma unroll
+                    for (int i = 0; i < NP / 2; ++i) {
+                        const f2 p = o[r].x[i], z = o[r].y[i];
+                        o[r].x[i] = fma2(p, c[i], mul2(z, s[i]));
+                        o[r].y[i] = fma2(mul2(p, s[i]), twice(-1.f), mul2(z, c[i]));
+                        if (a.norm) gx = fma2(mul2(o[r].x[i], w.x[i]), v[r].x[i], fma2(mul2(o[r].y[i], w.y[i]), v[r].y[i], gx));
+                    }
+                }
+                all[r] = both_sum(xx);
+                all[ROWS + r] = BWD ? both_sum(gx) : 0.f;
+            }
+            if (a.norm) {
+                if constexpr (BWD) {
+                    group_sums<2 * ROWS>(all, G);
+                } else {
+                    float xx[ROWS];
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) xx[r] = all[r];
+                    group_sums<ROWS>(xx, G);
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) all[r] = xx[r];
+                }
             }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const int h = hb + r * a.per_token + first;
+                const int h = (r0 + r) * a.per_token + first;
                 const bool use = live && h < sd.H;
-                Row<NP> v;
-                float rs = 1.f;
-                if (!BWD || a.norm) v = L.values(x[r]);
-                if (a.norm) {
-                    f2 ss = twice(0.f);
-#pragma unroll
-                    for (int i = 0; i < NP / 2; ++i) ss = fma2(v.x[i], v.x[i], fma2(v.y[i], v.y[i], ss));
-                    rs = rsqrtf(fmaf(group_sum(both_sum(ss), G), a.inv_d, a.eps));
-                }
-                const f2 rs2 = twice(rs), minus = twice(-1.f);
-                Row<NP> o;
-                if (!BWD) {
+                const float rs = rsqrtf(fmaf(all[r], a.inv_d, a.eps));
+                const f2 rs2 = twice(rs);
+                if constexpr (!BWD) {
 #pragma unroll
                     for (int i = 0; i < NP / 2; ++i) {
-                        f2 p = v.x[i], z = v.y[i];
+                        f2 p = v[r].x[i], z = v[r].y[i];
                         if (a.norm) p = mul2(p, mul2(w.x[i], rs2)), z = mul2(z, mul2(w.y[i], rs2));
-                        o.x[i] = fma2(p, c[i], mul2(mul2(z, s[i]), minus));
-                        o.y[i] = fma2(p, s[i], mul2(z, c[i]));
+                        o[r].x[i] = fma2(p, c[i], mul2(mul2(z, s[i]), twice(-1.f)));
+                        o[r].y[i] = fma2(p, s[i], mul2(z, c[i]));
                     }
-                } else {
-                    o = L.values(g[r]);
-                    f2 dot = twice(0.f);
+                } else if (a.norm) {
+                    // dx = rs (g - xh sum(g xh) / D) = rs g - x rs^3 sum(g x) / D
+                    const f2 k = twice(-rs * rs * rs * all[ROWS + r] * a.inv_d);
 #pragma unroll
                     for (int i = 0; i < NP / 2; ++i) {
-                        const f2 p = o.x[i], z = o.y[i];
-                        o.x[i] = fma2(p, c[i], mul2(z, s[i]));
-                        o.y[i] = fma2(z, c[i], mul2(mul2(p, s[i]), minus));
-                        if (a.norm) {
-                            v.x[i] = mul2(v.x[i], rs2), v.y[i] = mul2(v.y[i], rs2);
-                            sum.x[i] = fma2(o.x[i], v.x[i], sum.x[i]);
-                            sum.y[i] = fma2(o.y[i], v.y[i], sum.y[i]);
-                            o.x[i] = mul2(o.x[i], w.x[i]), o.y[i] = mul2(o.y[i], w.y[i]);
-                            dot = fma2(o.x[i], v.x[i], fma2(o.y[i], v.y[i], dot));
-                        }
-                    }
-                    if (a.norm) {
-                        const f2 d2 = twice(-group_sum(both_sum(dot), G) * a.inv_d);
-#pragma unroll
-                        for (int i = 0; i < NP / 2; ++i) {
-                            o.x[i] = mul2(rs2, fma2(v.x[i], d2, o.x[i]));
-                            o.y[i] = mul2(rs2, fma2(v.y[i], d2, o.y[i]));
-                        }
+                        sum.x[i] = fma2(o[r].x[i], mul2(v[r].x[i], rs2), sum.x[i]);
+                        sum.y[i] = fma2(o[r].y[i], mul2(v[r].y[i], rs2), sum.y[i]);
+                        o[r].x[i] = fma2(v[r].x[i], k, mul2(o[r].x[i], mul2(w.x[i], rs2)));
+                        o[r].y[i] = fma2(v[r].y[i], k, mul2(o[r].y[i], mul2(w.y[i], rs2)));
                     }
                 }
-                if (use) L.store(sd.out, y0 + int64_t(h) * a.D, o);
+                copy_next();  // into a place just read
+                if (use) L.store(sd.out, y0 + int64_t(h) * a.D, o[r]);
             }
         }
     }
+    if constexpr (VEC) cp_wait<0>();
     if (BWD && sd.part) {  // the groups' sums, added in their order
         float* red = &cs[0][0];
         for (int gi = 0; gi < groups; ++gi) {
@@ -340,7 +410,7 @@ __global__ void __launch_bounds__(RP_THREADS, 2) k_rope(RopeArgs a, int G) {
                     for (int e = 0; e < 2; ++e)
                         if (L.has(2 * i + e)) {
                             int ca, cb;
-                            pair_at(L.pair(2 * i + e), a.R, PAIRS, ca, cb);
+                            L.channels(2 * i + e, ca, cb);
                             red[ca] = gi ? red[ca] + u[e] : u[e];
                             red[cb] = gi ? red[cb] + u[2 + e] : u[2 + e];
                         }
@@ -367,7 +437,8 @@ bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 
 size_t esize(int dtype) { return dtype == KDA_DT_FP32 ? 4 : 2; }
 int64_t ld_or(int64_t ld, int64_t dense) { return ld ? ld : dense; }
 
-constexpr int RP_BLOCKS = 152 * 4;  // most blocks of a launch (and one more)
+constexpr int RP_SMS = 152;  // multiprocessors: a launch has one wave of blocks at most (and one more block)
+constexpr int RP_MAXBLOCKS = RP_SMS * 2;
 
 kda_status check_problem(const kda_rope_problem* p) {
     if (!p || p->T < 0 || p->T > INT32_MAX || p->Hq < 0 || p->Hq > 65535 || p->Hk < 0 || p->Hk > 65535 ||
@@ -389,25 +460,30 @@ void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     int G = 1;
     while (G < 32 && G * (VEC ? 2 * NP : 2) < a.D) G *= 2;
     const int groups = RP_THREADS / G, H = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
-    // a group takes 8 heads of a token, fewer where that leaves less than two waves of blocks; tiles of at most
-    // RP_TOKENS tokens
+    constexpr int most = RP_SMS * RP_OCCUPANCY;
+    // a group takes 8 heads of a token, fewer where that leaves less than a wave of blocks; tiles of at most RP_TOKENS
+    // tokens
     int per = 1;
     while (per < groups && (groups / per > RP_TOKENS || H > 8 * per)) per *= 2;
-    while (per < groups && per < H && a.T * per < int64_t(2) * RP_BLOCKS * groups) per *= 2;
+    while (per < groups && per < H && a.T * per < int64_t(most) * groups) per *= 2;
     a.per_token = per;
     const int64_t tiles = (a.T + groups / per - 1) / (groups / per);
     // blocks in proportion to the heads
     const int all = a.side[0].H + a.side[1].H;
     for (RopeSide& s : a.side) {
-        const int64_t share = (int64_t(RP_BLOCKS) * s.H + all - 1) / all;
+        const int64_t share = (int64_t(most) * s.H + all - 1) / all;
         s.blocks = int(s.H == 0 ? 0 : share < tiles ? share : tiles);
     }
     if (a.side[1].part) a.side[1].part = a.side[0].part + size_t(a.side[0].blocks) * a.D;
     const unsigned grid = unsigned(a.side[0].blocks + a.side[1].blocks);
     {
+        static unsigned long long done[2];
+        const size_t smem = VEC ? rp_smem<BWD>(int(sizeof(Pack<E, NP>))) : 0;
+        auto* kernel = pairs ? k_rope<E, NP, true, VEC, BWD> : k_rope<E, NP, false, VEC, BWD>;
+        // (the limit counts the static part too)
+        allow_smem(reinterpret_cast<const void*>(kernel), smem + RP_TOKENS * RP_MAXD * sizeof(float), &done[pairs]);
         ProfScope ps(BWD ? KK_ROPE_BWD : KK_ROPE_FWD, st);
-        if (pairs) k_rope<E, NP, true, VEC, BWD><<<grid, RP_THREADS, 0, st>>>(a, G);
-        else k_rope<E, NP, false, VEC, BWD><<<grid, RP_THREADS, 0, st>>>(a, G);
+        kernel<<<grid, RP_THREADS, smem, st>>>(a, G);
     }
     if (BWD && a.side[0].part) {
         ProfScope ps(KK_ROPE_REDUCE, st);
@@ -462,7 +538,7 @@ bool rows_ok(const kda_rope_problem* p, const void* q, const void* k) {
 }
 
 size_t part_bytes(const kda_rope_problem* p) {
-    return p->norm ? size_t(RP_BLOCKS + 1) * size_t(p->D) * 4 : 0;
+    return p->norm ? size_t(RP_MAXBLOCKS + 1) * size_t(p->D) * 4 : 0;
 }
 
 kda_status launched() { return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
