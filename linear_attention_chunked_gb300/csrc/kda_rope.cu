@@ -240,6 +240,8 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     extern __shared__ __align__(16) unsigned char ring_raw[];
     P* ring = reinterpret_cast<P*>(ring_raw);  // [DEPTH][x, then g: two packs][thread]
     __shared__ __align__(16) float cs[RP_TOKENS][RP_MAXD];  // cosines of R / 2 pairs, then sines
+    __shared__ unsigned long long turn[RP_MAXD / 2];        // turns_per_token of the pairs
+    __shared__ int place[RP_TOKENS];                        // the tile's positions
     const int tid = threadIdx.x, lane = tid & (G - 1), groups = RP_THREADS / G, group = tid / G;
     const int which = int(blockIdx.x) >= a.side[0].blocks;
     const RopeSide& sd = a.side[which];
@@ -280,15 +282,18 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     };
     for (int d = 0; d < DEPTH; ++d) copy_next();
     int at = 0;
+    // positions are read a tile ahead: the cosines and sines of a tile wait for no load
+    auto position = [&](int64_t tile) { return tid < tokens && tile * tokens + tid < a.T ? a.pos[tile * tokens + tid] : 0; };
+    for (int i = tid; i < half; i += RP_THREADS) turn[i] = turns_per_token(a.freq[i]);
+    int next = position(block);
     for (int64_t tile = block; tile < tiles; tile += sd.blocks) {
+        if (tid < tokens) place[tid] = next;
         __syncthreads();
         for (int i = tid; i < tokens * half; i += RP_THREADS) {
             const int t = i / half, k = i - t * half;
-            float c = 1.f, s = 0.f;
-            if (tile * tokens + t < a.T) cos_sin(a.pos[tile * tokens + t], turns_per_token(a.freq[k]), a.scale, c, s);
-            cs[t][k] = c;
-            cs[t][half + k] = s;
+            cos_sin(place[t], turn[k], a.scale, cs[t][k], cs[t][half + k]);
         }
+        next = position(tile + sd.blocks);
         __syncthreads();
         const int64_t t = tile * tokens + own;
         const bool live = t < a.T;

@@ -203,3 +203,35 @@ def test_gradient_against_differences():
         num = float(sum(((x - y) * z.double()).sum() for x, y, z in zip(out[0], out[1], (dq, dk))) / (2 * e))
         size = float(sum(x.norm() * z.norm() for x, z in zip(out[0], (dq, dk))))
         assert abs(num - float((g[n].double() * d.double()).sum())) <= 2.0 ** -22 * size / (2 * e) + 10 * e * e * size
+
+
+def test_offsets_beyond_32_bits():
+    T, wide = 36000, 64 * 1024
+    big = torch.empty((T, wide), dtype=torch.bfloat16, device="cuda")
+    q, k, dq, dk, pos, f, s, (wq, wk) = _case(T, 1, 1, 64, 64, "bf16", True, fused=False)
+    x = big[:, wide - 64:].unflatten(1, (1, 64)).copy_(q)
+    kw = dict(wq=wq, wk=wk, norm=True, scale=s)
+    want, _ = kda.kda_rope_fwd(q, k, pos, f, **kw)
+    got, _ = kda.kda_rope_fwd(x, k, pos, f, q_out=x, **kw)
+    assert got is x and torch.equal(x, want)
+
+
+def test_two_graphs_share_a_workspace():
+    a, b = _case(70, 4, 2, 128, 128, "bf16", True, seed=1), _case(70, 4, 2, 128, 128, "bf16", True, seed=2)
+    ws = torch.empty(kda.kda_rope_workspace_size(128), dtype=torch.uint8, device="cuda")
+
+    def call(c, ws=None):
+        q, k, dq, dk, pos, f, s, (wq, wk) = c
+        return kda.kda_rope_bwd(q, k, pos, f, dq, dk, wq=wq, wk=wk, norm=True, scale=s, ws=ws)
+
+    want, graphs, outs = [call(a), call(b)], [], []
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(c, ws))
+        graphs.append(g)
+    for _ in range(2):
+        for g, out, w in zip(graphs, outs, want):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(out[k], w[k]) for k in w)
