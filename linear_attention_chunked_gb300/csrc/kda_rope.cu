@@ -94,49 +94,59 @@ __device__ __forceinline__ void pair_at(int p, int R, bool pairs, int& a, int& b
 // A lane's row: NP pairs (x, y), two to a register pair
 template <int NP> struct Row { f2 x[NP / 2], y[NP / 2]; };
 
-// The channels of a lane.  VEC: two packs of NP channels, so that neighbouring lanes' packs are neighbours in memory.
-// Halves: the first and the second members of NP pairs (lanes past R: a channel of each half of the rest, which is not
-// turned).  Pairs: the pairs of NP channels in each half of the row.  Else up to NP single pairs, pair i at l + i G.
-template <class E, int NP, bool PAIRS, bool VEC>
+// The channels of a lane: U units, unit u the (l + u G)-th of its row, of two packs of N channels each, so that
+// neighbouring lanes' packs are neighbours in memory.  Halves: the first and the second members of N pairs (units past
+// R: channels of each half of the rest, which is not turned).  Pairs: the pairs of N channels in each half of the row.
+// N = 1: one pair, wherever its members lie.
+template <class E, int N, int U, bool PAIRS>
 struct Lane {
-    int o0, o1;
+    static constexpr int NP = N * U;  // pairs of a lane
+    int o0[U], o1[U];
     int l, D, R, G;
-    bool on;
     __device__ __forceinline__ Lane(int lane, int D_, int R_, int G_) : l(lane), D(D_), R(R_), G(G_) {
-        on = !VEC || 2 * NP * l < D;
-        const bool turned = 2 * NP * l < R;
-        o0 = PAIRS || turned ? NP * l : R + NP * l - R / 2;
-        o1 = PAIRS ? D / 2 + NP * l : turned ? R / 2 + NP * l : R + (D - R) / 2 + NP * l - R / 2;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = l + u * G;
+            if (N == 1) {
+                pair_at(j, R, PAIRS, o0[u], o1[u]);
+            } else {
+                const bool turned = 2 * N * j < R;
+                o0[u] = PAIRS || turned ? N * j : R + N * j - R / 2;
+                o1[u] = PAIRS ? D / 2 + N * j : turned ? R / 2 + N * j : R + (D - R) / 2 + N * j - R / 2;
+            }
+        }
     }
-    __device__ __forceinline__ bool has(int i) const { return VEC ? on : l + i * G < D / 2; }
-    // the pair of the rotation that pair i of the lane is (VEC: one that turns)
+    __device__ __forceinline__ bool on(int u) const { return 2 * N * (l + u * G) < D; }
+    __device__ __forceinline__ bool has(int i) const { return on(i / N); }
+    // the pair of the rotation that pair i of the lane is (where it turns)
     __device__ __forceinline__ int pair(int i) const {
-        if (!VEC) return l + i * G;
-        return !PAIRS ? NP * l + i : (2 * i < NP ? o0 : o1) / 2 + i % (NP / 2);
+        const int u = i / N, e = i % N;
+        if (N == 1 || !PAIRS) return N * (l + u * G) + e;
+        return (2 * e < N ? o0[u] : o1[u]) / 2 + e % (N / 2 > 0 ? N / 2 : 1);
     }
     __device__ __forceinline__ bool turns(int i) const {
-        if (!VEC) return l + i * G < R / 2;
-        return !PAIRS ? 2 * NP * l < R : (2 * i < NP ? o0 : o1) < R;
+        const int u = i / N, e = i % N;
+        if (N == 1 || !PAIRS) return 2 * N * (l + u * G) < R;
+        return (2 * e < N ? o0[u] : o1[u]) < R;
     }
     // the channels of pair i's members
     __device__ __forceinline__ void channels(int i, int& a, int& b) const {
-        if (!VEC) pair_at(l + i * G, R, PAIRS, a, b);
-        else if (!PAIRS) a = o0 + i, b = o1 + i;
-        else a = (2 * i < NP ? o0 : o1) + 2 * (i % (NP / 2)), b = a + 1;
+        const int u = i / N, e = i % N;
+        if (N == 1) a = o0[u], b = o1[u];
+        else if (!PAIRS) a = o0[u] + e, b = o1[u] + e;
+        else a = (2 * e < N ? o0[u] : o1[u]) + 2 * (e % (N / 2 > 0 ? N / 2 : 1)), b = a + 1;
     }
-    struct Raw { Pack<E, NP> a, b; };
-    // one element at a time
+    struct Raw { Pack<E, N> a[U], b[U]; };
+    // straight from memory (single pairs)
     __device__ __forceinline__ Raw load(const void* base, int64_t at, bool use) const {
         Raw r;
         const E* p = static_cast<const E*>(base) + at;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            r.a.e[i] = r.b.e[i] = rp_cast<E>(0.f);
-            if (has(i) && use) {
-                int ca, cb;
-                channels(i, ca, cb);
-                r.a.e[i] = p[ca];
-                r.b.e[i] = p[cb];
+        for (int u = 0; u < U; ++u) {
+            r.a[u] = r.b[u] = Pack<E, N>{};
+            if (on(u) && use) {
+                r.a[u] = *reinterpret_cast<const Pack<E, N>*>(p + o0[u]);
+                r.b[u] = *reinterpret_cast<const Pack<E, N>*>(p + o1[u]);
             }
         }
         return r;
@@ -145,14 +155,21 @@ struct Lane {
         Row<NP> v;
 #pragma unroll
         for (int i = 0; i < NP / 2; ++i) {
-            if (VEC && PAIRS) {
-                const Pack<E, NP>& n = 4 * i < NP ? r.a : r.b;
-                const int k = (4 * i) % NP;
+            const int u = 2 * i / N, e = 2 * i % N;
+            if constexpr (N == 1) {
+                v.x[i] = pk2(ssm_f<E>(r.a[2 * i].e[0]), ssm_f<E>(r.a[2 * i + 1].e[0]));
+                v.y[i] = pk2(ssm_f<E>(r.b[2 * i].e[0]), ssm_f<E>(r.b[2 * i + 1].e[0]));
+            } else if constexpr (PAIRS && N == 2) {  // one pair a pack
+                v.x[i] = pk2(ssm_f<E>(r.a[u].e[0]), ssm_f<E>(r.b[u].e[0]));
+                v.y[i] = pk2(ssm_f<E>(r.a[u].e[1]), ssm_f<E>(r.b[u].e[1]));
+            } else if constexpr (PAIRS) {
+                const Pack<E, N>& n = 2 * e < N ? r.a[u] : r.b[u];
+                const int k = 2 * e % N;
                 v.x[i] = pk2(ssm_f<E>(n.e[k]), ssm_f<E>(n.e[k + 2]));
                 v.y[i] = pk2(ssm_f<E>(n.e[k + 1]), ssm_f<E>(n.e[k + 3]));
             } else {
-                v.x[i] = pk2(ssm_f<E>(r.a.e[2 * i]), ssm_f<E>(r.a.e[2 * i + 1]));
-                v.y[i] = pk2(ssm_f<E>(r.b.e[2 * i]), ssm_f<E>(r.b.e[2 * i + 1]));
+                v.x[i] = pk2(ssm_f<E>(r.a[u].e[e]), ssm_f<E>(r.a[u].e[e + 1]));
+                v.y[i] = pk2(ssm_f<E>(r.b[u].e[e]), ssm_f<E>(r.b[u].e[e + 1]));
             }
         }
         return v;
@@ -165,25 +182,22 @@ struct Lane {
             up2(v.x[i], x[2 * i], x[2 * i + 1]);
             up2(v.y[i], y[2 * i], y[2 * i + 1]);
         }
-        if constexpr (VEC) {
-            if (!on) return;
-            Pack<E, NP> a, b;
 #pragma unroll
-            for (int i = 0; i < NP / 2; ++i) {
-                rp_put<E>(a.e + 2 * i, PAIRS ? pk2(x[i], y[i]) : v.x[i]);
-                rp_put<E>(b.e + 2 * i, PAIRS ? pk2(x[NP / 2 + i], y[NP / 2 + i]) : v.y[i]);
-            }
-            *reinterpret_cast<Pack<E, NP>*>(p + o0) = a;
-            *reinterpret_cast<Pack<E, NP>*>(p + o1) = b;
-        } else {
+        for (int u = 0; u < U; ++u) {
+            if (!on(u)) continue;
+            Pack<E, N> a, b;
+            if constexpr (N == 1) {
+                a.e[0] = rp_cast<E>(x[u]), b.e[0] = rp_cast<E>(y[u]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (has(i)) {
-                    int ca, cb;
-                    channels(i, ca, cb);
-                    p[ca] = rp_cast<E>(x[i]);
-                    p[cb] = rp_cast<E>(y[i]);
+                for (int e = 0; e < N; e += 2) {
+                    const int i = u * N + e, k = u * N + e / 2;
+                    rp_put<E>(a.e + e, PAIRS ? pk2(x[k], y[k]) : v.x[i / 2]);
+                    rp_put<E>(b.e + e, PAIRS ? pk2(x[k + N / 2], y[k + N / 2]) : v.y[i / 2]);
                 }
+            }
+            *reinterpret_cast<Pack<E, N>*>(p + o0[u]) = a;
+            *reinterpret_cast<Pack<E, N>*>(p + o1[u]) = b;
         }
     }
     // fp32 parameters of the lane's channels (w null: ones)
@@ -208,7 +222,7 @@ struct Lane {
 template <int BYTES>
 __device__ __forceinline__ void cp_bytes(void* smem, const void* gmem) {
     if constexpr (BYTES == 16) cp16(smem, gmem);
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(smem)), "l"(gmem));
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES));
 }
 
 template <int N>
@@ -227,18 +241,20 @@ __device__ __forceinline__ f2 twice(float x) { return pk2(x, x); }
 // Rows ahead in the ring, and blocks of a multiprocessor that its shared memory is sized for
 template <bool BWD> constexpr int rp_depth() { return BWD ? 4 : 8; }
 constexpr int RP_OCCUPANCY = 2;
-template <bool BWD> constexpr size_t rp_smem(int pack_bytes) {
-    return size_t(rp_depth<BWD>()) * (BWD ? 4 : 2) * pack_bytes * RP_THREADS;
+template <bool BWD> constexpr size_t rp_smem(int row_bytes) {  // bytes of both packs of a lane's units
+    return size_t(rp_depth<BWD>()) * (BWD ? 2 : 1) * row_bytes * RP_THREADS;
 }
 
 // BWD: inputs and gradients in, gradients out; otherwise inputs in, turned out.  The first side[0].blocks blocks do q, the
 // others k.  tokens = groups / per_token tokens a tile.
-template <class E, int NP, bool PAIRS, bool VEC, bool BWD>
+template <class E, int N, int U, bool PAIRS, bool BWD>
 __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, int G) {
-    using P = Pack<E, NP>;
+    using P = Pack<E, N>;
+    constexpr int NP = N * U;
+    constexpr bool RING = N > 1;
     constexpr int DEPTH = rp_depth<BWD>(), ROWS = BWD ? 1 : 2;  // ROWS rows of a group are worked on together
     extern __shared__ __align__(16) unsigned char ring_raw[];
-    P* ring = reinterpret_cast<P*>(ring_raw);  // [DEPTH][x, then g: two packs][thread]
+    P* ring = reinterpret_cast<P*>(ring_raw);  // [DEPTH][x, then g: two packs of every unit][thread]
     __shared__ __align__(16) float cs[RP_TOKENS][RP_MAXD];  // cosines of R / 2 pairs, then sines
     __shared__ unsigned long long turn[RP_MAXD / 2];        // turns_per_token of the pairs
     __shared__ int place[RP_TOKENS];                        // the tile's positions
@@ -246,7 +262,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     const int which = int(blockIdx.x) >= a.side[0].blocks;
     const RopeSide& sd = a.side[which];
     const int block = int(blockIdx.x) - (which ? a.side[0].blocks : 0);
-    const Lane<E, NP, PAIRS, VEC> L(lane, a.D, a.R, G);
+    const Lane<E, N, U, PAIRS> L(lane, a.D, a.R, G);
     const int half = a.R / 2, tokens = groups / a.per_token;
     const int own = group / a.per_token, first = group - own * a.per_token;
     const int rows = (sd.H + ROWS * a.per_token - 1) / (ROWS * a.per_token) * ROWS;  // of a group in a tile
@@ -255,25 +271,29 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) sum.x[i] = sum.y[i] = twice(0.f);
     const int64_t tiles = (a.T + tokens - 1) / tokens;
-    auto slot = [&](int d, int k) { return ring + (d * (BWD ? 4 : 2) + k) * RP_THREADS + tid; };
+    auto slot = [&](int d, int k, int u) { return ring + ((d * (BWD ? 4 : 2) + k) * U + u) * RP_THREADS + tid; };
     // the next row to be copied, and its place in the ring
     int64_t ahead = block;
     int ahead_row = 0, ahead_at = 0;
     auto copy_next = [&]() {
-        if constexpr (VEC) {
+        if constexpr (RING) {
             const int64_t t = ahead * tokens + own;
             const int h = ahead_row * a.per_token + first;
-            if (ahead < tiles && t < a.T && h < sd.H && L.on) {
-                if (!BWD || a.norm) {
-                    const E* p = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(h) * a.D;
-                    cp_bytes<sizeof(P)>(slot(ahead_at, 0), p + L.o0);
-                    cp_bytes<sizeof(P)>(slot(ahead_at, 1), p + L.o1);
-                }
-                if constexpr (BWD) {
-                    const E* p = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(h) * a.D;
-                    cp_bytes<sizeof(P)>(slot(ahead_at, 2), p + L.o0);
-                    cp_bytes<sizeof(P)>(slot(ahead_at, 3), p + L.o1);
-                }
+            if (ahead < tiles && t < a.T && h < sd.H) {
+                const E* x = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(h) * a.D;
+                const E* g = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(h) * a.D;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (L.on(u)) {
+                        if (!BWD || a.norm) {
+                            cp_bytes<sizeof(P)>(slot(ahead_at, 0, u), x + L.o0[u]);
+                            cp_bytes<sizeof(P)>(slot(ahead_at, 1, u), x + L.o1[u]);
+                        }
+                        if constexpr (BWD) {
+                            cp_bytes<sizeof(P)>(slot(ahead_at, 2, u), g + L.o0[u]);
+                            cp_bytes<sizeof(P)>(slot(ahead_at, 3, u), g + L.o1[u]);
+                        }
+                    }
             }
             cp_commit();
             ahead_at = ahead_at + 1 == DEPTH ? 0 : ahead_at + 1;
@@ -300,36 +320,31 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
         f2 c[NP / 2], s[NP / 2];
 #pragma unroll
         for (int i = 0; i < NP / 2; ++i) {
-            if constexpr (VEC) {
-                c[i] = twice(1.f), s[i] = twice(0.f);
-                if (L.turns(2 * i)) {  // (their pairs are neighbours, and R / 2 is even)
-                    c[i] = *reinterpret_cast<const f2*>(&cs[own][L.pair(2 * i)]);
-                    s[i] = *reinterpret_cast<const f2*>(&cs[own][half + L.pair(2 * i)]);
-                }
-            } else {
-                float u[4] = {1.f, 1.f, 0.f, 0.f};
+            float u[4] = {1.f, 1.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (L.has(2 * i + e) && L.turns(2 * i + e))
-                        u[e] = cs[own][L.pair(2 * i + e)], u[2 + e] = cs[own][half + L.pair(2 * i + e)];
-                c[i] = pk2(u[0], u[1]);
-                s[i] = pk2(u[2], u[3]);
-            }
+            for (int e = 0; e < 2; ++e)
+                if (L.has(2 * i + e) && L.turns(2 * i + e))
+                    u[e] = cs[own][L.pair(2 * i + e)], u[2 + e] = cs[own][half + L.pair(2 * i + e)];
+            c[i] = pk2(u[0], u[1]);
+            s[i] = pk2(u[2], u[3]);
         }
         const int64_t x0 = t * sd.ldx, g0 = t * sd.ldg, y0 = t * sd.ldo;
         // (every lane of a warp runs every round: the exchanges are warp-wide)
         for (int r0 = 0; r0 < rows; r0 += ROWS) {
-            typename Lane<E, NP, PAIRS, VEC>::Raw x[ROWS], g[ROWS];
-            if constexpr (VEC) cp_wait<DEPTH - ROWS>();
+            typename Lane<E, N, U, PAIRS>::Raw x[ROWS], g[ROWS];
+            if constexpr (RING) cp_wait<DEPTH - ROWS>();
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 const int h = (r0 + r) * a.per_token + first;
                 const bool use = live && h < sd.H;
-                if constexpr (VEC) {
-                    const bool full = use && L.on;  // (else what the ring holds is of no row)
+                if constexpr (RING) {
                     const P none{};
-                    if (!BWD || a.norm) x[r].a = full ? *slot(at, 0) : none, x[r].b = full ? *slot(at, 1) : none;
-                    if constexpr (BWD) g[r].a = full ? *slot(at, 2) : none, g[r].b = full ? *slot(at, 3) : none;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool full = use && L.on(u);  // (else what the ring holds is of no row)
+                        if (!BWD || a.norm) x[r].a[u] = full ? *slot(at, 0, u) : none, x[r].b[u] = full ? *slot(at, 1, u) : none;
+                        if constexpr (BWD) g[r].a[u] = full ? *slot(at, 2, u) : none, g[r].b[u] = full ? *slot(at, 3, u) : none;
+                    }
                     at = at + 1 == DEPTH ? 0 : at + 1;
                 } else {
                     if (!BWD || a.norm) x[r] = L.load(sd.x, x0 + int64_t(h) * a.D, use);
@@ -400,7 +415,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             }
         }
     }
-    if constexpr (VEC) cp_wait<0>();
+    if constexpr (RING) cp_wait<0>();
     if (BWD && sd.part) {  // the groups' sums, added in their order
         float* red = &cs[0][0];
         for (int gi = 0; gi < groups; ++gi) {
@@ -460,10 +475,10 @@ kda_status check_problem(const kda_rope_problem* p) {
     return KDA_OK;
 }
 
-template <class E, int NP, bool VEC, bool BWD>
+template <class E, int N, int U, bool BWD>
 void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     int G = 1;
-    while (G < 32 && G * (VEC ? 2 * NP : 2) < a.D) G *= 2;
+    while (G < 32 && G * 2 * N * (N == 1 ? 1 : U) < a.D) G *= 2;  // (single pairs: as many lanes as there are)
     const int groups = RP_THREADS / G, H = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
     constexpr int most = RP_SMS * RP_OCCUPANCY;
     // a group takes 8 heads of a token, fewer where that leaves less than a wave of blocks; tiles of at most RP_TOKENS
@@ -483,8 +498,8 @@ void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     const unsigned grid = unsigned(a.side[0].blocks + a.side[1].blocks);
     {
         static unsigned long long done[2];
-        const size_t smem = VEC ? rp_smem<BWD>(int(sizeof(Pack<E, NP>))) : 0;
-        auto* kernel = pairs ? k_rope<E, NP, true, VEC, BWD> : k_rope<E, NP, false, VEC, BWD>;
+        const size_t smem = N > 1 ? rp_smem<BWD>(2 * U * int(sizeof(Pack<E, N>))) : 0;
+        auto* kernel = pairs ? k_rope<E, N, U, true, BWD> : k_rope<E, N, U, false, BWD>;
         // (the limit counts the static part too)
         allow_smem(reinterpret_cast<const void*>(kernel), smem + RP_TOKENS * RP_MAXD * sizeof(float), &done[pairs]);
         ProfScope ps(BWD ? KK_ROPE_BWD : KK_ROPE_FWD, st);
@@ -499,8 +514,8 @@ void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
 template <class E, bool BWD>
 void launch(const RopeArgs& a, int layout, cudaStream_t st) {
     constexpr int V = 16 / int(sizeof(E));
-    // whole 16-byte accesses where the channels and every row allow them, 8-byte ones of 16-bit rows, else one pair at
-    // a time
+    // the widest packs that the channels and every row allow: 16 bytes a lane, or several units of 8 or 4, or pairs
+    // one at a time
     auto fits = [&](int n) {
         if (a.D % (2 * n) || a.R % (2 * n)) return false;
         for (const RopeSide& s : a.side)
@@ -510,9 +525,10 @@ void launch(const RopeArgs& a, int layout, cudaStream_t st) {
         return true;
     };
     const bool pairs = layout == KDA_ROPE_PAIRS;
-    if (fits(V)) launch_as<E, V, true, BWD>(a, pairs, st);
-    else if (V == 8 && fits(4)) launch_as<E, 4, true, BWD>(a, pairs, st);
-    else launch_as<E, 4, false, BWD>(a, pairs, st);
+    if (fits(V)) launch_as<E, V, 1, BWD>(a, pairs, st);
+    else if (V == 8 && fits(4)) launch_as<E, 4, V / 4, BWD>(a, pairs, st);
+    else if (fits(2)) launch_as<E, 2, V / 2, BWD>(a, pairs, st);
+    else launch_as<E, 1, 4, BWD>(a, pairs, st);
 }
 
 template <bool BWD>
