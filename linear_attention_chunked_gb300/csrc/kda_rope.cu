@@ -241,17 +241,22 @@ __device__ __forceinline__ f2 twice(float x) { return pk2(x, x); }
 // Rows ahead in the ring, and blocks of a multiprocessor that its shared memory is sized for
 template <bool BWD> constexpr int rp_depth() { return BWD ? 4 : 8; }
 constexpr int RP_OCCUPANCY = 2;
+// words of a lane's single pairs, and one more that keeps the groups' rows in banks of their own
+template <class E, int U> constexpr int rp_words() { return U * int(sizeof(E)) / 2; }
 template <bool BWD> constexpr size_t rp_smem(int row_bytes) {  // bytes of both packs of a lane's units
     return size_t(rp_depth<BWD>()) * (BWD ? 2 : 1) * row_bytes * RP_THREADS;
 }
 
 // BWD: inputs and gradients in, gradients out; otherwise inputs in, turned out.  The first side[0].blocks blocks do q, the
 // others k.  tokens = groups / per_token tokens a tile.
-template <class E, int N, int U, bool PAIRS, bool BWD>
+// AHEAD: rows come through the ring, for N = 1 as whole words of which a group's lanes then pick their pairs, and go out as
+// words too; else (rows that no word fits) element by element.
+template <class E, int N, int U, bool PAIRS, bool BWD, bool AHEAD>
 __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, int G) {
     using P = Pack<E, N>;
     constexpr int NP = N * U;
-    constexpr bool RING = N > 1;
+    constexpr bool RING = AHEAD && N > 1, WORDS = AHEAD && N == 1;
+    constexpr int WU = rp_words<E, U>();
     constexpr int DEPTH = rp_depth<BWD>(), ROWS = BWD ? 1 : 2;  // ROWS rows of a group are worked on together
     extern __shared__ __align__(16) unsigned char ring_raw[];
     P* ring = reinterpret_cast<P*>(ring_raw);  // [DEPTH][x, then g: two packs of every unit][thread]
@@ -272,19 +277,34 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     for (int i = 0; i < NP / 2; ++i) sum.x[i] = sum.y[i] = twice(0.f);
     const int64_t tiles = (a.T + tokens - 1) / tokens;
     auto slot = [&](int d, int k, int u) { return ring + ((d * (BWD ? 4 : 2) + k) * U + u) * RP_THREADS + tid; };
+    // WORDS: [DEPTH][x, then g][group][word], then a row of every group on its way out
+    const int row_words = a.D * int(sizeof(E)) / 4;
+    auto words = [&](int d, int k) {
+        return reinterpret_cast<uint32_t*>(ring_raw) + ((d * (BWD ? 2 : 1) + k) * groups + group) * (G * (WU + 1));
+    };
     // the next row to be copied, and its place in the ring
     int64_t ahead = block;
     int ahead_row = 0, ahead_at = 0;
     auto copy_next = [&]() {
-        if constexpr (RING) {
+        if constexpr (AHEAD) {
             const int64_t t = ahead * tokens + own;
             const int h = ahead_row * a.per_token + first;
             if (ahead < tiles && t < a.T && h < sd.H) {
                 const E* x = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(h) * a.D;
                 const E* g = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(h) * a.D;
+                if constexpr (WORDS) {
+#pragma unroll
+                    for (int i = 0; i < WU; ++i) {
+                        const int k = lane + i * G;
+                        if (k < row_words) {
+                            if (!BWD || a.norm) cp_bytes<4>(words(ahead_at, 0) + k, reinterpret_cast<const uint32_t*>(x) + k);
+                            if constexpr (BWD) cp_bytes<4>(words(ahead_at, 1) + k, reinterpret_cast<const uint32_t*>(g) + k);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (L.on(u)) {
+                    if (RING && L.on(u)) {
                         if (!BWD || a.norm) {
                             cp_bytes<sizeof(P)>(slot(ahead_at, 0, u), x + L.o0[u]);
                             cp_bytes<sizeof(P)>(slot(ahead_at, 1, u), x + L.o1[u]);
@@ -332,7 +352,8 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
         // (every lane of a warp runs every round: the exchanges are warp-wide)
         for (int r0 = 0; r0 < rows; r0 += ROWS) {
             typename Lane<E, N, U, PAIRS>::Raw x[ROWS], g[ROWS];
-            if constexpr (RING) cp_wait<DEPTH - ROWS>();
+            if constexpr (AHEAD) cp_wait<DEPTH - ROWS>();
+            if constexpr (WORDS) __syncwarp();  // the other lanes' words
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 const int h = (r0 + r) * a.per_token + first;
@@ -346,11 +367,26 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                         if constexpr (BWD) g[r].a[u] = full ? *slot(at, 2, u) : none, g[r].b[u] = full ? *slot(at, 3, u) : none;
                     }
                     at = at + 1 == DEPTH ? 0 : at + 1;
+                } else if constexpr (WORDS) {
+                    const E *px = reinterpret_cast<const E*>(words(at, 0)), *pg = reinterpret_cast<const E*>(words(at, BWD ? 1 : 0));
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool full = use && L.on(u);
+                        const P none{};
+                        x[r].a[u] = x[r].b[u] = none;
+                        if (full && (!BWD || a.norm)) x[r].a[u].e[0] = px[L.o0[u]], x[r].b[u].e[0] = px[L.o1[u]];
+                        if constexpr (BWD) {
+                            g[r].a[u] = g[r].b[u] = none;
+                            if (full) g[r].a[u].e[0] = pg[L.o0[u]], g[r].b[u].e[0] = pg[L.o1[u]];
+                        }
+                    }
+                    at = at + 1 == DEPTH ? 0 : at + 1;
                 } else {
                     if (!BWD || a.norm) x[r] = L.load(sd.x, x0 + int64_t(h) * a.D, use);
                     if (BWD) g[r] = L.load(sd.g, g0 + int64_t(h) * a.D, use);
                 }
             }
+            if constexpr (WORDS) __syncwarp();  // read by every lane, before the places are filled again
             Row<NP> v[ROWS], o[ROWS];
             float all[2 * ROWS];  // the rows' sums over channels: x^2, and g x (backward)
 #pragma unroll
@@ -411,11 +447,22 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                     }
                 }
                 copy_next();  // into a place just read
-                if (use) L.store(sd.out, y0 + int64_t(h) * a.D, o[r]);
+                if constexpr (WORDS) {
+                    uint32_t* out = words(DEPTH, 0);
+                    L.store(out, 0, o[r]);
+                    __syncwarp();
+                    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<E*>(sd.out) + y0 + int64_t(h) * a.D);
+#pragma unroll
+                    for (int i = 0; i < WU; ++i)
+                        if (use && lane + i * G < row_words) to[lane + i * G] = out[lane + i * G];
+                    __syncwarp();
+                } else if (use) {
+                    L.store(sd.out, y0 + int64_t(h) * a.D, o[r]);
+                }
             }
         }
     }
-    if constexpr (RING) cp_wait<0>();
+    if constexpr (AHEAD) cp_wait<0>();
     if (BWD && sd.part) {  // the groups' sums, added in their order
         float* red = &cs[0][0];
         for (int gi = 0; gi < groups; ++gi) {
@@ -475,10 +522,10 @@ kda_status check_problem(const kda_rope_problem* p) {
     return KDA_OK;
 }
 
-template <class E, int N, int U, bool BWD>
+template <class E, int N, int U, bool BWD, bool AHEAD>
 void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     int G = 1;
-    while (G < 32 && G * 2 * N * (N == 1 ? 1 : U) < a.D) G *= 2;  // (single pairs: as many lanes as there are)
+    while (G < 32 && G * 2 * N * (AHEAD ? U : 1) < a.D) G *= 2;  // (straight from memory: as many lanes as there are pairs)
     const int groups = RP_THREADS / G, H = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
     constexpr int most = RP_SMS * RP_OCCUPANCY;
     // a group takes 8 heads of a token, fewer where that leaves less than a wave of blocks; tiles of at most RP_TOKENS
@@ -498,8 +545,9 @@ void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     const unsigned grid = unsigned(a.side[0].blocks + a.side[1].blocks);
     {
         static unsigned long long done[2];
-        const size_t smem = N > 1 ? rp_smem<BWD>(2 * U * int(sizeof(Pack<E, N>))) : 0;
-        auto* kernel = pairs ? k_rope<E, N, U, true, BWD> : k_rope<E, N, U, false, BWD>;
+        const size_t smem = !AHEAD ? 0 : N > 1 ? rp_smem<BWD>(2 * U * int(sizeof(Pack<E, N>)))
+                                               : rp_smem<BWD>(4 * (rp_words<E, U>() + 1)) + 4 * (rp_words<E, U>() + 1) * RP_THREADS;
+        auto* kernel = pairs ? k_rope<E, N, U, true, BWD, AHEAD> : k_rope<E, N, U, false, BWD, AHEAD>;
         // (the limit counts the static part too)
         allow_smem(reinterpret_cast<const void*>(kernel), smem + RP_TOKENS * RP_MAXD * sizeof(float), &done[pairs]);
         ProfScope ps(BWD ? KK_ROPE_BWD : KK_ROPE_FWD, st);
@@ -516,8 +564,8 @@ void launch(const RopeArgs& a, int layout, cudaStream_t st) {
     constexpr int V = 16 / int(sizeof(E));
     // the widest packs that the channels and every row allow: 16 bytes a lane, or several units of 8 or 4, or pairs
     // one at a time
-    auto fits = [&](int n) {
-        if (a.D % (2 * n) || a.R % (2 * n)) return false;
+    auto fits = [&](int n, bool whole) {  // whole: rows of words, whatever the turned part
+        if (!whole && (a.D % (2 * n) || a.R % (2 * n))) return false;
         for (const RopeSide& s : a.side)
             if (s.H && (!al(s.x, n * sizeof(E)) || s.ldx % n || !al(s.g, n * sizeof(E)) || s.ldg % n ||
                         !al(s.out, n * sizeof(E)) || s.ldo % n))
@@ -525,10 +573,11 @@ void launch(const RopeArgs& a, int layout, cudaStream_t st) {
         return true;
     };
     const bool pairs = layout == KDA_ROPE_PAIRS;
-    if (fits(V)) launch_as<E, V, 1, BWD>(a, pairs, st);
-    else if (V == 8 && fits(4)) launch_as<E, 4, V / 4, BWD>(a, pairs, st);
-    else if (fits(2)) launch_as<E, 2, V / 2, BWD>(a, pairs, st);
-    else launch_as<E, 1, 4, BWD>(a, pairs, st);
+    if (fits(V, false)) launch_as<E, V, 1, BWD, true>(a, pairs, st);
+    else if (V == 8 && fits(4, false)) launch_as<E, 4, V / 4, BWD, true>(a, pairs, st);
+    else if (fits(2, false)) launch_as<E, 2, V / 2, BWD, true>(a, pairs, st);
+    else if (fits(4 / int(sizeof(E)), true)) launch_as<E, 1, V, BWD, true>(a, pairs, st);
+    else launch_as<E, 1, 4, BWD, false>(a, pairs, st);
 }
 
 template <bool BWD>
