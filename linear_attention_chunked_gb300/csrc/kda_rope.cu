@@ -34,6 +34,7 @@ struct RopeSide {
     float* dw;
     int64_t ldx, ldg, ldo;  // token strides
     int H;
+    int per_token;      // groups of a block that share a token's heads
     int blocks;         // of the launch
     float* part;        // [blocks][D] partial dw
 };
@@ -43,7 +44,6 @@ struct RopeArgs {
     float eps, scale, inv_d;
     const int* pos;
     const double* freq;
-    int per_token;      // groups that share a token's heads
     RopeSide side[2];
 };
 
@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     const RopeSide& sd = a.side[which];
     const int block = int(blockIdx.x) - (which ? a.side[0].blocks : 0);
     const Lane<E, N, U, PAIRS> L(lane, a.D, a.R, G);
-    const int half = a.R / 2, tokens = groups / a.per_token;
-    const int own = group / a.per_token, first = group - own * a.per_token;
-    const int rows = (sd.H + ROWS * a.per_token - 1) / (ROWS * a.per_token) * ROWS;  // of a group in a tile
+    const int half = a.R / 2, tokens = groups / sd.per_token;
+    const int own = group / sd.per_token, first = group - own * sd.per_token;
+    const int rows = (sd.H + ROWS * sd.per_token - 1) / (ROWS * sd.per_token) * ROWS;  // of a group in a tile
     const Row<NP> w = L.weights(a.norm ? sd.w : nullptr);
     Row<NP> sum;  // of dw
 #pragma unroll
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     auto copy_next = [&]() {
         if constexpr (AHEAD) {
             const int64_t t = ahead * tokens + own;
-            const int h = ahead_row * a.per_token + first;
+            const int h = ahead_row * sd.per_token + first;
             if (ahead < tiles && t < a.T && h < sd.H) {
                 const E* x = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(h) * a.D;
                 const E* g = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(h) * a.D;
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             if constexpr (WORDS) __syncwarp();  // the other lanes' words
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const int h = (r0 + r) * a.per_token + first;
+                const int h = (r0 + r) * sd.per_token + first;
                 const bool use = live && h < sd.H;
                 if constexpr (RING) {
                     const P none{};
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const int h = (r0 + r) * a.per_token + first;
+                const int h = (r0 + r) * sd.per_token + first;
                 const bool use = live && h < sd.H;
                 const float rs = rsqrtf(fmaf(all[r], a.inv_d, a.eps));
                 const f2 rs2 = twice(rs);
@@ -526,19 +526,17 @@ template <class E, int N, int U, bool BWD, bool AHEAD>
 void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     int G = 1;
     while (G < 32 && G * 2 * N * (AHEAD ? U : 1) < a.D) G *= 2;  // (straight from memory: as many lanes as there are pairs)
-    const int groups = RP_THREADS / G, H = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
+    const int groups = RP_THREADS / G, all = a.side[0].H + a.side[1].H;
     constexpr int most = RP_SMS * RP_OCCUPANCY;
-    // a group takes 8 heads of a token, fewer where that leaves less than a wave of blocks; tiles of at most RP_TOKENS
-    // tokens
-    int per = 1;
-    while (per < groups && (groups / per > RP_TOKENS || H > 8 * per)) per *= 2;
-    while (per < groups && per < H && a.T * per < int64_t(most) * groups) per *= 2;
-    a.per_token = per;
-    const int64_t tiles = (a.T + groups / per - 1) / (groups / per);
-    // blocks in proportion to the heads
-    const int all = a.side[0].H + a.side[1].H;
     for (RopeSide& s : a.side) {
+        // blocks in proportion to the heads
         const int64_t share = (int64_t(most) * s.H + all - 1) / all;
+        // a group takes 8 heads of a token, fewer where that leaves blocks without a tile; tiles of at most RP_TOKENS tokens
+        int per = 1;
+        while (per < groups && (groups / per > RP_TOKENS || s.H > 8 * per)) per *= 2;
+        while (per < groups && per < s.H && a.T * per < share * groups) per *= 2;
+        const int64_t tiles = (a.T + groups / per - 1) / (groups / per);
+        s.per_token = per;
         s.blocks = int(s.H == 0 ? 0 : share < tiles ? share : tiles);
     }
     if (a.side[1].part) a.side[1].part = a.side[0].part + size_t(a.side[0].blocks) * a.D;
