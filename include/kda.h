@@ -374,13 +374,14 @@ kda_status kda_layernorm_bwd(const kda_layernorm_problem* p, const void* x, cons
  * formula says).  States h0, ht, dht, dh0 are fp32 [N, H, 128, 128] indexed [key][value]; h0 nullable
  * (zero), ht nullable.  The states and every sum are fp32; an empty document's ht is its h0 and its dh0 its dht.
  * A document's results do not depend on the rest of the pack and are bitwise reproducible.  What is not finite in a
- * document's rows reaches that document alone (earlier tokens of the same 128 among them).
+ * document's rows reaches that document alone (earlier tokens of the same 128 among them).  Outputs overlap no input.
  *
  * kda_linattn_fwd with a non-NULL saved buffer leaves there what kda_linattn_bwd needs besides the inputs
  * (saved = NULL there recomputes it).  The backward is that of L = sum(o * dO) + sum(ht * dht): dq, dk
  * [T, Hk, 128] (the sums over the heads that share them), dv [T, H, 128] bf16, dh0 (nullable); dht nullable.
- * A saved set that was written for other sizes sets the device status KDA_ERR_DEVICE_CHECK and the backward
- * writes nothing; so do malformed cu_seqlens in both.  Workspace sizes (op: KDA_OP_FWD, KDA_OP_BWD_SAVED,
+ * A saved set serves the inputs of the forward that wrote it: one written for other sizes, or by no forward,
+ * sets the device status KDA_ERR_DEVICE_CHECK and the backward writes nothing.  Malformed cu_seqlens set the same
+ * status; what the call writes is then unspecified.  Workspace sizes (op: KDA_OP_FWD, KDA_OP_BWD_SAVED,
  * KDA_OP_BWD_REPLAY) depend on T, N, H, Hk only; KDA_OP_FWD's serves with and without a saved set.  The
  * first call on a device sets it up: make it before any stream capture. */
 typedef struct kda_linattn_problem {
@@ -418,7 +419,8 @@ kda_status kda_linattn_step(const kda_linattn_problem* p, const void* q, const v
  *     layout KDA_ROPE_HALF pairs channels (i, R / 2 + i), KDA_ROPE_PAIRS channels (2 i, 2 i + 1);
  *     channels from R on are not turned (nor scaled).
  * q [T, Hq, D] and k [T, Hk, D] are of p->dtype, inputs with token strides ld_q, ld_k and outputs with
- * ld_qo, ld_ko (elements; 0 = dense; element alignment); an output may be its input.  pos int32 [T] are any
+ * ld_qo, ld_ko (elements; 0 = dense; element alignment); an output may be its input, row for row, and overlaps no
+ * input otherwise.  pos int32 [T] are any
  * positions; freq fp64 [R / 2] is in radians per token (kda_rope_frequencies).  An angle is reduced in
  * 64-bit integers, so far positions keep their accuracy.  Arithmetic is fp32, rounded once.  Hq or Hk may
  * be 0 (that tensor is not read).
