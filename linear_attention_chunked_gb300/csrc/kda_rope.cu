@@ -72,17 +72,47 @@ __device__ __forceinline__ void cos_sin(int pos, unsigned long long F, float sca
     s *= scale;
 }
 
-template <class E, int N> struct alignas(N * sizeof(E)) Pack { E e[N]; };
 template <class E> __device__ __forceinline__ E rp_cast(float v);
 template <> __device__ __forceinline__ float rp_cast<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 rp_cast<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half rp_cast<__half>(float v) { return __float2half_rn(v); }
-// two values as one store's neighbours
-template <class E> __device__ __forceinline__ void rp_put(E* e, f2 v) {
-    float a, b;
-    up2(v, a, b);
-    e[0] = rp_cast<E>(a);
-    e[1] = rp_cast<E>(b);
+// Two neighbours of a 16-bit type as the word that they are, one instruction each way (element by element it is three)
+template <class E> __device__ __forceinline__ float word_lo(uint32_t w);
+template <class E> __device__ __forceinline__ float word_hi(uint32_t w);
+template <class E> __device__ __forceinline__ uint32_t word_of(float lo, float hi);
+template <> __device__ __forceinline__ float word_lo<__nv_bfloat16>(uint32_t w) { return __uint_as_float(w << 16); }
+template <> __device__ __forceinline__ float word_hi<__nv_bfloat16>(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+template <> __device__ __forceinline__ uint32_t word_of<__nv_bfloat16>(float lo, float hi) { return pack2(lo, hi); }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+template <> __device__ __forceinline__ float word_lo<__half>(uint32_t w) { return __low2float(as_half2(w)); }
+template <> __device__ __forceinline__ float word_hi<__half>(uint32_t w) { return __high2float(as_half2(w)); }
+template <> __device__ __forceinline__ uint32_t word_of<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// N consecutive elements: words where they fill them
+template <class E, int N> struct alignas(N * sizeof(E)) Pack { uint32_t w[N * sizeof(E) / 4]; };
+template <> struct alignas(2) Pack<__nv_bfloat16, 1> { __nv_bfloat16 e; };
+template <> struct alignas(2) Pack<__half, 1> { __half e; };
+template <class E, int N>
+__device__ __forceinline__ float pack_get(const Pack<E, N>& p, int i) {
+    if constexpr (sizeof(E) == 4) return __uint_as_float(p.w[i]);
+    else if constexpr (N == 1) return ssm_f<E>(p.e);
+    else return i & 1 ? word_hi<E>(p.w[i / 2]) : word_lo<E>(p.w[i / 2]);
+}
+// elements i and i + 1
+template <class E, int N>
+__device__ __forceinline__ void pack_put2(Pack<E, N>& p, int i, float a, float b) {
+    if constexpr (sizeof(E) == 4) p.w[i] = __float_as_uint(a), p.w[i + 1] = __float_as_uint(b);
+    else p.w[i / 2] = word_of<E>(a, b);
+}
+template <class E>
+__device__ __forceinline__ Pack<E, 1> pack_one(float a) {
+    Pack<E, 1> p;
+    if constexpr (sizeof(E) == 4) p.w[0] = __float_as_uint(a);
+    else p.e = rp_cast<E>(a);
+    return p;
 }
 
 // Channels of pair p of a row (p >= R / 2: channels that are not turned, two by two)
@@ -157,19 +187,19 @@ struct Lane {
         for (int i = 0; i < NP / 2; ++i) {
             const int u = 2 * i / N, e = 2 * i % N;
             if constexpr (N == 1) {
-                v.x[i] = pk2(ssm_f<E>(r.a[2 * i].e[0]), ssm_f<E>(r.a[2 * i + 1].e[0]));
-                v.y[i] = pk2(ssm_f<E>(r.b[2 * i].e[0]), ssm_f<E>(r.b[2 * i + 1].e[0]));
+                v.x[i] = pk2(pack_get<E, N>(r.a[2 * i], 0), pack_get<E, N>(r.a[2 * i + 1], 0));
+                v.y[i] = pk2(pack_get<E, N>(r.b[2 * i], 0), pack_get<E, N>(r.b[2 * i + 1], 0));
             } else if constexpr (PAIRS && N == 2) {  // one pair a pack
-                v.x[i] = pk2(ssm_f<E>(r.a[u].e[0]), ssm_f<E>(r.b[u].e[0]));
-                v.y[i] = pk2(ssm_f<E>(r.a[u].e[1]), ssm_f<E>(r.b[u].e[1]));
+                v.x[i] = pk2(pack_get<E, N>(r.a[u], 0), pack_get<E, N>(r.b[u], 0));
+                v.y[i] = pk2(pack_get<E, N>(r.a[u], 1), pack_get<E, N>(r.b[u], 1));
             } else if constexpr (PAIRS) {
                 const Pack<E, N>& n = 2 * e < N ? r.a[u] : r.b[u];
                 const int k = 2 * e % N;
-                v.x[i] = pk2(ssm_f<E>(n.e[k]), ssm_f<E>(n.e[k + 2]));
-                v.y[i] = pk2(ssm_f<E>(n.e[k + 1]), ssm_f<E>(n.e[k + 3]));
+                v.x[i] = pk2(pack_get<E, N>(n, k), pack_get<E, N>(n, k + 2));
+                v.y[i] = pk2(pack_get<E, N>(n, k + 1), pack_get<E, N>(n, k + 3));
             } else {
-                v.x[i] = pk2(ssm_f<E>(r.a[u].e[e]), ssm_f<E>(r.a[u].e[e + 1]));
-                v.y[i] = pk2(ssm_f<E>(r.b[u].e[e]), ssm_f<E>(r.b[u].e[e + 1]));
+                v.x[i] = pk2(pack_get<E, N>(r.a[u], e), pack_get<E, N>(r.a[u], e + 1));
+                v.y[i] = pk2(pack_get<E, N>(r.b[u], e), pack_get<E, N>(r.b[u], e + 1));
             }
         }
         return v;
@@ -187,13 +217,18 @@ struct Lane {
             if (!on(u)) continue;
             Pack<E, N> a, b;
             if constexpr (N == 1) {
-                a.e[0] = rp_cast<E>(x[u]), b.e[0] = rp_cast<E>(y[u]);
+                a = pack_one<E>(x[u]), b = pack_one<E>(y[u]);
             } else {
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
                     const int i = u * N + e, k = u * N + e / 2;
-                    rp_put<E>(a.e + e, PAIRS ? pk2(x[k], y[k]) : v.x[i / 2]);
-                    rp_put<E>(b.e + e, PAIRS ? pk2(x[k + N / 2], y[k + N / 2]) : v.y[i / 2]);
+                    if (PAIRS) {
+                        pack_put2<E, N>(a, e, x[k], y[k]);
+                        pack_put2<E, N>(b, e, x[k + N / 2], y[k + N / 2]);
+                    } else {
+                        pack_put2<E, N>(a, e, x[i], x[i + 1]);
+                        pack_put2<E, N>(b, e, y[i], y[i + 1]);
+                    }
                 }
             }
             *reinterpret_cast<Pack<E, N>*>(p + o0[u]) = a;
@@ -282,16 +317,22 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     auto words = [&](int d, int k) {
         return reinterpret_cast<uint32_t*>(ring_raw) + ((d * (BWD ? 2 : 1) + k) * groups + group) * (G * (WU + 1));
     };
-    // the next row to be copied, and its place in the ring
+    // the next row to be copied (its tile, place in the tile, head and addresses), and its place in the ring
+    const int step = sd.per_token * a.D;  // elements from a group's row to its next
     int64_t ahead = block;
     int ahead_row = 0, ahead_at = 0;
+    const E *ahead_x = nullptr, *ahead_g = nullptr;
+    int ahead_heads = 0;  // rows that the group has in the tile
     auto copy_next = [&]() {
         if constexpr (AHEAD) {
-            const int64_t t = ahead * tokens + own;
-            const int h = ahead_row * sd.per_token + first;
-            if (ahead < tiles && t < a.T && h < sd.H) {
-                const E* x = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(h) * a.D;
-                const E* g = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(h) * a.D;
+            if (ahead_row == 0) {
+                const int64_t t = ahead * tokens + own;
+                ahead_heads = ahead < tiles && t < a.T ? (sd.H - first + sd.per_token - 1) / sd.per_token : 0;
+                if (!BWD || a.norm) ahead_x = static_cast<const E*>(sd.x) + t * sd.ldx + int64_t(first) * a.D;
+                if (BWD) ahead_g = static_cast<const E*>(sd.g) + t * sd.ldg + int64_t(first) * a.D;
+            }
+            if (ahead_row < ahead_heads) {
+                const E *x = ahead_x, *g = ahead_g;
                 if constexpr (WORDS) {
 #pragma unroll
                     for (int i = 0; i < WU; ++i) {
@@ -317,6 +358,8 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             }
             cp_commit();
             ahead_at = ahead_at + 1 == DEPTH ? 0 : ahead_at + 1;
+            ahead_x += step;
+            ahead_g += step;
             if (++ahead_row == rows) ahead_row = 0, ahead += sd.blocks;
         }
     };
@@ -348,7 +391,8 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             c[i] = pk2(u[0], u[1]);
             s[i] = pk2(u[2], u[3]);
         }
-        const int64_t x0 = t * sd.ldx, g0 = t * sd.ldg, y0 = t * sd.ldo;
+        const int64_t x0 = t * sd.ldx, g0 = t * sd.ldg;
+        E* out = static_cast<E*>(sd.out) + t * sd.ldo + int64_t(first) * a.D;  // of the next row
         // (every lane of a warp runs every round: the exchanges are warp-wide)
         for (int r0 = 0; r0 < rows; r0 += ROWS) {
             typename Lane<E, N, U, PAIRS>::Raw x[ROWS], g[ROWS];
@@ -368,16 +412,16 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                     }
                     at = at + 1 == DEPTH ? 0 : at + 1;
                 } else if constexpr (WORDS) {
-                    const E *px = reinterpret_cast<const E*>(words(at, 0)), *pg = reinterpret_cast<const E*>(words(at, BWD ? 1 : 0));
+                    const P *px = reinterpret_cast<const P*>(words(at, 0)), *pg = reinterpret_cast<const P*>(words(at, BWD ? 1 : 0));
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const bool full = use && L.on(u);
                         const P none{};
                         x[r].a[u] = x[r].b[u] = none;
-                        if (full && (!BWD || a.norm)) x[r].a[u].e[0] = px[L.o0[u]], x[r].b[u].e[0] = px[L.o1[u]];
+                        if (full && (!BWD || a.norm)) x[r].a[u] = px[L.o0[u]], x[r].b[u] = px[L.o1[u]];
                         if constexpr (BWD) {
                             g[r].a[u] = g[r].b[u] = none;
-                            if (full) g[r].a[u].e[0] = pg[L.o0[u]], g[r].b[u].e[0] = pg[L.o1[u]];
+                            if (full) g[r].a[u] = pg[L.o0[u]], g[r].b[u] = pg[L.o1[u]];
                         }
                     }
                     at = at + 1 == DEPTH ? 0 : at + 1;
@@ -448,17 +492,18 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                 }
                 copy_next();  // into a place just read
                 if constexpr (WORDS) {
-                    uint32_t* out = words(DEPTH, 0);
-                    L.store(out, 0, o[r]);
+                    uint32_t* row = words(DEPTH, 0);
+                    L.store(row, 0, o[r]);
                     __syncwarp();
-                    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<E*>(sd.out) + y0 + int64_t(h) * a.D);
+                    uint32_t* to = reinterpret_cast<uint32_t*>(out);
 #pragma unroll
                     for (int i = 0; i < WU; ++i)
-                        if (use && lane + i * G < row_words) to[lane + i * G] = out[lane + i * G];
+                        if (use && lane + i * G < row_words) to[lane + i * G] = row[lane + i * G];
                     __syncwarp();
                 } else if (use) {
-                    L.store(sd.out, y0 + int64_t(h) * a.D, o[r]);
+                    L.store(out, 0, o[r]);
                 }
+                out += step;
             }
         }
     }
