@@ -167,7 +167,7 @@ __device__ __forceinline__ void piece_products(uint32_t d, uint32_t planes, uint
                                                bool three) {
     const uint64_t b = key + uint64_t((piece * 2048) >> 4);
     if (three) mma_ta(d, planes + 16, b, idesc, !first);
-    mma_ta(d, planes + 8, b, idesc, 1u);
+    mma_ta(d, planes + 8, b, idesc, three || !first);
     mma_ta(d, planes, b, idesc, 1u);
 }
 
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     const size_t doc_state = (size_t(g.doc) * a.H + hd) * D * D;
     // the state that the walk starts from, and where the document's last one goes
     const bool starts = back ? g.last : g.first, ends = back ? g.first : g.last;
+    // (a walk that starts from zero leaves Query X of its first chunk out, and its first product clears the state)
     const float* x0 = starts ? (p.s0 ? p.s0 + doc_state : nullptr)
                              : (back ? a.back + (size_t(g.w) * a.H + hd) * D * D
                                      : a.front + (size_t(g.w - 1) * a.H + hd) * D * D);
@@ -266,16 +267,30 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     float* fn = fshort + 128;                          // score factors in a block off the diagonal, by column
     float* fd = fn + 32;                               // and in it: [31 + row - column]
     const float slope = a.slope[hd];
-    if (tid == 0) {
-        for (int i = 0; i < B_SPARE; ++i) {
-            const bool four = (i >= B_A && i < B_AFREE) || i == B_B || i == B_SCALED || i == B_C || i == B_OFREE || i == B_STAGED;
-            tc::mbar_init(&bar[i], i == B_X0 ? 12 : i == B_FIX ? 8 : four ? 4 : 1);
+    // chunk c of the walk: its place in the segment and its tokens
+    auto place = [&](int c) { return back ? nc - 1 - c : c; };
+    auto tokens = [&](int c) { return min(LC, g.len - LC * place(c)); };
+    auto tile = [&](int i) { return sm + (i % W_TILES) * TILE; };  // tile 3 c: Query of chunk c, then Key, Value
+    auto load = [&](int i) {  // by one thread
+        const int b = i % W_TILES, c = i / 3, which = i - 3 * c;
+        tc::mbar_expect_tx(&bar[B_FULL + b], TILE);
+        tc::tma4(tile(i), &tm.m[which == 0 ? p.query : which == 1 ? p.key : p.value], 0, g.t0 + LC * place(c), 0,
+                 hd / (which == 0 ? p.rq : which == 1 ? p.rk : p.rv), &bar[B_FULL + b]);
+    };
+    if (w == 16) {  // the first rows are on their way while the rest is set up
+        if (elect()) {
+            for (int i = 0; i < B_SPARE; ++i) {
+                const bool four = (i >= B_A && i < B_AFREE) || i == B_B || i == B_SCALED || i == B_C || i == B_OFREE || i == B_STAGED;
+                tc::mbar_init(&bar[i], i == B_X0 ? 12 : i == B_FIX ? 8 : four ? 4 : 1);
+            }
+            *abort_flag = 0;
+            tc::fence_mbar_init();
+            tc::fence_async_smem();
+            for (int i = 0; i < min(W_TILES, 3 * nc); ++i) load(i);
         }
-        *abort_flag = 0;
-        tc::fence_mbar_init();
+        __syncwarp();
     }
     if (w == 0) tc::tmem_alloc(tslot, 512);
-    if (w == 16 && lane < 3) tc::tma_prefetch_map(&tm.m[lane == 0 ? p.query : lane == 1 ? p.key : p.value]);
     if (tid < LC) {
         fs[tid] = p.in * decay(slope, back ? tid + 1 : LC - 1 - tid);
         const int m = g.len - LC * (nc - 1);
@@ -294,10 +309,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     const uint32_t tl = tbase + (uint32_t(32 * (w & 3)) << 16);  // this warp's lanes
     const int row = 32 * (w & 3) + lane;
 
-    // chunk c of the walk: its place in the segment and its tokens
-    auto place = [&](int c) { return back ? nc - 1 - c : c; };
-    auto tokens = [&](int c) { return min(LC, g.len - LC * place(c)); };
-    auto tile = [&](int i) { return sm + (i % W_TILES) * TILE; };  // tile 3 c: Query of chunk c, then Key, Value
     // whether chunk c's values still reach a state that is read; whether its output leaves by TMA
     auto adds = [&](int c) { return c + 1 < nc || x1; };
     // The state that a document ends in is an fp32 output: the values that still weigh more than 1/32 in it are split into three
@@ -319,10 +330,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     // 32 columns of the state that the walk starts from
     auto start_block = [&](int j) {
         float v[32];
-        if (!x0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        } else if (p.trans) {
+        if (p.trans) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 const float4 x = *reinterpret_cast<const float4*>(x0 + row * D + 32 * j + i);
@@ -337,7 +345,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     auto landed = [&](int i) { return wait(B_FULL + i % W_TILES, i / W_TILES); };
     auto arrive = [&](int b) { warp_arrive(sbar + 8 * b, lane); };
     // the groups share the blocks
-    if (w < 16) {
+    const bool blank = !x0;
+    if (w < 16 && !blank) {
         start_block(w >> 2);
         if (w < 12) arrive(B_X0);
     }
@@ -465,6 +474,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         for (int c = 0; c < nc; ++c) {
             const int n = tokens(c);
             const float fx = decay(slope, n), fo = p.by * decay(slope, back ? max(n - 1 - row, 0) : row + 1);
+            if (c == 0 && blank) {
+                arrive(B_C);
+                arrive(B_SCALED);
+                continue;
+            }
             if (!(c > 0 ? wait(B_S, c - 1) : wait(B_X0, 0))) break;
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
@@ -508,15 +522,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         }
     } else if (w == 16) {
         // ---- loads ----
-        int i = 0;
+        int i = min(W_TILES, 3 * nc);
         for (; i < 3 * nc; ++i) {
-            const int b = i % W_TILES, c = i / 3, which = i - 3 * c;
-            if (i >= W_TILES && !wait(B_FREE + b, i / W_TILES - 1)) break;
-            if (elect()) {
-                tc::mbar_expect_tx(&bar[B_FULL + b], TILE);
-                tc::tma4(tile(i), &tm.m[which == 0 ? p.query : which == 1 ? p.key : p.value], 0, g.t0 + LC * place(c), 0,
-                         hd / (which == 0 ? p.rq : which == 1 ? p.rk : p.rv), &bar[B_FULL + b]);
-            }
+            if (!wait(B_FREE + i % W_TILES, i / W_TILES - 1)) break;
+            if (elect()) load(i);
             __syncwarp();
         }
         if (!ok)  // every copy has landed before the block ends
@@ -531,10 +540,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
         for (int c = -1; c < nc; ++c) {
             if (c >= 0) {
                 if (!wait(B_C, c) || (c > 0 && !wait(B_OFREE, c - 1))) break;
+                const bool first = c == 0 && blank;
                 if (elect()) {
                     const uint64_t dq = tc::sdesc(smem_u32(tile(3 * c)), 16, 1024);
+                    if (!first) {
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) tc::mma(tbase + C_O, dq + kstep(s), dX + kstep(s), ID, s > 0);
+                        for (int s = 0; s < 8; ++s) tc::mma(tbase + C_O, dq + kstep(s), dX + kstep(s), ID, s > 0);
+                    }
                     tc::mma_commit(&bar[B_QX]);
                     spent(3 * c);
                 }
@@ -547,7 +559,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                         const int b = i % W_PIECES;
                         if (!wait(B_A + b, c * (PIECES / W_PIECES) + i / W_PIECES)) break;
                         if (elect()) {
-                            piece_products(tbase + C_X, tbase + C_V + PLANES * b, dk, i, IDt, false, exact);
+                            piece_products(tbase + C_X, tbase + C_V + PLANES * b, dk, i, IDt, first && i == 0, exact);
                             tc::mma_commit(&bar[B_AFREE + b]);
                         }
                         __syncwarp();
@@ -561,7 +573,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                     const uint64_t dv = tc::sdesc(smem_u32(tile(3 * c + 2)), TILE / 2, 1024);
                     spent(3 * c + 1);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) mma_ta(tbase + C_O, tbase + C_P + 8 * s, dv + tstep(s), IDt, 1u);
+                    for (int s = 0; s < 8; ++s) mma_ta(tbase + C_O, tbase + C_P + 8 * s, dv + tstep(s), IDt, !first || s > 0);
                     spent(3 * c + 2);
                     tc::mma_commit(&bar[B_O]);
                 }
@@ -595,7 +607,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
             }
             __syncwarp();
         }
-        if (elect()) tc::bulk_wait0();
     }
     if (!ok) *abort_flag = 1;
     __syncwarp();
