@@ -9,19 +9,28 @@
 // Backwards (the state is Y, see kda_lin.cuh) the mask is j >= i with lambda^(j - i), Query Y takes lambda^(n - 1 - i)
 // and Value_j takes lambda^(j + 1).
 //
-// Bound by HBM: 1 KB of rows a token and head against 5 products of 128^3 a chunk (and 2 more of the state's), half
-// of the tensor cores' time at HBM's rate.  One block per multiprocessor; its state stays in tensor memory as X^T (lane
-// = value channel), the scaled values are the state product's left operand in tensor memory, split into three
-// bf16 planes (8 + 8 + 8 bits: exact, so the state's products are fp32 products), Q, K and V come by TMA, two chunks
-// deep, and every product reads them where they land:
+// What bounds it: a token and head is 1 KB of rows, 2.9 us of a multiprocessor's share of HBM for a chunk, and 40 to 48
+// products of 128 x 128 x 16, some 3550 to 4200 clocks.  One block per multiprocessor holds a state and works on
+// successive chunks: 16384 tokens (9000 / 5000 / 2384) x 64 heads take 197 us, 5.5 TB/s (81% of the measured 6.77), the
+// last third of it on the 64 blocks of the longest document; one document of 16384 x 64 (64 blocks) 305 us, 2.4 us a
+// chunk, bound by the chain of its own steps.  Of those 2.4 us the products alone take 1.9 and the hand-overs alone 1.3.
+//
+// The state stays in tensor memory as X^T (lane = value channel); the scaled values are the state product's left operand
+// in tensor memory, split into bf16 planes, so that with three of them (8 + 8 + 8 bits: exact) the state's products are fp32
+// products.  The scores and the state are rounded to bf16 as operands of products whose sums are rounded to bf16 rows:
+// each adds as much as the output's own rounding.  Query, Key and Value come by TMA and are read where they land:
 //     P      A = Query [tokens][keys],    B = Key [tokens][keys]
 //     QX     A = Query,                   B = X^T in shared memory, bf16 [values][keys]
 //     P'V    A = P' (tensor memory),      B = Value [tokens][values] read across
 //     state  A = values^T (tensor memory), B = Key read across
 // Four groups of warps work at once: A (two groups) scales and splits the values, B masks and rounds the scores and
-// hands the output to TMA, C rounds and decays the state and scales Query X's rows; three warps issue loads, products and
-// stores.  The chunk's tiles go through a ring of five, each taken again as soon as its last product has read it.
+// hands the output to TMA, C rounds and decays the state and scales Query X's rows; three warps issue loads, products
+// and stores.  The chunk's tiles go through a ring of five, each taken again as soon as its last product has read it.
 // Rows behind a document's end (another's) are cleared in K and V, so nothing of them, were it not finite, is multiplied.
+//
+// Measured beside it, one document of 16384 x 64 (305 us): one column factor for scores and state where the decay is mild,
+// without the pass over Query X's rows: 326; eight warps in B: 312; the output stored from registers: 508; lane 0 polling
+// for its warp: 471; products issued by one thread in one piece: 342.
 #include <limits.h>
 
 #include "kda_lin.cuh"
@@ -630,6 +639,8 @@ enum StateBar {
 };
 
 // No decay of the state between chunks: a token's factor reaches to the segment's end, the products add up.
+// Bound by HBM on paper (512 B a token and head; 24 products a chunk, half its time); 16384 tokens x 16 heads: 35 us,
+// 3.4 TB/s: one wave of 112 blocks, a sixth of whose time is their start and the store of the state.
 __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int ps, const __grid_constant__ LinMaps tm) {
     extern __shared__ unsigned char smraw[];
     unsigned char* sm = tc::align1024(smraw);

@@ -49,10 +49,11 @@ EncodeTiledFn encode_tiled() {
 }
 
 // Whether long documents are cut into segments, and the tokens of one (a power of two).  This depends on the heads
-// alone: a document's results must not depend on the pack.  A walk takes 2.3 us a chunk where it has its multiprocessor
-// and HBM to itself, so a document of 16384 tokens takes 0.29 ms uncut; cut, its states between segments cost a second
-// pass over two of the rows: at 64 heads 0.34 ms in all, at 16 heads 0.11.  A backward walks three times as many heads.
-// Segments of 2048 tokens make a wave of blocks of 16384 tokens and 16 heads; fewer heads take shorter ones.
+// alone: a document's results must not depend on the pack.  A walk takes 2.4 us a chunk where its block does not wait for
+// HBM, so a document of 16384 tokens takes 0.305 ms uncut, whatever the heads up to the multiprocessors' number; cut, its
+// states between segments cost a second pass over two of the rows: forward 0.094 ms at 16 heads, 0.171 at 32, 0.248 at 48,
+// 0.34 at 64.  A backward walks three times as many heads: cut 0.183 ms at 16, uncut 0.306 at 24 to 48.  Segments of
+// 2048 tokens make one wave of blocks of 16384 tokens and 16 heads; fewer heads take shorter ones.
 bool cuts(int H, bool back) { return H < (back ? 24 : 64); }
 int segment(int H) {
     int s = 512;

@@ -1,4 +1,5 @@
-// Segments of the linear attention's documents, and the states between them.
+// Segments of the linear attention's documents, and the states between them.  One block's scan (5 us) and a pass over the
+// slots (64 KB each, read and written once: 8 us for 16 heads of 16384 tokens) stand before a walk that is cut.
 #include "kda_lin.cuh"
 
 namespace kda {

