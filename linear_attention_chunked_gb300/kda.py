@@ -763,10 +763,24 @@ def kda_linattn_workspace_size(T, N, H, Hk, op):
     return ws.value, sv.value
 
 
-def _check_rows(fn, name, t):
-    """Rows that the library copies by 16 bytes."""
-    if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
+def _heads(fn, name, t, shape, dtype, dev):
+    """One tensor [T, heads, channels] of a call: dense heads, any token stride.  Returns that stride (0,
+    the library's dense, where there is at most one token)."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev:
+        T, H, C = shape
+        token, head, channel = t.stride()
+        if channel == 1 and head == C and token >= H * C:
+            return token if T > 1 else 0
+    _check_tensor(fn, name, t, shape, dtype, dev, True)
+    return _row_stride(t)
+
+
+def _aligned_heads(fn, name, t, shape, dev):
+    """bf16 heads whose rows the library copies by 16 bytes."""
+    ld = _heads(fn, name, t, shape, torch.bfloat16, dev)
+    if t.data_ptr() % 16 or ld % 8:
         raise ValueError(f"{fn}: {name} is not aligned to 16 bytes (address {t.data_ptr():#x}, token stride {t.stride(0)})")
+    return ld
 
 
 def _linattn_problem(fn, q, k, v, slope, scale, N, cu_seqlens):
@@ -780,16 +794,13 @@ def _linattn_problem(fn, q, k, v, slope, scale, N, cu_seqlens):
         raise ValueError(f"{fn}: v has head dim {d}, expected {D}")
     if Hk < 1 or H % Hk:
         raise ValueError(f"{fn}: {Hk} query and key heads do not divide {H} value heads")
-    _check_tensor(fn, "q", q, (T, Hk, D), torch.bfloat16, dev, True)
-    _check_tensor(fn, "k", k, (T, Hk, D), torch.bfloat16, dev, True)
-    _check_tensor(fn, "v", v, (T, H, D), torch.bfloat16, dev, True)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_rows(fn, name, t)
+    ld_q = _aligned_heads(fn, "q", q, (T, Hk, D), dev)
+    ld_k = _aligned_heads(fn, "k", k, (T, Hk, D), dev)
+    ld_v = _aligned_heads(fn, "v", v, (T, H, D), dev)
     _check_tensor(fn, "slope", slope, (H,), torch.float32, dev)
     if cu_seqlens is not None:
         _check_tensor(fn, "cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
-    return kda_linattn_problem(T, N, H, Hk, D, KDA_DT_BF16, float(scale), _row_stride(q), _row_stride(k), _row_stride(v),
-                               None if cu_seqlens is None else cu_seqlens.data_ptr())
+    return kda_linattn_problem(T, N, H, Hk, D, KDA_DT_BF16, float(scale), ld_q, ld_k, ld_v, _at(cu_seqlens))
 
 
 def kda_linattn_fwd(q, k, v, slope, cu_seqlens, *, h0=None, scale=1.0, save=True, o=None, ht=None,
@@ -811,7 +822,7 @@ def kda_linattn_fwd(q, k, v, slope, cu_seqlens, *, h0=None, scale=1.0, save=True
     else:
         _check_bytes(fn, "saved", saved, sv_b, dev)
     if o is None:
-        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+        o = torch.empty((pr.T, pr.H, D), dtype=torch.bfloat16, device=dev)
     else:
         _check_tensor(fn, "o", o, v.shape, torch.bfloat16, dev)
     if ht is None:
@@ -840,8 +851,8 @@ def kda_linattn_bwd(q, k, v, slope, cu_seqlens, dO, *, saved=None, h0=None, dht=
     if saved is not None:
         _check_bytes(fn, "saved", saved, sv_b, dev)
     ws, ws_n = _workspace(fn, ws, ws_b, dev)
-    rows = dict(dtype=torch.bfloat16, device=dev)
-    out = dict(dq=torch.empty(q.shape, **rows), dk=torch.empty(q.shape, **rows), dv=torch.empty(v.shape, **rows))
+    rows, shared = dict(dtype=torch.bfloat16, device=dev), (pr.T, pr.Hk, D)
+    out = dict(dq=torch.empty(shared, **rows), dk=torch.empty(shared, **rows), dv=torch.empty((pr.T, pr.H, D), **rows))
     if want_dh0:
         out["dh0"] = torch.empty(state, dtype=torch.float32, device=dev)
     _call(fn, dev, ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), slope.data_ptr(), _at(h0), dO.data_ptr(),
@@ -864,7 +875,7 @@ def kda_linattn_step(q, k, v, slope, h, *, scale=1.0, slots=None, h_out=None, o=
     else:
         _check_tensor(fn, "h_out", h_out, h.shape, torch.float32, dev)
     if o is None:
-        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+        o = torch.empty((pr.T, pr.H, D), dtype=torch.bfloat16, device=dev)
     else:
         _check_tensor(fn, "o", o, v.shape, torch.bfloat16, dev)
     _slots(fn, slots, N, h.shape[0], dev)
@@ -890,11 +901,6 @@ def kda_rope_frequencies(R, base=10000.0, *, scaling="plain", factor=1.0, traine
     return torch.tensor(list(f[:R // 2]), dtype=torch.float64, device=device), s.value
 
 
-def _rope_rows(fn, name, t, shape, dtype, dev):
-    """One tensor of a rope call: dense heads, any token stride."""
-    _check_tensor(fn, name, t, shape, dtype, dev, True)
-
-
 def _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale):
     """Checks what the forward and the backward share; k may be None (no key heads)."""
     if q.dim() != 3 or (k is not None and k.dim() != 3):
@@ -903,18 +909,19 @@ def _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale):
     Hk = 0 if k is None else k.shape[1]
     if dtype not in _DTYPES:
         raise ValueError(f"{fn}: q is {dtype}, expected one of bfloat16, float16, float32")
-    _rope_rows(fn, "q", q, (T, Hq, C), dtype, dev)
-    _rope_rows(fn, "k", k, (T, Hk, C), dtype, dev)
+    ld_q = _heads(fn, "q", q, (T, Hq, C), dtype, dev)
+    ld_k = 0 if k is None else _heads(fn, "k", k, (T, Hk, C), dtype, dev)
     _check_tensor(fn, "pos", pos, (T,), torch.int32, dev)
-    _check_tensor(fn, "freq", freq, (freq.numel(),), torch.float64, dev)
-    if 2 * freq.numel() > C:
-        raise ValueError(f"{fn}: {freq.numel()} frequencies turn more channels than the {C} of a head")
+    n = freq.numel()
+    _check_tensor(fn, "freq", freq, (n,), torch.float64, dev)
+    if 2 * n > C:
+        raise ValueError(f"{fn}: {n} frequencies turn more channels than the {C} of a head")
     if not norm and (wq is not None or wk is not None):
         raise ValueError(f"{fn}: wq and wk belong to the norm (norm=True)")
     _check_tensor(fn, "wq", wq, (C,), torch.float32, dev)
     _check_tensor(fn, "wk", wk, (C,), torch.float32, dev)
-    return kda_rope_problem(T, Hq, Hk, C, 2 * freq.numel(), KDA_ROPE_PAIRS if interleaved else KDA_ROPE_HALF, int(bool(norm)),
-                            _DTYPES[dtype], float(eps), float(scale), _row_stride(q), _row_stride(k), 0, 0)
+    return kda_rope_problem(T, Hq, Hk, C, 2 * n, KDA_ROPE_PAIRS if interleaved else KDA_ROPE_HALF, int(bool(norm)),
+                            _DTYPES[dtype], float(eps), float(scale), ld_q, ld_k, 0, 0)
 
 
 def kda_rope_workspace_size(D, *, norm=True):
@@ -936,17 +943,16 @@ def kda_rope_fwd(q, k, pos, freq, *, wq=None, wk=None, norm=False, eps=1e-6, int
     pr = _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale)
     dev = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif q_out is not q:
-        _rope_rows(fn, "q_out", q_out, q.shape, q.dtype, dev)
+        q_out = torch.empty((pr.T, pr.Hq, pr.D), dtype=q.dtype, device=dev)
+    else:
+        pr.ld_qo = _heads(fn, "q_out", q_out, (pr.T, pr.Hq, pr.D), q.dtype, dev)
     if k is None:
         if k_out is not None:
             raise ValueError(f"{fn}: k_out needs a k")
     elif k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    elif k_out is not k:
-        _rope_rows(fn, "k_out", k_out, k.shape, q.dtype, dev)
-    pr.ld_qo, pr.ld_ko = _row_stride(q_out), _row_stride(k_out)
+        k_out = torch.empty((pr.T, pr.Hk, pr.D), dtype=q.dtype, device=dev)
+    else:
+        pr.ld_ko = _heads(fn, "k_out", k_out, (pr.T, pr.Hk, pr.D), q.dtype, dev)
     _call(fn, dev, ctypes.byref(pr), q.data_ptr(), _at(k), pos.data_ptr(), freq.data_ptr(), _at(wq), _at(wk),
           q_out.data_ptr(), _at(k_out))
     return q_out, k_out
@@ -960,16 +966,15 @@ def kda_rope_bwd(q, k, pos, freq, dq_out, dk_out, *, wq=None, wk=None, norm=Fals
     fn = "kda_rope_bwd"
     pr = _rope_problem(fn, q, k, pos, freq, wq, wk, norm, eps, interleaved, scale)
     dev = q.device
-    _rope_rows(fn, "dq_out", dq_out, q.shape, q.dtype, dev)
+    pr.ld_qo = _heads(fn, "dq_out", dq_out, (pr.T, pr.Hq, pr.D), q.dtype, dev)
     if k is None:
         if dk_out is not None:
             raise ValueError(f"{fn}: dk_out needs a k")
     else:
-        _rope_rows(fn, "dk_out", dk_out, k.shape, q.dtype, dev)
-    pr.ld_qo, pr.ld_ko = _row_stride(dq_out), _row_stride(dk_out)
-    out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev))
+        pr.ld_ko = _heads(fn, "dk_out", dk_out, (pr.T, pr.Hk, pr.D), q.dtype, dev)
+    out = dict(dq=torch.empty((pr.T, pr.Hq, pr.D), dtype=q.dtype, device=dev))
     if k is not None:
-        out["dk"] = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        out["dk"] = torch.empty((pr.T, pr.Hk, pr.D), dtype=q.dtype, device=dev)
     if wq is not None:
         out["dwq"] = torch.empty_like(wq)
     if wk is not None:
