@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             for (int r = 0; r < ROWS; ++r) {
                 const int h = (r0 + r) * sd.per_token + first;
                 const bool use = live && h < sd.H;
-                const float rs = rsqrtf(fmaf(all[r], a.inv_d, a.eps));
+                // (no row, no part in dw: without an eps its 1 / sqrt(0) would be one)
+                const float rs = !BWD || use ? rsqrtf(fmaf(all[r], a.inv_d, a.eps)) : 0.f;
                 const f2 rs2 = twice(rs);
                 if constexpr (!BWD) {
 #pragma unroll

@@ -1,0 +1,53 @@
+"""The norm and rotation of queries and keys (kda_rope_*) where their arithmetic could leave its range: no eps, tiles that are
+not full, rows far from one, values that are not finite.  Bounds as in test_rope_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_chunked_gb300 import kda
+from oracle import rope
+from test_rope_gpu import U, _case, _np, _pair_size
+
+pytestmark = pytest.mark.gpu
+
+TINY = 2.0 ** -126  # below it the kernels' results are zero
+
+
+def _bounds(x, pos, f, dy, w, inter, scale, eps, half):
+    """Definition and bounds of one tensor, forward and backward: {name: (value, tolerance)}."""
+    R, o = 2 * len(f), dict(norm=True, interleaved=inter, scale=scale, w=w, eps=eps)
+    y = rope.rope_fwd(x, pos, f, **o)
+    dx, dw = rope.rope_bwd(x, pos, f, dy, **o)
+    turned, _ = rope.rope_bwd(x, pos, f, dy, norm=False, interleaved=inter, scale=scale)
+    size, wa = _pair_size(turned, R, inter), np.abs(w)
+    r = 1 / np.sqrt((x ** 2).mean(-1, keepdims=True) + eps)
+    xr = np.abs(x * r)
+    part = r * (size * wa + xr * (size * wa * xr).mean(-1, keepdims=True))
+    least = 2.0 ** -25 if half == 2.0 ** -11 else TINY  # fp16: below its normal range
+    return {"": (y, half * np.abs(y) + 16 * U * _pair_size(y, R, inter) + least),
+            "d": (dx, half * np.abs(dx) + 32 * U * part + least),
+            "dw": (dw, U * (32 + 512) * (size * xr).sum((0, 1)) + TINY)}
+
+
+def _check(c, inter, eps):
+    q, k, dq, dk, pos, f, s, (wq, wk) = c
+    kw = dict(wq=wq, wk=wk, norm=True, interleaved=inter, scale=s, eps=eps)
+    got = dict(zip("qk", kda.kda_rope_fwd(q, k, pos, f, **kw)))
+    got.update(kda.kda_rope_bwd(q, k, pos, f, dq, dk, **kw))
+    for n, x, dy, w in (("q", q, dq, wq), ("k", k, dk, wk)):
+        eps32 = float(np.float32(eps))  # what the call takes
+        for what, (ref, tol) in _bounds(_np(x), _np(pos), _np(f), _np(dy), _np(w), inter, s, eps32, torch.finfo(q.dtype).eps / 2).items():
+            err = np.abs(_np(got[what + n]) - ref)
+            assert (err <= tol).all(), (what + n, float(np.nanmax(err / tol)), int(np.isnan(err).sum()))
+
+
+# tiles of tokens that the last ones do not fill, heads that a tile's groups do not share evenly, every pack width
+PARTS = [(1, 1, 1, 128, 128), (37, 5, 3, 128, 64), (1777, 32, 8, 128, 128), (1777, 7, 3, 80, 52), (2500, 3, 1, 64, 64), (129, 11, 2, 96, 48),
+         (33, 9, 5, 34, 10), (65, 3, 3, 254, 130), (4099, 2, 3, 128, 128)]
+
+
+@pytest.mark.parametrize("shape", PARTS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_no_eps(shape, dtype, inter):
+    _check(_case(*shape, dtype, True), inter, 0.0)
