@@ -4,7 +4,8 @@
 //   y  = scale R(pos freq) n on the first R channels, in pairs, n on the others
 //   backward:  d = the turn undone on dy (scale kept),  dw = sum_rows d xh,  g = d w
 //              dx = (g - xh sum_c(g xh) / D) / sqrt(..)          (norm; else dx = d)
-//   sum x^2 and sum g x go through one exchange: dx = rs g - x rs^3 sum(g x) / D with rs = 1 / sqrt(..)
+//   sum x^2 and sum g x go through one exchange: dx = rs (g - xh rs sum(g x) / D) with rs = 1 / sqrt(..) (rs^3 leaves fp32 where
+//   rs, xh and the gradient do not)
 //
 // Bound by HBM: forward 2, backward 3 (2 without the norm) row transfers.  A row of D channels belongs to a
 // group of lanes that each hold 8 pairs (4 of fp32) as two 16-byte accesses; both members of a pair lie in one lane, so
@@ -484,14 +485,14 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                         o[r].y[i] = fma2(p, s[i], mul2(z, c[i]));
                     }
                 } else if (a.norm) {
-                    // dx = rs (g - xh sum(g xh) / D) = rs g - x rs^3 sum(g x) / D
-                    const f2 k = twice(-rs * rs * rs * all[ROWS + r] * a.inv_d);
+                    const f2 k = twice(-rs * all[ROWS + r] * a.inv_d);
 #pragma unroll
                     for (int i = 0; i < NP / 2; ++i) {
-                        sum.x[i] = fma2(o[r].x[i], mul2(v[r].x[i], rs2), sum.x[i]);
-                        sum.y[i] = fma2(o[r].y[i], mul2(v[r].y[i], rs2), sum.y[i]);
-                        o[r].x[i] = fma2(v[r].x[i], k, mul2(o[r].x[i], mul2(w.x[i], rs2)));
-                        o[r].y[i] = fma2(v[r].y[i], k, mul2(o[r].y[i], mul2(w.y[i], rs2)));
+                        const f2 xh = mul2(v[r].x[i], rs2), yh = mul2(v[r].y[i], rs2);
+                        sum.x[i] = fma2(o[r].x[i], xh, sum.x[i]);
+                        sum.y[i] = fma2(o[r].y[i], yh, sum.y[i]);
+                        o[r].x[i] = mul2(fma2(xh, k, mul2(o[r].x[i], w.x[i])), rs2);
+                        o[r].y[i] = mul2(fma2(yh, k, mul2(o[r].y[i], w.y[i])), rs2);
                     }
                 }
                 copy_next();  // into a place just read

@@ -51,3 +51,23 @@ PARTS = [(1, 1, 1, 128, 128), (37, 5, 3, 128, 64), (1777, 32, 8, 128, 128), (177
 @pytest.mark.parametrize("inter", [False, True])
 def test_no_eps(shape, dtype, inter):
     _check(_case(*shape, dtype, True), inter, 0.0)
+
+
+# rows whose root mean square's inverse has no cube in fp32, both ways
+@pytest.mark.parametrize("dtype,far,eps", [("bf16", 1e13, 1e-6), ("fp32", 1e13, 0.0), ("fp32", 3e16, 1e-6), ("bf16", 1e-12, 1e-30), ("fp32", 1e-13, 1e-30),
+                                           ("fp32", 1e-14, 0.0), ("bf16", 1e-16, 0.0)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rows_far_from_one(dtype, far, eps, inter):
+    for shape in ((77, 5, 3, 128, 64), (9, 7, 3, 80, 52), (5, 3, 3, 254, 130)):
+        q, k, *rest = _case(*shape, dtype, True, fused=False)
+        _check((q * far, k * far, *rest), inter, eps)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_rows_of_zeros(dtype):
+    # x = 0 is an ordinary row where eps > 0: y = 0, dx = dy w / sqrt(eps) (in fp16's range where eps is not tiny)
+    for eps in (1e-6,) if dtype == "fp16" else (1e-6, 1e-30):
+        q, k, *rest = _case(21, 5, 3, 128, 64, dtype, True, fused=False)
+        q[3], k[20, 1] = 0, 0
+        q[7, 4] = 0
+        _check((q, k, *rest), False, eps)
