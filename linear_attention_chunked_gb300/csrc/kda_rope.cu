@@ -163,6 +163,13 @@ struct Lane {
         if (N == 1 || !PAIRS) return 2 * N * (l + u * G) < R;
         return (2 * e < N ? o0[u] : o1[u]) < R;
     }
+    // of pairs 2 i and 2 i + 1 of narrow packs: turned where they turn, else plain
+    __device__ __forceinline__ f2 pick(int i, f2 turned, f2 plain) const {
+        float t0, t1, p0, p1;
+        up2(turned, t0, t1);
+        up2(plain, p0, p1);
+        return pk2(turns(2 * i) ? t0 : p0, turns(2 * i + 1) ? t1 : p1);
+    }
     // the channels of pair i's members
     __device__ __forceinline__ void channels(int i, int& a, int& b) const {
         const int u = i / N, e = i % N;
@@ -288,9 +295,12 @@ template <bool BWD> constexpr size_t rp_smem(int row_bytes) {  // bytes of both 
 
 // BWD: inputs and gradients in, gradients out; otherwise inputs in, turned out.  The first side[0].blocks blocks do q, the
 // others k.  tokens = groups / per_token tokens a tile.
+// STAY (wide packs): some channels do not turn.  They are passed on, not turned by 1 and 0, which would take 0 times an infinity into
+// another channel of no pair with it.  Wide packs turn as a whole or not at all; where all turn, the test would cost 5% of the
+// backward.  Narrow packs pick member by member.
 // AHEAD: rows come through the ring, for N = 1 as whole words of which a group's lanes then pick their pairs, and go out as
 // words too; else (rows that no word fits) element by element.
-template <class E, int N, int U, bool PAIRS, bool BWD, bool AHEAD>
+template <class E, int N, int U, bool PAIRS, bool BWD, bool AHEAD, bool STAY>
 __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, int G) {
     using P = Pack<E, N>;
     constexpr int NP = N * U;
@@ -315,6 +325,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) sum.x[i] = sum.y[i] = twice(0.f);
     const int64_t tiles = (a.T + tokens - 1) / tokens;
+    const bool some_stay = N <= 2 && a.R < a.D;
     auto slot = [&](int d, int k, int u) { return ring + ((d * (BWD ? 4 : 2) + k) * U + u) * RP_THREADS + tid; };
     // WORDS: [DEPTH][x, then g][group][word], then a row of every group on its way out
     const int row_words = a.D * int(sizeof(E)) / 4;
@@ -446,11 +457,20 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                     for (int i = 0; i < NP / 2; ++i) xx = fma2(v[r].x[i], v[r].x[i], fma2(v[r].y[i], v[r].y[i], xx));
                 if constexpr (BWD) {  // the turn undone
                     o[r] = L.values(g[r]);
-#pragma unroll
-                    for (int i = 0; i < NP / 2; ++i) {
+                    auto undo = [&](int i) {
                         const f2 p = o[r].x[i], z = o[r].y[i];
                         o[r].x[i] = fma2(p, c[i], mul2(z, s[i]));
                         o[r].y[i] = fma2(mul2(p, s[i]), twice(-1.f), mul2(z, c[i]));
+                        if (some_stay) o[r].x[i] = L.pick(i, o[r].x[i], p), o[r].y[i] = L.pick(i, o[r].y[i], z);
+                    };
+                    if constexpr (STAY) {
+#pragma unroll
+                        for (int i = 0; i < NP / 2; ++i)
+                            if (L.turns(2 * i)) undo(i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NP / 2; ++i) {
+                        if (!STAY) undo(i);
                         if (a.norm) gx = fma2(mul2(o[r].x[i], w.x[i]), v[r].x[i], fma2(mul2(o[r].y[i], w.y[i]), v[r].y[i], gx));
                     }
                 }
@@ -481,8 +501,13 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
                     for (int i = 0; i < NP / 2; ++i) {
                         f2 p = v[r].x[i], z = v[r].y[i];
                         if (a.norm) p = mul2(p, mul2(w.x[i], rs2)), z = mul2(z, mul2(w.y[i], rs2));
-                        o[r].x[i] = fma2(p, c[i], mul2(mul2(z, s[i]), twice(-1.f)));
-                        o[r].y[i] = fma2(p, s[i], mul2(z, c[i]));
+                        o[r].x[i] = p;
+                        o[r].y[i] = z;
+                        if (!STAY || L.turns(2 * i)) {
+                            o[r].x[i] = fma2(p, c[i], mul2(mul2(z, s[i]), twice(-1.f)));
+                            o[r].y[i] = fma2(p, s[i], mul2(z, c[i]));
+                        }
+                        if (some_stay) o[r].x[i] = L.pick(i, o[r].x[i], p), o[r].y[i] = L.pick(i, o[r].y[i], z);
                     }
                 } else if (a.norm) {
                     const f2 k = twice(-rs * all[ROWS + r] * a.inv_d);
@@ -592,12 +617,15 @@ void launch_as(RopeArgs a, bool pairs, cudaStream_t st) {
     if (a.side[1].part) a.side[1].part = a.side[0].part + size_t(a.side[0].blocks) * a.D;
     const unsigned grid = unsigned(a.side[0].blocks + a.side[1].blocks);
     {
-        static unsigned long long done[2];
+        static unsigned long long done[4];
         const size_t smem = !AHEAD ? 0 : N > 1 ? rp_smem<BWD>(2 * U * int(sizeof(Pack<E, N>)))
                                                : rp_smem<BWD>(4 * (rp_words<E, U>() + 1)) + 4 * (rp_words<E, U>() + 1) * RP_THREADS;
-        auto* kernel = pairs ? k_rope<E, N, U, true, BWD, AHEAD> : k_rope<E, N, U, false, BWD, AHEAD>;
+        constexpr bool WIDE = N > 2;
+        const bool stay = WIDE && a.R < a.D;
+        auto* kernel = pairs ? (stay ? k_rope<E, N, U, true, BWD, AHEAD, WIDE> : k_rope<E, N, U, true, BWD, AHEAD, false>)
+                             : (stay ? k_rope<E, N, U, false, BWD, AHEAD, WIDE> : k_rope<E, N, U, false, BWD, AHEAD, false>);
         // (the limit counts the static part too)
-        allow_smem(reinterpret_cast<const void*>(kernel), smem + RP_TOKENS * RP_MAXD * sizeof(float), &done[pairs]);
+        allow_smem(reinterpret_cast<const void*>(kernel), smem + RP_TOKENS * RP_MAXD * sizeof(float), &done[2 * stay + pairs]);
         ProfScope ps(BWD ? KK_ROPE_BWD : KK_ROPE_FWD, st);
         kernel<<<grid, RP_THREADS, smem, st>>>(a, G);
     }

@@ -71,3 +71,50 @@ def test_rows_of_zeros(dtype):
         q[3], k[20, 1] = 0, 0
         q[7, 4] = 0
         _check((q, k, *rest), False, eps)
+
+
+def _at(x, odd):
+    """x as a view at an odd address with an odd token stride."""
+    T, H, C = x.shape
+    if not odd:
+        return x
+    return torch.empty((T, H * C + 3), dtype=x.dtype, device="cuda")[:, 1:1 + H * C].unflatten(1, (H, C)).copy_(x)
+
+
+def _same(a, b):
+    return torch.equal(torch.nan_to_num(a, 7.0), torch.nan_to_num(b, 7.0)) and torch.equal(torch.isnan(a), torch.isnan(b))
+
+
+# every pack width, and the same rows where only single elements can be read
+@pytest.mark.parametrize("C,R", [(128, 64), (128, 0), (80, 52), (72, 40), (96, 48), (34, 10), (254, 130), (16, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("odd", [False, True])
+def test_channels_that_do_not_turn_pass_through(C, R, dtype, inter, odd):
+    # without a norm an unturned channel is its input and no other channel depends on it, whatever it holds
+    q, k, dq, dk, pos, f, s, _ = _case(11, 3, 2, C, R, dtype, False, fused=False)
+    kw = dict(interleaved=inter, scale=s)
+    a = [_at(x, odd) for x in (q, k)]
+    fwd, bwd = kda.kda_rope_fwd(*a, pos, f, **kw), kda.kda_rope_bwd(*a, pos, f, _at(dq, odd), _at(dk, odd), **kw)
+    rest = list(range(R, C))
+    for bad in (float("inf"), float("nan")):
+        for c in (rest[0], rest[len(rest) // 2], rest[-1]):
+            x = [t.clone() for t in (q, k, dq, dk)]
+            for t in x:
+                t[4, 1, c] = bad
+                t[0, 0, c] = -bad
+                t[5, 0, R:] = bad
+                t[6, 0, R:] = -0.0
+            y = kda.kda_rope_fwd(_at(x[0], odd), _at(x[1], odd), pos, f, **kw)
+            g = kda.kda_rope_bwd(*a, pos, f, _at(x[2], odd), _at(x[3], odd), **kw)
+            for got, clean, given in ((y[0], fwd[0], x[0]), (y[1], fwd[1], x[1]), (g["dq"], bwd["dq"], x[2]), (g["dk"], bwd["dk"], x[3])):
+                assert torch.equal(got[..., :R], clean[..., :R])
+                assert _same(got[..., R:], given[..., R:])
+                assert torch.equal(torch.signbit(got[6, 0, R:]), torch.signbit(given[6, 0, R:]))
+    # with a norm an infinite channel takes the others of its head to zero and is no number itself
+    x = q.clone()
+    x[4, 1, rest[0]] = float("inf")
+    y, _ = kda.kda_rope_fwd(_at(x, odd), a[1], pos, f, norm=True, **kw)
+    want = torch.zeros(C, device="cuda")
+    want[rest[0]] = float("nan")
+    assert _same(y[4, 1].float(), want)
