@@ -382,7 +382,13 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
     int at = 0;
     // positions are read a tile ahead: the cosines and sines of a tile wait for no load
     auto position = [&](int64_t tile) { return tid < tokens && tile * tokens + tid < a.T ? a.pos[tile * tokens + tid] : 0; };
-    for (int i = tid; i < half; i += RP_THREADS) turn[i] = turns_per_token(a.freq[i]);
+    int bad = 0;
+    for (int i = tid; i < half; i += RP_THREADS) {
+        const double f = a.freq[i];
+        turn[i] = turns_per_token(f);
+        bad |= !isfinite(f);
+    }
+    const bool broken = __syncthreads_or(bad);  // no number among the frequencies: its pairs' angles are none
     int next = position(block);
     for (int64_t tile = block; tile < tiles; tile += sd.blocks) {
         if (tid < tokens) place[tid] = next;
@@ -391,6 +397,11 @@ __global__ void __launch_bounds__(RP_THREADS, RP_OCCUPANCY) k_rope(RopeArgs a, i
             const int t = i / half, k = i - t * half;
             cos_sin(place[t], turn[k], a.scale, cs[t][k], cs[t][half + k]);
         }
+        if (broken)
+            for (int i = tid; i < tokens * half; i += RP_THREADS) {
+                const int t = i / half, k = i - t * half;
+                if (!isfinite(a.freq[k])) cs[t][k] = cs[t][half + k] = __int_as_float(0x7fffffff);
+            }
         next = position(tile + sd.blocks);
         __syncthreads();
         const int64_t t = tile * tokens + own;

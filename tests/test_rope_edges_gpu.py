@@ -118,3 +118,22 @@ def test_channels_that_do_not_turn_pass_through(C, R, dtype, inter, odd):
     want = torch.zeros(C, device="cuda")
     want[rest[0]] = float("nan")
     assert _same(y[4, 1].float(), want)
+
+
+@pytest.mark.parametrize("C,R", [(128, 128), (80, 52), (34, 10)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_frequencies_that_are_no_numbers(C, R, inter):
+    # their pairs' angles are no numbers, at position 0 either; the other pairs turn as before
+    q, k, dq, dk, pos, f, s, _ = _case(9, 3, 2, C, R, "fp32", False)
+    kw = dict(interleaved=inter, scale=s)
+    i = np.arange(R // 2)
+    a, b = (2 * i, 2 * i + 1) if inter else (i, R // 2 + i)
+    call = lambda f: [*kda.kda_rope_fwd(q, k, pos, f, **kw), *kda.kda_rope_bwd(q, k, pos, f, dq, dk, **kw).values()]  # noqa: E731
+    clean = call(f)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        g = f.clone()
+        g[1] = g[R // 2 - 1] = bad
+        lost = [int(x) for p in (1, R // 2 - 1) for x in (a[p], b[p])]
+        kept = [c for c in range(C) if c not in lost]
+        for got, want in zip(call(g), clean):
+            assert torch.isnan(got[..., lost]).all() and torch.equal(got[..., kept], want[..., kept])
