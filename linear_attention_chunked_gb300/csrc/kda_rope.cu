@@ -663,8 +663,8 @@ void launch(const RopeArgs& a, int layout, cudaStream_t st) {
     if (fits(V, false)) launch_as<E, V, 1, BWD, true>(a, pairs, st);
     else if (V == 8 && fits(4, false)) launch_as<E, 4, V / 4, BWD, true>(a, pairs, st);
     else if (fits(2, false)) launch_as<E, 2, V / 2, BWD, true>(a, pairs, st);
-    else if (fits(4 / int(sizeof(E)), true)) launch_as<E, 1, V, BWD, true>(a, pairs, st);
-    else launch_as<E, 1, 4, BWD, false>(a, pairs, st);
+    else if (sizeof(E) == 4 || fits(2, true)) launch_as<E, 1, V, BWD, true>(a, pairs, st);  // (fp32 rows are words at any address)
+    else if constexpr (sizeof(E) == 2) launch_as<E, 1, 4, BWD, false>(a, pairs, st);
 }
 
 template <bool BWD>

@@ -137,3 +137,12 @@ def test_frequencies_that_are_no_numbers(C, R, inter):
         kept = [c for c in range(C) if c not in lost]
         for got, want in zip(call(g), clean):
             assert torch.isnan(got[..., lost]).all() and torch.equal(got[..., kept], want[..., kept])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rows_of_odd_addresses_and_strides(dtype, inter):
+    # no word of two elements fits these rows, forward or backward
+    for shape in ((40, 3, 2, 128, 128), (37, 5, 1, 80, 52), (9, 2, 3, 254, 130), (300, 1, 1, 2, 2), (65, 33, 4, 34, 10)):
+        q, k, dq, dk, *rest = _case(*shape, dtype, True, fused=False)
+        _check((*(_at(x, True) for x in (q, k, dq, dk)), *rest), inter, 1e-6)
