@@ -469,7 +469,8 @@ kda_status kda_read_device_status(void* ws, int* device_status, kda_stream_t str
  * cannot complete (an mbarrier nothing arrives on).  After limit_us microseconds of GPU global
  * time (1 .. 1,000,000) the wait gives up and the kernel writes KDA_ERR_TIMEOUT into the status
  * word at the start of `ws` and returns, exactly as the library's kernels report a timed-out
- * wait; the context stays usable.  ws: >= 256 bytes of 16-byte aligned device memory (any
+ * wait; the context stays usable.  A wait of a whole warp that runs out for some of its lanes alone is
+ * made besides: where its lanes did not all get the same answer, the status is KDA_ERR_DEVICE_CHECK.  ws: >= 256 bytes of 16-byte aligned device memory (any
  * workspace), read with kda_read_device_status.  Returns KDA_ERR_INVALID_ARG for a null or
  * misaligned ws or a limit out of range; does not synchronise `stream`. */
 kda_status kda_selftest_wait_timeout(void* ws, uint32_t limit_us, kda_stream_t stream);

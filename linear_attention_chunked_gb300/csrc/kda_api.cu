@@ -728,13 +728,20 @@ namespace kda {
 // up after limit_ns of global time and the kernel reports KDA_ERR_TIMEOUT in the status word, as
 // every kernel's timed-out wait does, and returns (no trap, the context stays usable).
 __global__ void k_selftest_wait(int* status, uint64_t limit_ns) {
-    __shared__ __align__(8) uint64_t bar;
+    __shared__ __align__(8) uint64_t bar, come;
     if (threadIdx.x == 0) {
         tc::mbar_init(&bar, 1);
+        tc::mbar_init(&come, 1);
         tc::fence_mbar_init();
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&come)) : "memory");
     }
     __syncthreads();
-    if (threadIdx.x == 0 && !tc::mbar_wait(&bar, 0, limit_ns)) status[0] = KDA_ERR_TIMEOUT;
+    const bool late = threadIdx.x == 0 && !tc::mbar_wait(&bar, 0, limit_ns);
+    __syncwarp();
+    // a warp's wait that runs out for half of the lanes answers all of them alike
+    const bool part = tc::warp_wait<64>(smem_u32(threadIdx.x & 1 ? &bar : &come), 0);
+    const bool agreed = __all_sync(0xffffffffu, !part) && tc::warp_wait<64>(smem_u32(&come), 0);
+    if (late) status[0] = agreed ? KDA_ERR_TIMEOUT : KDA_ERR_DEVICE_CHECK;
 }
 }  // namespace kda
 

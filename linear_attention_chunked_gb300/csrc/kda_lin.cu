@@ -87,22 +87,9 @@ __device__ __forceinline__ void tma_store4(const CUtensorMap* map, int x, int y,
                  : "memory");
 }
 
-// Waits for the phase of the given parity; false if it has not come after WAIT_TRIES suspensions of some 7800 clocks
-// each: about a second.  The loop has no instruction but its own and reads no clock: a chunk's chain of hand-overs pays
-// for every one, and the roles' code has to share the instruction cache (with the clock read here the walk takes 8% longer).
+// A wait gives up after about a second.  (The roles' code has to share the instruction cache: with the clock read in the
+// wait's loop the walk takes 8% longer.)
 constexpr uint32_t WAIT_TRIES = 250000;
-__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-        "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " @p bra D%=;\n add.u32 n, n, 1;\n setp.lt.u32 p, n, %3;\n @p bra W%=;\n setp.ne.u32 p, 0, 0;\n"
-        "D%=: selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "n"(WAIT_TRIES)
-        : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -328,11 +315,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     };
     auto staged = [&](int c) { return !p.out_fp32 && tokens(c) == LC; };
     // Waits for the turn-th completion of barrier b.  A wait that runs out of tries ends the warp's part; every other
-    // wait runs out too, and the block reports and ends.
-    bool ok = true;
+    // wait runs out too, and the block reports and ends, when nothing of its copies and products is in flight any more.
+    bool ok = true;  // the same in a warp's lanes
+    int loaded = 0;  // tiles (warp 16)
     auto wait = [&](int b, int turn) {
-        ok = ok && bounded_wait(sbar + 8 * b, uint32_t(turn) & 1u);
-        __syncwarp();
+        ok = ok && tc::warp_wait<WAIT_TRIES>(sbar + 8 * b, uint32_t(turn) & 1u);
         tc::fence_after_sync();
         return ok;
     };
@@ -537,8 +524,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
             if (elect()) load(i);
             __syncwarp();
         }
-        if (!ok)  // every copy has landed before the block ends
-            for (int k = max(i - W_TILES, 0); k < i; ++k) tc::mbar_wait(&bar[B_FULL + k % W_TILES], (k / W_TILES) & 1, 100000000ull);
+        loaded = i;
     } else if (w == 17) {
         // ---- products ----
         const uint32_t ID = tc::idesc_bf16(128, 128, false, false), IDt = tc::idesc_bf16(128, 128, false, true);
@@ -601,7 +587,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
                 __syncwarp();
             }
         }
-        if (!ok && elect()) tc::drain_mmas(&bar[B_SPARE], 100000000ull);
     } else {
         // ---- stores ----
         for (int c = 0; c < nc; ++c) {
@@ -621,7 +606,14 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (tid == 0 && *abort_flag) *a.status = KDA_ERR_TIMEOUT;
+    if (*abort_flag) {  // whichever warp gave up
+        if (tid == 0) *a.status = KDA_ERR_TIMEOUT;
+        if (w == 16)
+            for (int k = max(loaded - W_TILES, 0); k < loaded; ++k)
+                tc::mbar_wait(&bar[B_FULL + k % W_TILES], (k / W_TILES) & 1, 100000000ull);
+        if (w == 17 && elect()) tc::drain_mmas(&bar[B_SPARE], 100000000ull);
+        __syncthreads();
+    }
     if (w == 0) tc::tmem_dealloc(tbase, 512);
 }
 
@@ -676,9 +668,9 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
     const int row = 32 * (w & 3) + lane;
     auto tile = [&](int c, int which) { return sm + ((c % S_STAGES) * 2 + which) * TILE; };
     bool ok = true;  // waits as in the walk
+    int loaded = 0;  // chunks (warp 8)
     auto wait = [&](int b, int turn) {
-        ok = ok && bounded_wait(sbar + 8 * b, uint32_t(turn) & 1u);
-        __syncwarp();
+        ok = ok && tc::warp_wait<WAIT_TRIES>(sbar + 8 * b, uint32_t(turn) & 1u);
         tc::fence_after_sync();
         return ok;
     };
@@ -719,7 +711,6 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
         }
     } else if (w == 8) {
         const CUtensorMap *mk = &tm.m[p.key], *mv = &tm.m[p.value];
-        int done = 0;
         for (int c = 0; c < nc; ++c) {
             const int s = c % S_STAGES, t = g.t0 + LC * c;
             if (c >= S_STAGES && !wait(SB_EMPTY + s, c / S_STAGES - 1)) break;
@@ -729,11 +720,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
                 tc::tma4(tile(c, 0), mk, 0, t, 0, hd / p.rk, &bar[SB_FULL + s]);
             }
             __syncwarp();
-            done = c + 1;
+            loaded = c + 1;
         }
-        if (!ok)
-            for (int c = max(done - S_STAGES, 0); c < done; ++c)
-                tc::mbar_wait(&bar[SB_FULL + c % S_STAGES], (c / S_STAGES) & 1, 100000000ull);
     } else {
         const uint32_t IDt = tc::idesc_bf16(128, 128, false, true);
         for (int c = 0; c < nc; ++c) {
@@ -751,13 +739,19 @@ __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int p
             }
             if (!ok) break;
         }
-        if (!ok && elect()) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
     }
     if (!ok) *abort_flag = 1;
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (tid == 0 && *abort_flag) *a.status = KDA_ERR_TIMEOUT;
+    if (*abort_flag) {
+        if (tid == 0) *a.status = KDA_ERR_TIMEOUT;
+        if (w == 8)
+            for (int c = max(loaded - S_STAGES, 0); c < loaded; ++c)
+                tc::mbar_wait(&bar[SB_FULL + c % S_STAGES], (c / S_STAGES) & 1, 100000000ull);
+        if (w == 9 && elect()) tc::drain_mmas(&bar[SB_SPARE], 100000000ull);
+        __syncthreads();
+    }
     if (w == 0) tc::tmem_dealloc(tbase, 512);
 }
 

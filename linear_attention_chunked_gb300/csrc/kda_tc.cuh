@@ -66,6 +66,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     }
 }
 
+// Waits, a whole warp together, for the phase of the given parity: true in every lane where it has come for every lane, false in
+// every lane where one of them saw TRIES suspensions of some 7800 clocks each go by without it.  (Lanes poll for themselves, and
+// one may give up just before the phase comes for another: without the vote the warp would part, and the next elect.sync or
+// __syncwarp would never end.)  The loop has no instruction but its own and reads no clock: a chain of hand-overs pays for
+// every one.
+template <uint32_t TRIES>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+        "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " @p bra D%=;\n add.u32 n, n, 1;\n setp.lt.u32 p, n, %3;\n @p bra W%=;\n setp.ne.u32 p, 0, 0;\n"
+        "D%=: selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "n"(TRIES)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0);
+}
+
 // ---- TMA ----
 // 2-D tile load into shared memory; completion is counted on `bar` as transaction bytes.
 // x (innermost coordinate) must be a multiple of 8 for bf16 data.
