@@ -110,7 +110,8 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int n, int tid) 
 
 // A piece (16 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into bf16 planes
 // as the left operand of a product in tensor memory: lane = channel, token pairs in the columns taddr.. of hi, mid and
-// lo, 8 each.  Three planes are cut off (8 bits each: exact), two are rounded (off by 2^-18 at most, 2.5e-6 in the 2-norm).  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
+// lo, 8 each.  Three planes are cut off (8 bits each: exact), two are rounded (the rest of the first, at most 2^-8, to 8 bits:
+// off by 2^-17 at most, 2.5e-6 in the 2-norm).  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
 // the pairs that a 16-lane store takes.
 constexpr int PIECES = LC / 16;
 constexpr uint32_t PLANES = 24;  // columns of a piece
@@ -307,11 +308,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_lin_walk(LinArgs a, const _
 
     // whether chunk c's values still reach a state that is read; whether its output leaves by TMA
     auto adds = [&](int c) { return c + 1 < nc || x1; };
-    // The state that a document ends in is an fp32 output: the values that still weigh more than 1/32 in it are split into three
-    // planes, exactly; those before them, and a state that only bf16 rows are made of, get two.
+    // The state that a document ends in is an fp32 output: the values that still weigh more than 1/64 in it are split into three
+    // planes, exactly; those before them get two, which is off by 2^-23 of what they were at their time (three everywhere: 5%
+    // of a forward), and so does a state that only bf16 rows are made of.
     auto three = [&](int c) {
         const int beyond = back ? LC * place(c) : max(g.len - LC * (c + 1), 0);  // tokens that the walk still meets
-        return x1 && (beyond == 0 || slope * float(beyond) > -3.5f);
+        return x1 && (beyond == 0 || slope * float(beyond) > -4.16f);
     };
     auto staged = [&](int c) { return !p.out_fp32 && tokens(c) == LC; };
     // Waits for the turn-th completion of barrier b.  A wait that runs out of tries ends the warp's part; every other
