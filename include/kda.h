@@ -374,7 +374,8 @@ kda_status kda_layernorm_bwd(const kda_layernorm_problem* p, const void* x, cons
  * formula says).  States h0, ht, dht, dh0 are fp32 [N, H, 128, 128] indexed [key][value]; h0 nullable
  * (zero), ht nullable.  The states and every sum are fp32; an empty document's ht is its h0 and its dh0 its dht.
  * A document's results do not depend on the rest of the pack and are bitwise reproducible.  What is not finite in a
- * document's rows reaches that document alone (earlier tokens of the same 128 among them).  Outputs overlap no input.
+ * document's rows reaches that document alone (earlier tokens of the same 128 among them).  Outputs overlap no input
+ * (one that is an input that is still read, ht = h0 for one, is KDA_ERR_INVALID_ARG).
  *
  * kda_linattn_fwd with a non-NULL saved buffer leaves there what kda_linattn_bwd needs besides the inputs
  * (saved = NULL there recomputes it).  The backward is that of L = sum(o * dO) + sum(ht * dht): dq, dk

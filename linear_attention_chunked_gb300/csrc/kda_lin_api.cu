@@ -211,6 +211,7 @@ kda_status kda_linattn_fwd(const kda_linattn_problem* p, const void* q, const vo
     if (!req(slope) || !opt(h0) || !opt(ht) || !opt(saved) || !req(ws)) return KDA_ERR_INVALID_ARG;
     const Regions r = regions(p);
     if (ws_bytes < r.fwd) return KDA_ERR_WORKSPACE;
+    if (ht && ht == h0) return KDA_ERR_INVALID_ARG;  // blocks of a document's ends read the one and write the other
     if (kda_status s = setup_lin()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LinArgs a = make_args(p, r, false, slope, ws);
@@ -242,6 +243,10 @@ kda_status kda_linattn_bwd(const kda_linattn_problem* p, const void* q, const vo
     if (!req(slope) || !opt(h0) || !opt(dht) || !opt(saved) || !opt(dh0) || !req(ws)) return KDA_ERR_INVALID_ARG;
     const Regions r = regions(p);
     if (ws_bytes < (saved ? r.bwd_saved : r.bwd_replay)) return KDA_ERR_WORKSPACE;
+    // three walks read the inputs side by side while they write the outputs
+    if (dh0 && (dh0 == h0 || dh0 == dht)) return KDA_ERR_INVALID_ARG;
+    for (const void* out : {dq, dk, dv})
+        if (p->T > 0 && (out == q || out == k || out == v || out == dO)) return KDA_ERR_INVALID_ARG;
     if (kda_status s = setup_lin()) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     LinArgs a = make_args(p, r, true, slope, ws);

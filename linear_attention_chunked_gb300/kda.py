@@ -829,6 +829,8 @@ def kda_linattn_fwd(q, k, v, slope, cu_seqlens, *, h0=None, scale=1.0, save=True
         ht = torch.empty(state, dtype=torch.float32, device=dev)
     else:
         _check_tensor(fn, "ht", ht, state, torch.float32, dev)
+        if h0 is not None and ht.data_ptr() == h0.data_ptr():
+            raise ValueError(f"{fn}: ht is h0, outputs overlap no input")
     _check_tensor(fn, "h0", h0, state, torch.float32, dev)
     _call(fn, dev, ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), slope.data_ptr(), _at(h0), o.data_ptr(),
           ht.data_ptr(), _at(saved), ws.data_ptr(), ws_n)
