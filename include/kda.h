@@ -373,6 +373,8 @@ kda_status kda_layernorm_bwd(const kda_layernorm_problem* p, const void* x, cons
  * slope fp32 [H] is a constant of the model, usually <= 0 (-inf: no memory; above 0 the state grows as the
  * formula says).  States h0, ht, dht, dh0 are fp32 [N, H, 128, 128] indexed [key][value]; h0 nullable
  * (zero), ht nullable.  The states and every sum are fp32; an empty document's ht is its h0 and its dh0 its dht.
+ * What a token adds to a state enters its product exactly where it weighs more than 1/64 in ht or dh0; below that, and
+ * on its way into bf16 rows, as two bf16 numbers (2^-17).
  * A document's results do not depend on the rest of the pack and are bitwise reproducible.  What is not finite in a
  * document's rows reaches that document alone (earlier tokens of the same 128 among them).  Outputs overlap no input
  * (one that is an input that is still read, ht = h0 for one, is KDA_ERR_INVALID_ARG).
@@ -423,8 +425,10 @@ kda_status kda_linattn_step(const kda_linattn_problem* p, const void* q, const v
  * ld_qo, ld_ko (elements; 0 = dense; element alignment); an output may be its input, row for row, and overlaps no
  * input otherwise.  pos int32 [T] are any
  * positions; freq fp64 [R / 2] is in radians per token (kda_rope_frequencies).  An angle is reduced in
- * 64-bit integers, so far positions keep their accuracy.  Arithmetic is fp32, rounded once.  Hq or Hk may
- * be 0 (that tensor is not read).
+ * 64-bit integers, so far positions keep their accuracy (what the frequency's own rounding leaves: 10^-7 radians at
+ * 2^31 for one radian a token); a frequency that is no number gives its pair none.  Arithmetic is fp32, rounded once; values below
+ * 2^-126 count as zero, eps too, and a row's sum of squares has to fit.  eps = 0 leaves a row of zeros undefined.
+ * Without a norm a channel that does not turn is its input, whatever it holds.  Hq or Hk may be 0 (that tensor is not read).
  * The backward takes the forward's inputs q, k (read when norm = 1, nullable otherwise) and the gradients of
  * its outputs, dense or with strides ld_qo, ld_ko, and gives dq, dk (dense; may be dq_out, dk_out when those
  * are dense) and, for norm = 1, dwq, dwk fp32 [D] (nullable), summed in a fixed order in the workspace. */
@@ -471,8 +475,8 @@ kda_status kda_read_device_status(void* ws, int* device_status, kda_stream_t str
  * time (1 .. 1,000,000) the wait gives up and the kernel writes KDA_ERR_TIMEOUT into the status
  * word at the start of `ws` and returns, exactly as the library's kernels report a timed-out
  * wait; the context stays usable.  A wait of a whole warp that runs out for some of its lanes alone is
- * made besides: where its lanes did not all get the same answer, the status is KDA_ERR_DEVICE_CHECK.  ws: >= 256 bytes of 16-byte aligned device memory (any
- * workspace), read with kda_read_device_status.  Returns KDA_ERR_INVALID_ARG for a null or
+ * made besides: where its lanes did not all get the same answer, the status is KDA_ERR_DEVICE_CHECK.
+ * ws: >= 256 bytes of 16-byte aligned device memory (any workspace), read with kda_read_device_status.  Returns KDA_ERR_INVALID_ARG for a null or
  * misaligned ws or a limit out of range; does not synchronise `stream`. */
 kda_status kda_selftest_wait_timeout(void* ws, uint32_t limit_us, kda_stream_t stream);
 

@@ -11,14 +11,18 @@
 //
 // What bounds it: a token and head is 1 KB of rows, 2.9 us of a multiprocessor's share of HBM for a chunk, and 40 to 48
 // products of 128 x 128 x 16, some 3550 to 4200 clocks.  One block per multiprocessor holds a state and works on
-// successive chunks: 16384 tokens (9000 / 5000 / 2384) x 64 heads take 197 us, 5.5 TB/s (81% of the measured 6.77), the
-// last third of it on the 64 blocks of the longest document; one document of 16384 x 64 (64 blocks) 305 us, 2.4 us a
-// chunk, bound by the chain of its own steps.  Of those 2.4 us the products alone take 1.9 and the hand-overs alone 1.3.
+// successive chunks: 16384 tokens (9000 / 5000 / 2384) x 64 heads take 199 us, 5.4 TB/s (80% of the measured 6.77), the
+// last third of it on the 64 blocks of the longest document; one document of 16384 x 64 (64 blocks) 305 to 340 us from card to
+// card, 2.4 us a chunk and more, bound by the chain of its own steps.  Of those 2.4 us the products alone take 1.9 and the
+// hand-overs alone 1.3.
 //
 // The state stays in tensor memory as X^T (lane = value channel); the scaled values are the state product's left operand
 // in tensor memory, split into bf16 planes, so that with three of them (8 + 8 + 8 bits: exact) the state's products are fp32
 // products.  The scores and the state are rounded to bf16 as operands of products whose sums are rounded to bf16 rows:
-// each adds as much as the output's own rounding.  Query, Key and Value come by TMA and are read where they land:
+// each adds as much as the output's own rounding: 0.0023 of a row's length from 64 bits in all, where one rounding is 0.0017.
+// (The delta rule's triangular inverse multiplies such errors, so KDA's products carry hi and lo operands.  Here nothing
+// does; second planes of scores and state would be 16 products more beside a chunk's 40 to 48, and shared memory holds one
+// plane of the state.)  Query, Key and Value come by TMA and are read where they land:
 //     P      A = Query [tokens][keys],    B = Key [tokens][keys]
 //     QX     A = Query,                   B = X^T in shared memory, bf16 [values][keys]
 //     P'V    A = P' (tensor memory),      B = Value [tokens][values] read across
@@ -111,8 +115,8 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int n, int tid) 
 // A piece (16 tokens) of a chunk's values, times the tokens' factors f (shared memory) and `all`, split into bf16 planes
 // as the left operand of a product in tensor memory: lane = channel, token pairs in the columns taddr.. of hi, mid and
 // lo, 8 each.  Three planes are cut off (8 bits each: exact), two are rounded (the rest of the first, at most 2^-8, to 8 bits:
-// off by 2^-17 at most, 2.5e-6 in the 2-norm).  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded, which gives a lane
-// the pairs that a 16-lane store takes.
+// off by 2^-17 at most, 2.5e-6 in the 2-norm).  A warp does its 32 channels; 8 x 8 blocks are transposed as they are loaded,
+// which gives a lane the pairs that a 16-lane store takes.
 constexpr int PIECES = LC / 16;
 constexpr uint32_t PLANES = 24;  // columns of a piece
 template <int N>
@@ -181,7 +185,8 @@ __device__ __forceinline__ bool lin_segment(const LinArgs& a, int i, Seg& s) {
         s.first = e.z >> 16 & 1, s.last = e.z >> 17 & 1;
         return true;
     }
-    // a document for every i: the longest first, by a warp's lanes, where they have a lane each
+    // a document for every i: the longest first, by a warp's lanes, where they have a lane each.  (More of them are taken in the
+    // pack's order: a rank is a shuffle a document in every block, and no form that keeps it once was built.)
     if (a.N > 1 && a.N <= 32) {
         const int lane = threadIdx.x & 31;
         const int own = lane < a.N ? a.cu[lane + 1] - a.cu[lane] : INT_MIN;
@@ -634,7 +639,7 @@ enum StateBar {
 
 // No decay of the state between chunks: a token's factor reaches to the segment's end, the products add up.
 // Bound by HBM on paper (512 B a token and head; 24 products a chunk, half its time); 16384 tokens x 16 heads: 35 us,
-// 3.4 TB/s: one wave of 112 blocks, a sixth of whose time is their start and the store of the state.
+// 3.4 TB/s: one wave of 112 blocks that work (144 are launched), a sixth of whose time is their start and the store of the state.
 __global__ void __launch_bounds__(STATE_THREADS, 1) k_lin_state(LinArgs a, int ps, const __grid_constant__ LinMaps tm) {
     extern __shared__ unsigned char smraw[];
     unsigned char* sm = tc::align1024(smraw);

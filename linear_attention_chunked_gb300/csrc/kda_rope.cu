@@ -14,9 +14,11 @@
 // token and the weights in registers and walks the token's heads.  The rows come through a ring in shared memory that
 // cp.async fills ahead, over the ends of tiles too; a thread copies exactly the bytes that it reads, so the ring needs no
 // barrier.
-// 16384 tokens x 2 x 64 heads of 128 channels, bf16: forward 180 us (5.9 TB/s, 88% of the measured HBM peak), backward 280 us
-// (5.7 TB/s, 85%): what is left is instructions, 16 warps a multiprocessor at 120 registers.  Without a norm 180.  Rows
-// that allow 4-byte packs only 1.25 times that, single pairs picked out of words 1.5 (neighbours) to 2.7 times.
+// 16384 tokens x 2 x 64 heads of 128 channels, bf16: forward and backward 466 us, 5.7 TB/s, 85% of the measured HBM peak:
+// what is left is instructions, 16 warps a multiprocessor at 120 registers.  In a loop on the same tensors (16384 x 2 x 64 heads,
+// forward / backward in shares of that peak): 128 channels 81 / 81%, half of them turned 82 / 83%, fp32 84 / 85%, 96 channels 85 / 61%
+// (6 of a group's 8 lanes), 80 70 / 51%, 144 65 / 48%, 52 of 80 (8-byte packs) 51 / 33%, single pairs picked out of words
+// 126 41 / 28% (neighbours 54 / 40%), 50 34 / 21% (44 / 31%), 130 25 / 18% (33 / 26%: 65 of 128 places).
 //
 // Angles.  A position times a frequency in fp32 is off by a thousandth of a turn at position 10^4 already.
 // Here a frequency is a 64-bit fraction of a turn per token, F = freq / (2 pi) 2^64 mod 2^64, so pos F mod
